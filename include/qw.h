@@ -405,6 +405,105 @@ int qw_sample_last(qw_handle* h, float temperature, int32_t top_k, float top_p, 
 int qw_gemm_bf16(const uint16_t* a_hi, const uint16_t* a_lo, const uint16_t* b, int32_t M,
                  int32_t N, int32_t K, float* c, int32_t bn, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * A paged cache for a batch of sequences: the step around the projections when more
+ * than one sequence is served. Keys and values of one layer lie in a pool of pages,
+ * and every sequence owns a list of pages; qw_paged_append puts the new tokens of the
+ * batch into them and qw_paged_attention reads them back for those tokens' queries.
+ * Lengths and tables live on the device, so a captured CUDA graph replays with new
+ * ones. All buffers are the caller's; calls queue on `stream` and return at once.
+ * ------------------------------------------------------------------------- */
+
+/* Element type of the activations (raw projections, rotated queries, outputs). */
+enum { QW_ACT_F32 = 0, QW_ACT_BF16 = 1 };
+
+/* Bits that the kernels add (atomic OR) to qw_paged_kv.status. BAD_PAGE: a page id in
+ * use lies outside [0, n_pages); append drops that row, attention reads page 0 instead
+ * (that sequence's output is then meaningless). BAD_LENGTH: a kv_len outside
+ * [0, max_pages * page_size], or smaller than the sequence's new tokens (append drops
+ * rows that have no place, attention clamps). TIMEOUT: a device-side wait of attention
+ * gave up; its outputs are invalid. */
+enum { QW_PAGED_TIMEOUT = 1, QW_PAGED_BAD_PAGE = 2, QW_PAGED_BAD_LENGTH = 4 };
+
+/* One layer's pages and the batch that uses them. Set struct_size =
+ * sizeof(qw_paged_kv). All pointers are DEVICE addresses on the current device.
+ *
+ * The tokens of a call are rows 0 .. n_tokens-1; those of sequence b are rows
+ * q_start[b] .. q_start[b+1]-1 (a sequence may have none), and they are the last
+ * q_start[b+1] - q_start[b] of its kv_len[b] keys. Key r of sequence b is row
+ * r % page_size of page page_table[b][r / page_size]; entries behind the last key's
+ * page are not read. Rows of the call outside [q_start[0], q_start[n_seqs]) belong to
+ * no sequence: their outputs are left as they were.
+ *
+ * A shared prefix (prefix_len > 0) is prefix_len keys in the pages prefix_pages that
+ * every sequence sees before its own keys; kv_len and page_table count a sequence's own
+ * keys only. Slots of a page behind a sequence's last key may hold anything (NaN too).
+ * Two sequences may share pages that the call does not append to. */
+typedef struct qw_paged_kv {
+  uint32_t struct_size;
+  uint32_t kv_format;          /* QW_KV_F32 or QW_KV_BF16 */
+  int32_t n_pages;             /* pages of the pool; n_pages * n_kv_heads * page_size < 2^31 */
+  int32_t page_size;           /* keys of a page: 16, 32, 64, 128 or 256 */
+  int32_t n_kv_heads;
+  int32_t head_dim;            /* 64 or 128 */
+  int32_t n_seqs;
+  int32_t max_pages;           /* columns of page_table */
+  int32_t prefix_len;          /* keys of the shared prefix, 0 for none */
+  uint32_t reserved0;
+  void* k_pages;               /* [n_pages, n_kv_heads, page_size, head_dim], 16-byte aligned */
+  void* v_pages;               /* the same shape */
+  const int32_t* page_table;   /* [n_seqs, max_pages] */
+  const int32_t* kv_len;       /* [n_seqs]: keys of each sequence, the call's tokens included */
+  const int32_t* q_start;      /* [n_seqs + 1], not decreasing */
+  const int32_t* prefix_pages; /* [ceil(prefix_len / page_size)], or NULL */
+  int32_t* status;             /* [1], QW_PAGED_* bits, or NULL */
+} qw_paged_kv;
+size_t qw_sizeof_paged_kv(void);
+
+/* Per-head RMSNorm (with q_norm and k_norm), rotation, and append: of every token's raw
+ * projections (q heads, k heads, v heads, biases added) the rotated queries go to q_out
+ * and the keys (normed, rotated) and values (as they are) into the token's slot, each
+ * rounded once to the type it is stored in.
+ *   qkv:       act_format [n_tokens, ld] DEVICE, ld >= (n_q_heads + 2 n_kv_heads) * head_dim
+ *              elements and a multiple of 16 bytes; 16-byte aligned
+ *   q_norm, k_norm: bf16 [head_dim] DEVICE, both or neither (NULL)
+ *   rotation (rotate-half): pair (j, j + head_dim/2) turns by position * rope_theta^(-2j/head_dim);
+ *              the angle keeps f32 accuracy for positions up to 2^24 in magnitude
+ *   positions: without sections, int32 [n_tokens] DEVICE, or NULL for prefix_len + cache row;
+ *              with sections, int32 [n_tokens, 3] DEVICE (time, height, width)
+ *   sections:  HOST int32 [3] or NULL: how many of the head_dim/2 pairs turn by each axis, the
+ *              first sections[0] by axis 0, the next sections[1] by axis 1, the rest by axis 2
+ *   q_out:     act_format [n_tokens, n_q_heads * head_dim] DEVICE, 16-byte aligned; must not
+ *              overlap qkv
+ * n_tokens = 0 does nothing. Two tokens must not name the same slot. */
+int qw_paged_append(const qw_paged_kv* c, const void* qkv, uint32_t act_format, int64_t ld,
+                    int32_t n_tokens, int32_t n_q_heads, const uint16_t* q_norm,
+                    const uint16_t* k_norm, float eps, float rope_theta, const int32_t* positions,
+                    const int32_t* sections, void* q_out, void* stream);
+
+/* Causal attention of the call's tokens over their pages (append them first): token i of
+ * sequence b sees the whole prefix and its own keys 0 .. kv_len[b] - (new tokens of b) + i.
+ * Scores are scaled by 1/sqrt(head_dim); query head h reads KV head h / (n_q_heads /
+ * n_kv_heads), at most 8 query heads per KV head. A token that sees no key gets zeros. The
+ * prefix's keys are read once for the whole batch and joined with each sequence's own by
+ * their softmax statistics. f32 activations give results of f32 accuracy from either cache
+ * format; bf16 activations with a bf16 cache run one bf16 product with f32 sums. Results do
+ * not depend on the order in which the CTAs finish. Keys and values that a call's tokens may
+ * see are finite.
+ *   q:         act_format [n_tokens, ldq] DEVICE, ldq >= n_q_heads * head_dim elements and a
+ *              multiple of 16 bytes; 16-byte aligned (q_out of qw_paged_append, ldq = n_q_heads * head_dim)
+ *   max_new:   the most new tokens of one sequence, which chooses the kernel; a wrong value
+ *              costs speed only
+ *   out:       act_format [n_tokens, n_q_heads * head_dim] DEVICE, 16-byte aligned
+ *   workspace: DEVICE scratch of qw_paged_attention_workspace_bytes(n_tokens, n_q_heads,
+ *              head_dim, prefix_len) bytes, 16-byte aligned, zero-filled before its first use and
+ *              left ready for the next call; calls that overlap on the GPU need one each */
+size_t qw_paged_attention_workspace_bytes(int32_t n_tokens, int32_t n_q_heads, int32_t head_dim,
+                                          int32_t prefix_len);
+int qw_paged_attention(const qw_paged_kv* c, const void* q, uint32_t act_format, int64_t ldq,
+                       int32_t n_tokens, int32_t n_q_heads, int32_t max_new, void* out,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -30,6 +30,11 @@ QW_WEIGHTS_INT4_G128 = 1
 QW_WEIGHTS_Q8_0 = 2
 QW_KV_F32 = 0
 QW_KV_BF16 = 1
+QW_ACT_F32 = 0
+QW_ACT_BF16 = 1
+QW_PAGED_TIMEOUT = 1
+QW_PAGED_BAD_PAGE = 2
+QW_PAGED_BAD_LENGTH = 4
 QW_CAPTURE_EMBEDDING = 0
 QW_CAPTURE_BLOCK0 = 1
 QW_CAPTURE_FINAL_NORM = 2
@@ -71,6 +76,15 @@ class qw_weights(C.Structure):
 class qw_lora(C.Structure):
     _fields_ = [("struct_size", C.c_uint32), ("rank", C.c_int32), ("alpha", C.c_float),
                 ("reserved0", C.c_uint32), ("q_a", PP), ("q_b", PP), ("v_a", PP), ("v_b", PP)]
+
+
+class qw_paged_kv(C.Structure):
+    _fields_ = [("struct_size", C.c_uint32), ("kv_format", C.c_uint32), ("n_pages", C.c_int32),
+                ("page_size", C.c_int32), ("n_kv_heads", C.c_int32), ("head_dim", C.c_int32),
+                ("n_seqs", C.c_int32), ("max_pages", C.c_int32), ("prefix_len", C.c_int32),
+                ("reserved0", C.c_uint32), ("k_pages", C.c_void_p), ("v_pages", C.c_void_p),
+                ("page_table", C.c_void_p), ("kv_len", C.c_void_p), ("q_start", C.c_void_p),
+                ("prefix_pages", C.c_void_p), ("status", C.c_void_p)]
 
 
 _SIG = {
@@ -129,6 +143,15 @@ _SIG = {
     "qw_lm_head_argmax": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int32, C.c_int32,
                                     C.c_float, C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t,
                                     C.c_void_p]),
+    "qw_sizeof_paged_kv": (C.c_size_t, []),
+    "qw_paged_append": (C.c_int, [C.POINTER(qw_paged_kv), C.c_void_p, C.c_uint32, C.c_int64,
+                                  C.c_int32, C.c_int32, C.c_void_p, C.c_void_p, C.c_float,
+                                  C.c_float, C.c_void_p, C.POINTER(C.c_int32), C.c_void_p,
+                                  C.c_void_p]),
+    "qw_paged_attention_workspace_bytes": (C.c_size_t, [C.c_int32] * 4),
+    "qw_paged_attention": (C.c_int, [C.POINTER(qw_paged_kv), C.c_void_p, C.c_uint32, C.c_int64,
+                                     C.c_int32, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p,
+                                     C.c_size_t, C.c_void_p]),
 }
 
 _lib: Optional[C.CDLL] = None
@@ -153,7 +176,7 @@ def lib() -> C.CDLL:
             f.restype = res
             f.argtypes = args
         for name, st in (("qw_sizeof_config", qw_config), ("qw_sizeof_weights", qw_weights),
-                         ("qw_sizeof_lora", qw_lora)):
+                         ("qw_sizeof_lora", qw_lora), ("qw_sizeof_paged_kv", qw_paged_kv)):
             if getattr(L, name)() != C.sizeof(st):
                 raise RuntimeError(f"ctypes {st.__name__} ({C.sizeof(st)} B) does not match "
                                    f"the library ({getattr(L, name)()} B)")

@@ -1,0 +1,162 @@
+"""A paged KV cache for a batch of sequences, over qw_paged_append and qw_paged_attention.
+
+``PagedKV`` holds one layer's pages and the batch's lengths and tables as torch CUDA tensors and
+queues the two calls on torch's current stream. PyTorch is used for device memory and streams
+only; every computation is a libqw.so kernel.
+"""
+from __future__ import annotations
+
+import ctypes as C
+
+from . import _binding as B
+
+_FORMATS = {"torch.float32": 0, "torch.bfloat16": 1}  # QW_KV_* and QW_ACT_* alike
+
+
+def _format(t, what: str) -> int:
+    f = _FORMATS.get(str(t.dtype))
+    if f is None:
+        raise ValueError(f"{what}: float32 or bfloat16 wanted, got {t.dtype}")
+    return f
+
+
+class PagedKV:
+    """One layer's pages and the batch that uses them (fields as in qw_paged_kv).
+
+    k_pages, v_pages: [n_pages, n_kv_heads, page_size, head_dim], float32 or bfloat16;
+    page_table: int32 [n_seqs, max_pages]; kv_len: int32 [n_seqs], keys of each sequence with the
+    call's new tokens; q_start: int32 [n_seqs + 1], first token row of each sequence;
+    prefix_pages: int32 pages of ``prefix_len`` keys that all sequences share, or None.
+    All are contiguous tensors on one CUDA device. They are borrowed, not copied: write new lengths
+    or page ids into them between calls (or into a captured graph's inputs before a replay).
+    """
+
+    def __init__(self, k_pages, v_pages, page_table, kv_len, q_start, prefix_pages=None,
+                 prefix_len: int = 0):
+        import torch
+        if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
+            raise ValueError("k_pages and v_pages: two [n_pages, n_kv_heads, page_size, head_dim] "
+                             "tensors of one type")
+        n_seqs = page_table.shape[0] if page_table.dim() == 2 else 0
+        if n_seqs < 1 or kv_len.shape != (n_seqs,) or q_start.shape != (n_seqs + 1,):
+            raise ValueError("page_table [n_seqs, max_pages], kv_len [n_seqs] and q_start [n_seqs + 1] "
+                             "do not agree")
+        ints = [page_table, kv_len, q_start] + ([prefix_pages] if prefix_pages is not None else [])
+        if any(t.dtype != torch.int32 for t in ints):
+            raise ValueError("page_table, kv_len, q_start and prefix_pages are int32")
+        self.device = k_pages.device
+        for t in [k_pages, v_pages] + ints:
+            if not t.is_cuda or t.device != self.device or not t.is_contiguous():
+                raise ValueError("every tensor of the cache is contiguous and on one CUDA device")
+        page = k_pages.shape[2]
+        if prefix_len < 0 or (prefix_len > 0 and (prefix_pages is None or
+                                                  prefix_pages.numel() * page < prefix_len)):
+            raise ValueError("prefix_pages do not hold prefix_len keys")
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._keep = (k_pages, v_pages, page_table, kv_len, q_start, prefix_pages)
+        self._ws = None
+        self._lib = B.lib()
+        self.head_dim = k_pages.shape[3]
+        self.n_kv_heads = k_pages.shape[1]
+        self.c = B.qw_paged_kv(
+            struct_size=C.sizeof(B.qw_paged_kv), kv_format=_format(k_pages, "pages"),
+            n_pages=k_pages.shape[0], page_size=page, n_kv_heads=k_pages.shape[1],
+            head_dim=k_pages.shape[3], n_seqs=n_seqs, max_pages=page_table.shape[1],
+            prefix_len=prefix_len, k_pages=k_pages.data_ptr(), v_pages=v_pages.data_ptr(),
+            page_table=page_table.data_ptr(), kv_len=kv_len.data_ptr(),
+            q_start=q_start.data_ptr(), status=self.status.data_ptr(),
+            prefix_pages=prefix_pages.data_ptr() if prefix_len > 0 else None)
+        self._cref = C.byref(self.c)
+
+    def _rows(self, t, what: str, width: int, rows=None):
+        """Checks an activation matrix of rows with unit inner stride; (format, row stride)."""
+        f = _format(t, what)
+        if t.device != self.device:
+            raise ValueError(f"{what} is not on the cache's device")
+        inner = t.stride()
+        if t.dim() == 3:  # [rows, heads, head_dim], heads back to back
+            ok = t.shape[1] * t.shape[2] == width and inner[2] == 1 and \
+                (inner[1] == t.shape[2] or t.shape[1] == 1)
+        else:
+            ok = t.dim() == 2 and t.shape[1] == width and inner[1] == 1
+        if not ok or (rows is not None and t.shape[0] != rows):
+            raise ValueError(f"{what}: rows of {width} adjacent elements wanted, got {tuple(t.shape)} "
+                             f"with strides {inner}")
+        return f, (inner[0] if t.shape[0] > 1 else width)
+
+    def _out(self, out, like, n_q_heads: int, fmt: int):
+        import torch
+        if out is None:
+            return torch.zeros(like.shape[0], n_q_heads, self.head_dim, dtype=like.dtype,
+                               device=self.device)
+        width = n_q_heads * self.head_dim
+        f, ld = self._rows(out, "out", width, like.shape[0])
+        if f != fmt or ld != width:
+            raise ValueError("out: contiguous rows of the input's type wanted")
+        return out
+
+    def _stream(self):
+        import torch
+        if torch.cuda.current_device() != self.device.index:
+            raise ValueError("the cache's device is not the current one")
+        return torch.cuda.current_stream().cuda_stream
+
+    def append(self, qkv, n_q_heads: int, q_norm=None, k_norm=None, eps: float = 1e-6,
+               rope_theta: float = 1e6, positions=None, sections=None, out=None):
+        """Norm, rotate and append the tokens' raw projections; returns the rotated queries.
+
+        qkv: [n_tokens, (n_q_heads + 2 n_kv_heads) * head_dim] (rows may be strided); q_norm, k_norm:
+        bfloat16 (or int16 bits) [head_dim]; positions: int32 [n_tokens], or [n_tokens, 3] with
+        sections = (pairs of axis 0, 1, 2), or None for each token's place in the cache.
+        """
+        n = qkv.shape[0]
+        fmt, ld = self._rows(qkv, "qkv", (n_q_heads + 2 * self.n_kv_heads) * self.head_dim)
+        out = self._out(out, qkv, n_q_heads, fmt)
+        for t in (q_norm, k_norm):
+            if t is not None and (t.element_size() != 2 or t.shape != (self.head_dim,) or
+                                  not t.is_contiguous() or t.device != self.device):
+                raise ValueError("q_norm and k_norm: bfloat16 [head_dim] on the cache's device")
+        if positions is not None:
+            want = (n, 3) if sections is not None else (n,)
+            if str(positions.dtype) != "torch.int32" or positions.shape != want or \
+                    not positions.is_contiguous() or positions.device != self.device:
+                raise ValueError(f"positions: contiguous int32 {want} wanted")
+        sec = (C.c_int32 * 3)(*sections) if sections is not None else None
+        rc = self._lib.qw_paged_append(
+            self._cref, qkv.data_ptr(), fmt, ld, n, n_q_heads,
+            q_norm.data_ptr() if q_norm is not None else None,
+            k_norm.data_ptr() if k_norm is not None else None, eps, rope_theta,
+            positions.data_ptr() if positions is not None else None, sec, out.data_ptr(),
+            self._stream())
+        if rc:
+            B.check("qw_paged_append", rc)
+        return out
+
+    def attend(self, q, max_new: int = 1, out=None):
+        """Attention of the tokens' rotated queries [n_tokens, n_q_heads, head_dim] over their
+        sequences' keys (and the shared prefix). max_new: the most new tokens of one sequence.
+        The workspace is the cache's own: calls of one PagedKV must not overlap on the GPU."""
+        import torch
+        n = q.shape[0]
+        width = q.shape[1] * q.shape[2] if q.dim() == 3 else q.shape[1]
+        heads = width // self.head_dim
+        fmt, ld = self._rows(q, "q", heads * self.head_dim)
+        out = self._out(out, q, heads, fmt)
+        need = self._lib.qw_paged_attention_workspace_bytes(n, heads, self.head_dim,
+                                                            self.c.prefix_len)
+        if self._ws is None or self._ws.numel() < need:
+            self._ws = torch.zeros(max(need, 1), dtype=torch.uint8, device=self.device)
+        rc = self._lib.qw_paged_attention(self._cref, q.data_ptr(), fmt, ld, n, heads, max_new,
+                                          out.data_ptr(), self._ws.data_ptr(), self._ws.numel(),
+                                          self._stream())
+        if rc:
+            B.check("qw_paged_attention", rc)
+        return out
+
+    def check(self) -> None:
+        """Raises if a call so far met a bad page id or length or gave up a wait (synchronises)."""
+        bits = int(self.status.item())
+        if bits:
+            names = [n for n in ("TIMEOUT", "BAD_PAGE", "BAD_LENGTH")
+                     if bits & getattr(B, "QW_PAGED_" + n)]
+            raise RuntimeError("paged cache: " + ", ".join(names))

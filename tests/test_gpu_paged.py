@@ -1,0 +1,342 @@
+"""Paged append and attention against their 64-bit forms, at the lengths, layouts and masks where
+they can go wrong; captured graphs, other streams, reported errors and untouched rows."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from paged_ref import DT, HALF, Batch
+
+pytestmark = pytest.mark.gpu
+
+TYPES = [("f32", "f32"), ("f32", "bf16"), ("bf16", "bf16"), ("bf16", "f32")]
+HEADS = [(16, 8, 128), (16, 2, 128), (4, 2, 64), (5, 1, 128), (14, 2, 64), (3, 3, 64), (12, 2, 128)]
+# (new tokens, keys before): lengths around tile and page borders, empty ones among them
+STEP = [(1, 0), (1, 14), (1, 15), (1, 16), (1, 62), (1, 63), (1, 64), (0, 0), (0, 40), (1, 127), (1, 700)]
+CHUNKS = [(3, 0), (1, 33), (0, 5), (17, 60), (40, 0), (2, 255), (9, 119)]
+
+
+def attend_close(b, got, ref=None):
+    want, tol = ref or b.attend()
+    got = got[:b.tokens].double().cpu()
+    assert torch.isfinite(got).all()
+    assert ((got - want).abs() <= tol).all(), float(((got - want).abs() / tol).max())
+    # independent roundings add up as a root: far below the bound above
+    rel = float((got - want).norm() / want.norm()) if float(want.norm()) else 0.0
+    assert rel <= (4e-6 if b.act == "f32" else 1e-2), rel
+
+
+@pytest.mark.parametrize("act,kv", TYPES)
+@pytest.mark.parametrize("nq,nkv,hd", HEADS)
+def test_attend_steps(act, kv, nq, nkv, hd):
+    b = Batch(STEP, nq, nkv, hd, 16, act, kv, seed=1)
+    c = b.cache()
+    attend_close(b, c.attend(b.q.cuda()))
+    c.check()
+
+
+@pytest.mark.parametrize("act,kv", TYPES)
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+def test_attend_pages(act, kv, page):
+    b = Batch([(1, 0), (1, 100), (1, 255), (1, 256), (1, 511)], 8, 2, 128, page, act, kv, seed=2)
+    c = b.cache()
+    attend_close(b, c.attend(b.q.cuda()))
+    c.check()
+
+
+@pytest.mark.parametrize("act,kv", TYPES)
+@pytest.mark.parametrize("nq,nkv,hd", [(4, 2, 64), (16, 2, 128), (5, 1, 128), (7, 1, 64)])
+def test_attend_chunks(act, kv, nq, nkv, hd):
+    b = Batch(CHUNKS, nq, nkv, hd, 16, act, kv, seed=3)
+    c = b.cache()
+    ref = b.attend()
+    attend_close(b, c.attend(b.q.cuda(), max_new=40), ref)
+    attend_close(b, c.attend(b.q.cuda(), max_new=1), ref)   # a wrong hint costs speed only
+    c.check()
+
+
+@pytest.mark.parametrize("act,kv", TYPES)
+@pytest.mark.parametrize("prefix", [1, 16, 63, 64, 65, 300])
+def test_attend_prefix(act, kv, prefix):
+    # sequences without own keys see the prefix alone
+    b = Batch([(1, 0), (1, 30), (0, 3), (1, 64), (2, 10)] + [(1, 3)] * 9, 8, 2, 64, 16, act, kv,
+              prefix=prefix, pad=2, seed=prefix)
+    c = b.cache()
+    attend_close(b, c.attend(b.q.cuda(), max_new=2))
+    c.check()
+
+
+@pytest.mark.parametrize("act,kv", TYPES)
+@pytest.mark.parametrize("nq,nkv,hd", [(16, 2, 128), (4, 2, 64)])
+def test_attend_prefix_and_chunks(act, kv, nq, nkv, hd):
+    b = Batch([(30, 0), (1, 70), (45, 20)], nq, nkv, hd, 32, act, kv, prefix=130, seed=5)
+    c = b.cache()
+    attend_close(b, c.attend(b.q.cuda(), max_new=45))
+    c.check()
+
+
+def test_rows_without_a_key_are_zero():
+    # kv_len 0 with one token: nothing to see; and with a prefix the prefix alone
+    for act, kv in TYPES:
+        for prefix in (0, 20):
+            b = Batch([(1, 5), (1, 0)], 4, 2, 64, 16, act, kv, prefix=prefix, seed=7)
+            b.len[1] = 0
+            c = b.cache()
+            got = c.attend(b.q.cuda())[1].double().cpu()
+            if prefix == 0:
+                assert (got == 0).all()
+            else:
+                k, v = b.keys(b.k, 1), b.keys(b.v, 1)
+                for h in range(4):
+                    p = torch.softmax(k[h // 2] @ b.q[1, h].double() / 8.0, 0)
+                    want = p @ v[h // 2]
+                    # 20 keys: a bf16 P and output round by 2^-8 of at most max |v| each
+                    tol = 1e-5 if "f32" in (act, kv) and act == "f32" else 2 * HALF["bf16"] * float(v.abs().max())
+                    assert (got[h] - want).abs().max() <= tol
+
+
+@pytest.mark.parametrize("act,kv", TYPES)
+def test_large_scores_and_ties(act, kv):
+    # one key far above the rest, equal keys, and large values: the softmax's reference moves
+    b = Batch([(1, 300), (1, 90)], 4, 2, 64, 16, act, kv, seed=9)
+    at, slot = b.table[0, 250 // 16], 250 % 16
+    b.k[at, :, slot] = (b.q[0, 0].double() * 8).to(DT[kv])
+    b.k[b.table[1, 0], :, :8] = 0.0
+    b.v[b.table[1, 1]] *= 1000
+    c = b.cache()
+    attend_close(b, c.attend(b.q.cuda()))
+
+
+@pytest.mark.parametrize("act,kv", [("f32", "f32"), ("f32", "bf16"), ("bf16", "bf16")])
+def test_long_split_sequences(act, kv):
+    # one long and many short sequences: items split over many CTAs, and the same bits again
+    b = Batch([(1, 3000)] + [(1, i) for i in range(40)], 8, 1, 64, 64, act, kv, seed=11)
+    c = b.cache()
+    q = b.q.cuda()
+    got = c.attend(q)
+    attend_close(b, got)
+    for _ in range(3):
+        assert torch.equal(c.attend(q), got)
+
+
+def test_padding_rows_are_left_and_strides():
+    for act, kv in TYPES:
+        b = Batch([(2, 9), (1, 40)], 4, 2, 64, 16, act, kv, pad=3, seed=13)
+        c = b.cache()
+        wide = torch.full((b.rows, 4 * 64 + 64), math.nan, dtype=DT[act], device="cuda")
+        wide[:, :256] = b.q.cuda().reshape(b.rows, 256)
+        out = torch.full((b.rows, 4, 64), 7.0, dtype=DT[act], device="cuda")
+        got = c.attend(wide[:, :256], max_new=2, out=out)
+        attend_close(b, got)
+        assert (got[b.tokens:] == 7.0).all()
+        qkv = torch.full((b.rows, 8 * 64 + 8), math.nan, dtype=DT[act], device="cuda")
+        qkv[:, :512] = b.qkv.cuda()
+        out = torch.full((b.rows, 4, 64), 7.0, dtype=DT[act], device="cuda")
+        got = c.append(qkv[:, :512], 4, out=out)
+        assert (got[b.tokens:] == 7.0).all()
+        check_append(b, got, {})
+
+
+# ------------------------------------------------------------------------------- append
+# Roundings of an f32 rotation: the turn's fraction (four of 2^-25 turns, 7.5e-7 rad), sincospif
+# and the two products (about 6 U), the norm (rsqrtf 2 ulp, its sum of at most 18 adds, two
+# products): below 2e-6 of |x_j| + |x_{j+hd/2}|.
+ROT = 2e-6
+
+
+def check_append(b, got, kw):
+    q, k, v, qs, ks = b.append(**kw)
+    n = b.tokens
+    tol = ROT * qs + HALF[b.act] * (b.act != "f32") * q.abs()
+    assert ((got[:n].double().cpu() - q).abs() <= tol).all()
+    at, slot = b.slots()
+    at_t, slot_t = torch.from_numpy(at), torch.from_numpy(slot)
+    kd, vd = b.kd.cpu(), b.vd.cpu()
+    kk, vv = kd[at_t, :, slot_t].double(), vd[at_t, :, slot_t].double()
+    tol = ROT * ks + HALF[b.kv] * (b.kv != "f32") * k.abs()
+    assert ((kk - k).abs() <= tol).all()
+    assert torch.equal(vv, v.to(DT[b.kv]).double())
+    # every other slot is left as it was
+    old_k, old_v = b.k.clone(), b.v.clone()
+    old_k[at_t, :, slot_t] = kd[at_t, :, slot_t]
+    old_v[at_t, :, slot_t] = vd[at_t, :, slot_t]
+    bits = torch.int16 if b.kv == "bf16" else torch.int32
+    assert torch.equal(old_k.view(bits), kd.view(bits))
+    assert torch.equal(old_v.view(bits), vd.view(bits))
+
+
+@pytest.mark.parametrize("act,kv", TYPES)
+@pytest.mark.parametrize("nq,nkv,hd", HEADS)
+@pytest.mark.parametrize("norm", [False, True])
+def test_append(act, kv, nq, nkv, hd, norm):
+    b = Batch(CHUNKS + [(1, 0), (1, 15), (1, 16)], nq, nkv, hd, 16, act, kv, seed=17)
+    c = b.cache()
+    kw = {}
+    if norm:
+        g = torch.Generator().manual_seed(3)
+        kw = {"q_norm": (1 + 0.1 * torch.randn(hd, generator=g)).to(torch.bfloat16),
+              "k_norm": (1 + 0.1 * torch.randn(hd, generator=g)).to(torch.bfloat16), "eps": 1e-6}
+    dev = {k: (v.cuda() if isinstance(v, torch.Tensor) else v) for k, v in kw.items()}
+    check_append(b, c.append(b.qkv.cuda(), nq, **dev), kw)
+    c.check()
+
+
+@pytest.mark.parametrize("act,kv", [("f32", "bf16"), ("bf16", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("hd,sections", [(128, (16, 24, 24)), (64, (8, 0, 24)), (64, (0, 0, 32)),
+                                         (128, (64, 0, 0))])
+def test_append_three_axes(act, kv, hd, sections):
+    b = Batch([(37, 3), (1, 80), (5, 0)], 4, 2, hd, 32, act, kv, prefix=10, seed=19)
+    c = b.cache()
+    r = np.random.default_rng(1)
+    pos = torch.from_numpy(r.integers(0, 1 << 20, (b.rows, 3)).astype(np.int32))
+    got = c.append(b.qkv.cuda(), 4, positions=pos.cuda(), sections=sections, rope_theta=1e6)
+    check_append(b, got, {"positions": pos, "sections": sections})
+
+
+def test_append_far_and_negative_positions():
+    b = Batch([(64, 0)], 2, 1, 128, 64, "f32", "f32", seed=23)
+    c = b.cache()
+    pos = torch.tensor([0, 1, -1, 65535, 65536, 131071, -65537, (1 << 24) - 1, 1 << 24, -(1 << 24)] * 6 +
+                       [5, 6, 7, 8], dtype=torch.int32)
+    got = c.append(b.qkv.cuda(), 2, positions=pos.cuda(), rope_theta=1e4)
+    check_append(b, got, {"positions": pos, "theta": 1e4})
+
+
+def test_prefix_shifts_the_default_positions():
+    b = Batch([(3, 4), (1, 0)], 4, 2, 64, 16, "f32", "bf16", prefix=77, seed=29)
+    c = b.cache()
+    check_append(b, c.append(b.qkv.cuda(), 4), {})
+
+
+def test_many_sequences():
+    b = Batch([(1, i % 7) for i in range(700)], 2, 1, 64, 16, "f32", "bf16", seed=31)
+    c = b.cache()
+    check_append(b, c.append(b.qkv.cuda(), 2), {})
+    b.k, b.v = b.kd.cpu(), b.vd.cpu()
+    attend_close(b, c.attend(b.q.cuda()))
+
+
+# ------------------------------------------------------------------------------- together
+@pytest.mark.parametrize("act,kv", TYPES)
+def test_append_then_attend_as_a_server_does(act, kv):
+    """A prompt in two chunks, then steps, against attention over the exact rotated keys."""
+    b = Batch([(0, 0), (0, 0)], 8, 2, 64, 16, act, kv, prefix=40, seed=37, extra_cols=12)
+    total = [50, 21]
+    r = np.random.default_rng(5)
+    # pages for the whole conversation
+    need = [-(-t // 16) for t in total]
+    pool = torch.full((sum(need) + len(b.pre) + 3, 2, 16, 64), math.nan, dtype=DT[kv])
+    pre = np.arange(sum(need), sum(need) + len(b.pre))
+    for i, p in enumerate(b.pre):
+        pool[pre[i]] = b.k[p]
+    b.n_pages, b.pre, b.k, b.v = pool.shape[0], pre, pool, pool.clone()
+    order = r.permutation(sum(need))
+    b.table[0, :need[0]], b.table[1, :need[1]] = order[:need[0]], order[need[0]:]
+    b.new, b.len, b.tokens, b.rows = np.array([1, 1]), np.array([1, 1]), 2, 2
+    c = b.cache()
+    done = [0, 0]
+    for step in [(30, 5), (13, 9), (1, 1), (1, 1), (5, 0), (0, 5)]:
+        b.new = np.array(step)
+        done = [done[0] + step[0], done[1] + step[1]]
+        b.len, b.tokens = np.array(done), sum(step)
+        b.rows, b.start = b.tokens, np.concatenate([[0], np.cumsum(step)])
+        b.len_d.copy_(torch.from_numpy(b.len.astype(np.int32)))
+        b.start_d.copy_(torch.from_numpy(b.start.astype(np.int32)))
+        b.qkv = torch.from_numpy(r.standard_normal((b.tokens, 12 * 64))).to(DT[act])
+        q = c.append(b.qkv.cuda(), 8, positions=None)
+        check_append(b, q, {})
+        got = c.attend(q, max_new=max(step))
+        b.k, b.v, b.q = b.kd.cpu(), b.vd.cpu(), q.cpu()
+        attend_close(b, got)
+    c.check()
+
+
+def test_captured_graph_replays_with_new_lengths():
+    b = Batch([(1, 200), (1, 17), (1, 90)], 8, 2, 128, 16, "f32", "bf16", prefix=33, seed=41)
+    c = b.cache()
+    q, qkv = b.q.cuda(), b.qkv.cuda()
+    out = torch.zeros(b.rows, 8, 128, device="cuda")
+    rot = torch.zeros_like(out)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        c.append(qkv, 8, out=rot)
+        c.attend(q, out=out)
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.append(qkv, 8, out=rot)
+        c.attend(q, out=out)
+    for lens in ([201, 18, 91], [60, 3, 16], [1, 1, 1]):
+        b.len = np.array(lens)
+        b.len_d.copy_(torch.from_numpy(b.len.astype(np.int32)))
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        b.k, b.v = b.kd.cpu(), b.vd.cpu()
+        attend_close(b, out)
+    c.check()
+
+
+def test_other_streams():
+    b = Batch([(1, 500), (1, 3)], 8, 2, 128, 16, "bf16", "bf16", seed=43)
+    c = b.cache()
+    q = b.q.cuda()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        got = c.attend(q)
+    s.synchronize()
+    attend_close(b, got)
+
+
+# ------------------------------------------------------------------------------- reported errors
+def test_bad_pages_and_lengths_are_reported():
+    b = Batch([(1, 20), (1, 20)], 4, 2, 64, 16, "f32", "bf16", seed=47)
+    good, tol = b.attend()
+    b.table[0, 0] = b.n_pages
+    c = b.cache()
+    got = c.attend(b.q.cuda()).double().cpu()
+    assert ((got[1] - good[1]).abs() <= tol[1]).all()          # the other sequence is not affected
+    with pytest.raises(RuntimeError, match="BAD_PAGE"):
+        c.check()
+    c.status.zero_()
+    b.table_d[0, 1] = -5                                       # the new token's own page
+    before = b.kd.clone()
+    c.append(b.qkv.cuda(), 4)
+    with pytest.raises(RuntimeError, match="BAD_PAGE"):
+        c.check()
+    at, slot = b.table[1, 1], 20 % 16                          # only sequence 1 was written
+    before[at, :, slot] = b.kd[at, :, slot]
+    assert torch.equal(before.view(torch.int16), b.kd.view(torch.int16))
+    c.status.zero_()
+    b.len_d[1] = 10000                                         # past the table
+    c.append(b.qkv.cuda(), 4)
+    with pytest.raises(RuntimeError, match="BAD_LENGTH"):
+        c.check()
+    c.status.zero_()
+    c.attend(b.q.cuda())
+    with pytest.raises(RuntimeError, match="BAD_LENGTH"):
+        c.check()
+
+
+def test_tensors_that_do_not_fit_are_refused():
+    from sequence_decode_step_gb300 import PagedKV
+    b = Batch([(1, 20)], 4, 2, 64, 16, "f32", "bf16", seed=53)
+    c = b.cache()
+    q = b.q.cuda()
+    with pytest.raises(ValueError):
+        c.attend(q.double())
+    with pytest.raises(ValueError):
+        c.attend(q.cpu())
+    with pytest.raises(ValueError):
+        c.attend(q, out=torch.zeros(1, 4, 64, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError):
+        c.append(b.qkv.cuda()[:, ::2], 4)
+    with pytest.raises(ValueError):
+        c.append(b.qkv.cuda(), 4, positions=torch.zeros(1, dtype=torch.int64, device="cuda"))
+    with pytest.raises(ValueError):
+        PagedKV(b.kd, b.vd, b.table_d.long(), b.len_d, b.start_d)
+    with pytest.raises(ValueError):
+        PagedKV(b.kd, b.vd, b.table_d, b.len_d, b.start_d, prefix_pages=b.len_d, prefix_len=17)
