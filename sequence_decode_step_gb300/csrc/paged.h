@@ -40,7 +40,27 @@ struct AppendArgs {
 };
 cudaError_t launch_paged_append(const AppendArgs& a, int hd, bool act_bf16, cudaStream_t s);
 
-// ---- attention (paged_attention.cu) ----
+// ---- attention ----
+// Partial records of query rows: [rows][hd] unnormalised outputs and their (reference maximum,
+// sum) in base 2. A launch has two slots of `rows` rows per CTA for the items it splits.
+struct PagedSlots {
+  float* o;
+  float2* ml;
+  int rows;
+};
+// The prefix launch's results as the launch over the sequences' own keys finds them: an item
+// that one CTA did whole is in `whole` (a record per (token, query head)), a split one in the
+// slots of CTAs c0 .. c1, which follow from the launch's shape.
+struct PagedPrefix {
+  PagedSlots slots;
+  float* whole_o;      // [n_tokens][nq][hd], nullptr without a prefix
+  float2* whole_ml;    // [n_tokens][nq]
+  int tpt, kt, grid;   // tokens per row tile, keys per tile, CTAs
+};
+struct PagedSplit {    // a split item of a CTA, for the kernel that joins its records
+  int c1;              // last CTA, -1: this CTA begins no split item
+  int token, rows, head;  // first token row, query rows, first query head
+};
 struct PagedAttnArgs {
   PagedView c;
   const void* q;            // [n_tokens][ldq]
@@ -50,23 +70,28 @@ struct PagedAttnArgs {
   int act_bf16;
   int tpt;                  // tokens per row tile
   float scale_log2;         // log2(e) / sqrt(hd)
-  // split items (see PagedSched): slot records of [rows][hd] unnormalised outputs and their
-  // (reference maximum, sum) in base 2, two slots per CTA, and an arrival counter per CTA
-  float* part_o;
-  float2* part_ml;
-  int* counters;
-  // the shared prefix's record per (token, query head): written by the prefix launch
-  // (prefix_pass = 1), merged by the launch over the sequences' own keys (or nullptr)
-  float* pre_o;             // [n_tokens][nq][hd]
-  float2* pre_ml;           // [n_tokens][nq]
-  int prefix_pass;
-  int n_ctas;               // grid size
+  PagedSlots slots;         // of this launch
+  int* counters;            // [grid] arrivals of split items, 0 between launches
+  PagedSplit* splits;       // [grid] (kernels whose records a second kernel joins)
+  int prefix_pass;          // 1: this launch reads the prefix's keys
+  PagedPrefix pre;
   uint64_t wait_ns;
 };
-constexpr int kPagedMaxCtas = 512;  // most CTAs of one attention launch (workspace slots)
+// Keys per tile, query rows per item and CTAs of a launch: a rule on types and row counts.
+struct PagedPlan {
+  bool tc;                  // paged_attention_tc.cu, else paged_attention.cu
+  int kt, rows, grid;
+};
+PagedPlan plan_paged_pass(const PagedAttnArgs& a, int hd, int max_rows, int sms);
 size_t paged_attn_workspace_bytes(int n_tokens, int nq, int hd, bool prefix);
 cudaError_t launch_paged_attention(const PagedAttnArgs& base, int hd, int max_new, void* workspace,
                                    int sms, cudaStream_t s);
 cudaError_t set_paged_attributes();
+
+// ---- tensor-core tiles (paged_attention_tc.cu) ----
+constexpr int kPagedTcKeys = 128;  // keys per tile
+int paged_tc_rows(bool act_bf16);  // query rows per item
+cudaError_t launch_paged_tc(const PagedAttnArgs& a, int hd, int grid, bool pdl, cudaStream_t s);
+cudaError_t set_paged_tc_attributes();
 
 }  // namespace qw

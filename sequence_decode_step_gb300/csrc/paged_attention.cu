@@ -134,6 +134,7 @@ __device__ __forceinline__ void finish_segment(const PagedAttnArgs& a, const Pag
     const float4 y = *reinterpret_cast<const float4*>(join + R * HD + i * 4);
     return make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
   };
+  if (a.pre.whole_o && !a.prefix_pass) pdl_wait();  // the prefix's records, before any is read
   if (whole) {
     for (int i = tid; i < N; i += kConsumers * 32) {
       const int r = i / V4;
@@ -148,10 +149,11 @@ __device__ __forceinline__ void finish_segment(const PagedAttnArgs& a, const Pag
   }
   const long long begin = c.u - c.kt;  // the item's first unit
   const int c0 = (int)(begin / c.per), c1 = (int)((begin + c.nkt - 1) / c.per);
-  const int slot = 2 * blockIdx.x + (first ? 1 : 0);
+  const size_t slot = (size_t)(2 * blockIdx.x + (first ? 1 : 0)) * a.slots.rows;
   for (int i = tid; i < rows * V4; i += kConsumers * 32)
-    __stcg(reinterpret_cast<float4*>(a.part_o + (size_t)slot * R * HD) + i, local(i));
-  if (tid < rows) __stcg(a.part_ml + (size_t)slot * R + tid, row_ml[tid]);
+    __stcg(reinterpret_cast<float4*>(a.slots.o + slot * HD) + i, local(i));
+  if (tid < rows) __stcg(a.slots.ml + slot + tid, row_ml[tid]);
+  if (a.prefix_pass) return;  // joined by the next launch
   __threadfence();
   consumer_sync();
   if (tid == 0) {
@@ -163,24 +165,16 @@ __device__ __forceinline__ void finish_segment(const PagedAttnArgs& a, const Pag
   if (*flag) {
     __threadfence();
     for (int i = tid; i < rows * V4; i += kConsumers * 32) {
-      const int r = i / V4;
+      const int r = i / V4, d = (i % V4) * 4;
       PagedAcc acc;
-      for (int x = c0; x <= c1; ++x)
-        acc.m = fmaxf(acc.m, __ldcg(a.part_ml + (size_t)(2 * x + (x == c0)) * R + r).x);
-      const float mu = acc.m == -INFINITY ? 0.f : acc.m;
-#pragma unroll 4
-      for (int x = c0; x <= c1; ++x) {
-        const size_t sl = (size_t)(2 * x + (x == c0));
-        const float2 ml = __ldcg(a.part_ml + sl * R + r);
-        const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part_o + sl * R * HD) + i);
-        acc.add(paged_exp2(ml.x - mu), ml.y, o);
-      }
-      paged_emit(a, HD, c.s.lo + tok0 + r / a.gq, c.kvh * a.gq + r % a.gq, (i % V4) * 4, acc);
+      paged_join_slots(a.slots, HD, c0, c1, r, d, acc);
+      paged_emit(a, HD, c.s.lo + tok0 + r / a.gq, c.kvh * a.gq + r % a.gq, d, acc);
     }
   }
 }
 
-// Barriers, the CTA's start; false when there is nothing to do.
+// Barriers, the CTA's start; false when there is nothing to do. Every thread of a launch waits for
+// the launch before it (pdl_wait) before it leaves, so that stream order holds for what follows.
 template <int KT, class LY>
 __device__ __forceinline__ bool open_cta(const PagedAttnArgs& a, uint8_t* sm) {
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + LY::off_bar);
@@ -193,6 +187,7 @@ __device__ __forceinline__ bool open_cta(const PagedAttnArgs& a, uint8_t* sm) {
     }
     fence_barrier_init();
   }
+  if (a.prefix_pass) pdl_launch_dependents();
   paged_find_start<KT, kThreads>(a, st, reinterpret_cast<long long*>(sm + LY::off_start + 64));
   return st->u < st->u1;
 }
@@ -266,11 +261,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + LY::off_bar);
   uint64_t* empty = full + NS;
   PagedStart* st = reinterpret_cast<PagedStart*>(sm + LY::off_start);
-  if (!open_cta<KT, LY>(a, sm)) return;
+  if (!open_cta<KT, LY>(a, sm)) return pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == kConsumers) {
     produce<HD, KT, true>(a, &tk, &tv, st, sm, full, empty);
-    return;
+    return pdl_wait();
   }
   float* join = reinterpret_cast<float*>(sm + LY::off_join);
   float2* ml_s = reinterpret_cast<float2*>(sm + LY::off_ml);
@@ -487,11 +482,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + LY::off_bar);
   uint64_t* empty = full + NS;
   PagedStart* st = reinterpret_cast<PagedStart*>(sm + LY::off_start);
-  if (!open_cta<KT, LY>(a, sm)) return;
+  if (!open_cta<KT, LY>(a, sm)) return pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == kConsumers) {
     produce<HD, KT, false>(a, nullptr, nullptr, st, sm, full, empty);
-    return;
+    return pdl_wait();
   }
   float* join = reinterpret_cast<float*>(sm + LY::off_join);
   float2* ml_s = reinterpret_cast<float2*>(sm + LY::off_ml);
@@ -612,8 +607,23 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (bad && lane == 0 && a.c.status) atomicOr(a.c.status, PG_TIMEOUT);
 }
 
+// One launch; with `pdl` it may start while the launch before it (the prefix's) still runs.
+template <class K, class... Args>
+cudaError_t launch(K kernel, int grid, uint32_t smem, bool pdl, cudaStream_t s, const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 template <int HD, int NT>
-cudaError_t launch_mma(PagedAttnArgs a, cudaStream_t s) {
+cudaError_t launch_mma(const PagedAttnArgs& a, int grid, bool pdl, cudaStream_t s) {
   constexpr int R = NT == 1 ? 16 : 8;
   CUtensorMap tk, tv;
   const uint64_t rows = (uint64_t)a.c.n_pages * a.c.nkv << a.c.page_shift;
@@ -621,23 +631,20 @@ cudaError_t launch_mma(PagedAttnArgs a, cudaStream_t s) {
   if (!make_tmap_bf16_2d(&tk, a.c.k_pages, rows, HD, box) ||
       !make_tmap_bf16_2d(&tv, a.c.v_pages, rows, HD, box))
     return cudaErrorInvalidValue;
-  a.tpt = R / a.gq;
-  paged_attn_mma_kernel<HD, NT><<<a.n_ctas, kThreads, PgLayout<HD, 64, 2, R>::bytes, s>>>(a, tk, tv);
-  return cudaGetLastError();
+  return launch(paged_attn_mma_kernel<HD, NT>, grid, PgLayout<HD, 64, 2, R>::bytes, pdl, s, a, tk, tv);
 }
 template <int HD, int R>
-cudaError_t launch_fma_r(PagedAttnArgs a, cudaStream_t s) {
-  a.tpt = R / a.gq;
-  paged_attn_fma_kernel<HD, R><<<a.n_ctas, kThreads, PgLayout<HD, 32, 4, R>::bytes, s>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_fma(const PagedAttnArgs& a, int grid, bool pdl, cudaStream_t s) {
+  return launch(paged_attn_fma_kernel<HD, R>, grid, PgLayout<HD, 32, 4, R>::bytes, pdl, s, a);
 }
 template <int HD>
-cudaError_t launch_pass(const PagedAttnArgs& a, int max_new, cudaStream_t s) {
-  if (a.c.kv_bf16) return a.act_bf16 ? launch_mma<HD, 1>(a, s) : launch_mma<HD, 3>(a, s);
-  const int rows = max_new * a.gq;  // the smallest tile that holds them
-  if (rows <= 2) return launch_fma_r<HD, 2>(a, s);
-  if (rows <= 4) return launch_fma_r<HD, 4>(a, s);
-  return launch_fma_r<HD, 8>(a, s);
+cudaError_t launch_pass(const PagedAttnArgs& a, const PagedPlan& p, bool pdl, cudaStream_t s) {
+  if (p.tc) return launch_paged_tc(a, HD, p.grid, pdl, s);
+  if (a.c.kv_bf16)
+    return a.act_bf16 ? launch_mma<HD, 1>(a, p.grid, pdl, s) : launch_mma<HD, 3>(a, p.grid, pdl, s);
+  if (p.rows == 2) return launch_fma<HD, 2>(a, p.grid, pdl, s);
+  if (p.rows == 4) return launch_fma<HD, 4>(a, p.grid, pdl, s);
+  return launch_fma<HD, 8>(a, p.grid, pdl, s);
 }
 
 template <class K>
@@ -654,18 +661,30 @@ cudaError_t set_attributes_hd() {
   return e;
 }
 
-// Workspace: arrival counters, then the slots of both launches (records of up to 16 rows), then
-// the prefix's records.
-constexpr int kMaxR = 16;
+// Workspace of a call: counters and split descriptors, the slots of the two launches, the
+// prefix's whole records. A slot holds as many rows as an item can have: at most kMaxRows and at
+// most 8 query heads of every token.
+constexpr int kMaxSms = 192;         // CTAs per launch: at most two per SM
+constexpr int kMaxRows = 256;
 constexpr size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+int slot_rows(int n_tokens) {
+  return std::max(16, (int)std::min<long long>(kMaxRows, (8LL * n_tokens + 15) / 16 * 16));
+}
 struct Workspace {
-  size_t counters = 0, ml, o, pre_ml, pre_o, total;
+  size_t counters = 0, splits, ml[2], o[2], whole_ml, whole_o, total;
   Workspace(int n_tokens, int nq, int hd, bool prefix) {
-    ml = align256(kPagedMaxCtas * 4);
-    o = ml + align256((size_t)2 * kPagedMaxCtas * kMaxR * 8);
-    pre_ml = o + align256((size_t)2 * kPagedMaxCtas * kMaxR * hd * 4);
-    pre_o = pre_ml + (prefix ? align256((size_t)n_tokens * nq * 8) : 0);
-    total = pre_o + (prefix ? (size_t)n_tokens * nq * hd * 4 : 0);
+    // an item of more than 16 rows belongs to one CTA per SM, smaller ones to two
+    const size_t rows = (size_t)2 * std::max(kMaxSms * slot_rows(n_tokens), 2 * kMaxSms * 16);
+    splits = align256(2 * kMaxSms * 4);
+    size_t at = splits + align256(2 * kMaxSms * sizeof(PagedSplit));
+    for (int i = 0; i < (prefix ? 2 : 1); ++i) {
+      ml[i] = at;
+      o[i] = at + align256(rows * 8);
+      at = o[i] + align256(rows * hd * 4);
+    }
+    whole_ml = at;
+    whole_o = at + (prefix ? align256((size_t)n_tokens * nq * 8) : 0);
+    total = whole_o + (prefix ? (size_t)n_tokens * nq * hd * 4 : 0);
   }
 };
 
@@ -677,7 +696,25 @@ size_t paged_attn_workspace_bytes(int n_tokens, int nq, int hd, bool prefix) {
 
 cudaError_t set_paged_attributes() {
   cudaError_t e = set_attributes_hd<64>();
-  return e == cudaSuccess ? set_attributes_hd<128>() : e;
+  if (e == cudaSuccess) e = set_attributes_hd<128>();
+  return e == cudaSuccess ? set_paged_tc_attributes() : e;
+}
+
+// max_rows: the most query rows (tokens x heads of a KV head) that meet one key.
+PagedPlan plan_paged_pass(const PagedAttnArgs& a, int hd, int max_rows, int sms) {
+  sms = std::min(sms, kMaxSms);
+  PagedPlan p{};
+  if (a.c.kv_bf16) {
+    p.tc = max_rows > 16;
+    p.kt = p.tc ? kPagedTcKeys : 64;
+    p.rows = p.tc ? paged_tc_rows(a.act_bf16) : a.act_bf16 ? 16 : 8;
+    p.grid = p.tc ? sms : 2 * sms;
+  } else {
+    p.kt = 32;
+    p.rows = max_rows <= 2 ? 2 : max_rows <= 4 ? 4 : 8;  // the smallest tile that holds them
+    p.grid = 2 * sms;
+  }
+  return p;
 }
 
 cudaError_t launch_paged_attention(const PagedAttnArgs& base, int hd, int max_new, void* workspace,
@@ -687,21 +724,30 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& base, int hd, int max_ne
   const Workspace w(a.n_tokens, a.nq, hd, prefix);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.counters = reinterpret_cast<int*>(ws);
-  a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
-  a.part_o = reinterpret_cast<float*>(ws + w.o);
-  a.pre_ml = prefix ? reinterpret_cast<float2*>(ws + w.pre_ml) : nullptr;
-  a.pre_o = prefix ? reinterpret_cast<float*>(ws + w.pre_o) : nullptr;
-  a.n_ctas = std::min(2 * sms, kPagedMaxCtas);
-  auto pass = [&](int rows_new) {
-    return hd == 64 ? launch_pass<64>(a, rows_new, s) : launch_pass<128>(a, rows_new, s);
+  a.splits = reinterpret_cast<PagedSplit*>(ws + w.splits);
+  auto run = [&](const PagedPlan& p, int i, bool pdl) {
+    a.tpt = p.rows > 128 ? 2 * (128 / a.gq) : p.rows / a.gq;
+    a.slots.ml = reinterpret_cast<float2*>(ws + w.ml[i]);
+    a.slots.o = reinterpret_cast<float*>(ws + w.o[i]);
+    a.slots.rows = p.tc ? slot_rows(a.n_tokens) : p.rows;
+    return hd == 64 ? launch_pass<64>(a, p, pdl, s) : launch_pass<128>(a, p, pdl, s);
   };
+  const long long cap = 1 << 20;  // row counts only choose a kernel
   if (prefix) {
+    a.pre.whole_ml = reinterpret_cast<float2*>(ws + w.whole_ml);
+    a.pre.whole_o = reinterpret_cast<float*>(ws + w.whole_o);
     a.prefix_pass = 1;
-    const cudaError_t e = pass(a.n_tokens);
+    const PagedPlan p = plan_paged_pass(a, hd, (int)std::min(cap, (long long)a.n_tokens * a.gq), sms);
+    const cudaError_t e = run(p, 1, false);
     if (e != cudaSuccess) return e;
     a.prefix_pass = 0;
+    a.pre.slots = a.slots;
+    a.pre.tpt = a.tpt;
+    a.pre.kt = p.kt;
+    a.pre.grid = p.grid;
   }
-  return pass(max_new);
+  const int rows = (int)std::min(cap, (long long)std::min(max_new, a.n_tokens) * a.gq);
+  return run(plan_paged_pass(a, hd, rows, sms), 0, prefix);
 }
 
 }  // namespace qw

@@ -1,0 +1,559 @@
+// qw_paged_attention for many query rows per key: a prefix that a batch shares, and chunks of
+// prompts. bf16 pages, tcgen05 tiles of 128 query rows x 128 keys.
+//
+//   S = Q K^T (TMEM, f32),  P = 2^(s scale - m) as bf16 back into TMEM,  O += P V (TMEM, f32)
+//
+// with the running maximum m and sum of a row in the registers of the one thread that owns the
+// row. m only moves when a row's maximum rises by more than 8 (P stays below 2^8, l and O in f32),
+// so the rescaling of O in TMEM is rare. K tiles are K-major and V tiles MN-major as their pages
+// hold them (rows of head_dim): nothing is transposed.
+//
+// bf16 activations (NT = 1): two row tiles (streams) of 128 rows per CTA share the key tiles, which
+// halves their L2 traffic, and the tensor core works on one stream's products while the other
+// stream's warps form their exponentials. A stream's P overwrites its S. Per stream and tile the
+// products take 2 x 128^3 MACs = 1024 cycles at the dense bf16 rate and the 128 x 128 exponentials
+// and packing about as long, so two streams keep the tensor core busy.
+// f32 activations (NT = 3): q and P as three bf16 terms each (24 bits, f32 results), six products
+// per tile, one stream with two S buffers; the tensor core is the bound by itself.
+//
+// Warps: 0 page look-up and TMA, 1 MMA issue, 4-7 (and 8-11) softmax; TMEM is S/P and O:
+//   NT = 1: S_A, S_B (128 columns each), O_A, O_B
+//   NT = 3: S_0, S_1, O, X_0, X_1 (64 each); P's first two terms overwrite S_i, the third is in X_i
+// Work is shared as in paged_sched.cuh with one CTA per SM (its tiles fill the shared memory).
+
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "paged.h"
+#include "paged_sched.cuh"
+#include "qw_internal.h"
+#include "qw_ptx.cuh"
+
+namespace qw {
+namespace {
+
+constexpr int KT = kPagedTcKeys;
+
+// mbar_wait inlined: a call in the softmax loop would have to save the row of scores around it.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, int phase, uint64_t limit_ns) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 1;; ++n) {
+    if (mbar_try_wait(bar, (uint32_t)(phase & 1))) return true;
+    if ((n & 15u) != 0) continue;
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    else if (now - t0 > limit_ns) return false;
+  }
+}
+
+template <int HD, int NT>
+struct TcLayout {
+  static constexpr int kStreams = NT == 1 ? 2 : 1;
+  static constexpr int kThreads = 128 + 128 * kStreams;
+  static constexpr uint32_t kQ1 = 128 * HD * 2;            // one term of a stream's q tile
+  static constexpr uint32_t kQ = kQ1 * (NT == 1 ? 2 : 3);
+  static constexpr uint32_t kTile = KT * HD * 2;           // a K or V tile
+  static constexpr int kSlots = (224 * 1024 - kQ) / kTile > 10 ? 10 : (224 * 1024 - kQ) / kTile;
+  static constexpr uint32_t off_ring = kQ;
+  static constexpr uint32_t off_start = off_ring + kSlots * kTile;
+  static constexpr uint32_t off_bar = off_start + 64 + 128;
+  static constexpr int kBars = 2 * kSlots + 8;
+  static constexpr uint32_t off_tmem = off_bar + kBars * 8;
+  static constexpr uint32_t bytes = off_tmem + 16;
+  static constexpr uint32_t t_o = 256, t_x = 384;          // TMEM columns (t_x: NT = 3)
+  static_assert(bytes <= 227 * 1024, "tiles fit one CTA's shared memory");
+};
+
+__device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+  hi = paged_pack(a, b);
+  const float ra = a - __uint_as_float(hi << 16), rb = b - __uint_as_float(hi & 0xffff0000u);
+  mid = paged_pack(ra, rb);
+  lo = paged_pack(ra - __uint_as_float(mid << 16), rb - __uint_as_float(mid & 0xffff0000u));
+}
+
+template <int HD, int NT>
+__global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
+    paged_attn_tc_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ CUtensorMap tk,
+                         const __grid_constant__ CUtensorMap tv) {
+  using LY = TcLayout<HD, NT>;
+  constexpr int NS = LY::kSlots, ST = LY::kStreams, QA = HD / 64;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(sm + LY::off_bar);
+  uint64_t* kv_empty = kv_full + NS;
+  uint64_t* q_full = kv_empty + NS;
+  uint64_t* s_full = q_full + 1;   // NT = 1: of each stream; NT = 3: of each S buffer
+  uint64_t* p_full = s_full + 2;   // NT = 1: of each stream; NT = 3: p_full[0]
+  uint64_t* o_full = p_full + 2;   // NT = 1: the end of an item, of each stream; NT = 3: every tile
+  uint64_t* done = o_full + 2;     // every MMA of this CTA has finished
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + LY::off_tmem);
+  PagedStart* st = reinterpret_cast<PagedStart*>(sm + LY::off_start);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (a.prefix_pass) pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
+    }
+    mbar_init(q_full, 4 * ST);  // one arrival per softmax warp
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_full[i], 1);
+    }
+    mbar_init(done, 1);
+    fence_barrier_init();
+    if (!a.prefix_pass) a.splits[blockIdx.x].c1 = -1;
+  }
+  if (warp == 1) {
+    tmem_alloc(tslot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  paged_find_start<KT, LY::kThreads>(a, st, reinterpret_cast<long long*>(sm + LY::off_start + 64));
+  tc_fence_after();
+  const uint32_t tb = *tslot;
+  const int half = 128 / a.gq;  // tokens of a row tile
+  const bool idle = st->u >= st->u1;
+
+  if (idle) {
+  } else if (warp == 0) {
+    // ---- producer: lane = (K or V) x column block x piece of a page's rows
+    const int prow = min(KT, 1 << a.c.page_shift), np = KT / prow;
+    const int piece = lane % np, cb = (lane / np) % QA, kv = lane / (np * QA);
+    const bool mine = kv < 2;
+    PagedCursor c = paged_cursor<KT>(a, st);
+    auto page_of = [&](const PagedCursor& x) {
+      const int key = x.kt * KT + piece * prow;
+      return key < x.limit ? paged_page(a, x.b, key) : -1;
+    };
+    int page = page_of(c), issued = 0;
+    bool ok = true;
+    while (ok && c.u < c.u1) {
+      const int key = c.kt * KT + piece * prow, kvh = c.kvh, now = page;
+      const int pieces = min(np, (max(c.limit - c.kt * KT, 0) + prow - 1) / prow);
+      ++c.u;
+      ++c.kt;
+      if (c.u < c.u1) {
+        if (c.kt == c.nkt) c.next_item<KT>(a);
+        page = page_of(c);
+      }
+#pragma unroll 1
+      for (int t = 0; t < 2; ++t) {
+        const int slot = issued % NS;
+        if (issued >= NS &&
+            !__all_sync(0xffffffffu,
+                        wait_for(&kv_empty[slot], issued / NS - 1, a.wait_ns))) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) mbar_expect_tx(&kv_full[slot], (uint32_t)pieces * prow * HD * 2);
+        __syncwarp();
+        if (mine && kv == t && now >= 0)
+          tma_load_2d(sm + LY::off_ring + slot * LY::kTile + cb * (KT * 128) + piece * prow * 128,
+                      t ? &tv : &tk, cb * 64, (int)paged_row(a, now, kvh, key), &kv_full[slot]);
+        ++issued;
+      }
+    }
+    if (!ok && lane == 0 && a.c.status) atomicOr(a.c.status, PG_TIMEOUT);
+    for (int i = max(0, issued - NS); i < issued; ++i)  // the copies have landed
+      wait_for(&kv_full[i % NS], i / NS, kDrainNs);
+  } else if (warp == 1) {
+    // ---- MMA issue
+    if (lane == 0) {
+      constexpr uint32_t id_s = idesc_bf16_f32(128, KT);
+      constexpr uint32_t id_o = idesc_bf16_f32(128, HD) | kIdescBMnMajor;
+      const uint32_t qs = smem_addr(sm), ring = smem_addr(sm + LY::off_ring);
+      auto issue_s = [&](uint32_t q, uint32_t k, uint32_t d) {  // d = q . k^T (all terms of q)
+#pragma unroll
+        for (int c = 0; c < QA; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint64_t dk = sw128_kmajor_desc(k + c * (KT * 128) + i * 32);
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+              tc_mma_bf16(d, sw128_kmajor_desc(q + t * LY::kQ1 + c * (128 * 128) + i * 32), dk, id_s,
+                          (c | i | t) != 0);
+          }
+      };
+      PagedCursor c = paged_cursor<KT>(a, st);
+      int items = 0, tiles = 0;  // of this CTA so far; tile g uses slots 2g (K), 2g + 1 (V)
+      int turns[2] = {0, 0};     // tiles of each stream
+      auto wait = [&](uint64_t* bar, int n) { return wait_for(bar, n, a.wait_ns); };
+      auto kv_wait = [&](int use) { return wait(&kv_full[use % NS], use / NS); };
+      auto slot_at = [&](int use) { return ring + (uint32_t)(use % NS) * LY::kTile; };
+      bool ok = true;
+      while (ok && c.u < c.u1) {
+        const int n = (int)min((long long)(c.nkt - c.kt), c.u1 - c.u);
+        const bool two = NT == 1 && c.s.nb - c.rt * a.tpt > half;  // the second stream has rows
+        ok = wait(q_full, items) && kv_wait(2 * tiles);
+        if (!ok) break;
+        tc_fence_after();
+        if constexpr (NT == 1) {
+          issue_s(qs, slot_at(2 * tiles), tb);
+          tc_commit(&s_full[0]);
+          if (two) {
+            issue_s(qs + LY::kQ1, slot_at(2 * tiles), tb + 128);
+            tc_commit(&s_full[1]);
+          }
+          tc_commit(&kv_empty[(2 * tiles) % NS]);
+          for (int x = 0; x < n; ++x) {
+            const int g = tiles + x;
+            ok = kv_wait(2 * g + 1);
+            for (int s = 0; ok && s < (two ? 2 : 1); ++s) {
+              ok = wait(&p_full[s], turns[s]++);
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t v = slot_at(2 * g + 1), p = tb + 128 * s;
+#pragma unroll
+              for (int i = 0; i < KT / 16; ++i)
+                tc_mma_bf16_ta(tb + LY::t_o + 128 * s, p + 8 * i,
+                               sw128_mnmajor_desc(v + i * 2048, KT * 128), id_o, (x | i) != 0);
+              if (x + 1 < n) {  // the stream's next scores, into the columns P leaves
+                if (s == 0) ok = kv_wait(2 * g + 2);
+                if (!ok) break;
+                issue_s(qs + s * LY::kQ1, slot_at(2 * g + 2), p);
+                tc_commit(&s_full[s]);
+              } else {
+                tc_commit(&o_full[s]);
+              }
+            }
+            if (!ok) break;
+            tc_commit(&kv_empty[(2 * g + 1) % NS]);
+            if (x + 1 < n) tc_commit(&kv_empty[(2 * g + 2) % NS]);
+          }
+        } else {
+          issue_s(qs, slot_at(2 * tiles), tb + 128 * (tiles & 1));
+          tc_commit(&s_full[tiles & 1]);
+          tc_commit(&kv_empty[(2 * tiles) % NS]);
+          for (int x = 0; x < n; ++x) {
+            const int g = tiles + x;
+            if (x + 1 < n) {  // the next tile's scores while this one's weights are formed
+              ok = kv_wait(2 * g + 2);
+              if (!ok) break;
+              tc_fence_after();
+              issue_s(qs, slot_at(2 * g + 2), tb + 128 * ((g + 1) & 1));
+              tc_commit(&s_full[(g + 1) & 1]);
+              tc_commit(&kv_empty[(2 * g + 2) % NS]);
+            }
+            ok = kv_wait(2 * g + 1) && wait(&p_full[0], g);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t v = slot_at(2 * g + 1), p = tb + 128 * (g & 1);
+            const uint32_t px = tb + LY::t_x + 64 * (g & 1);
+#pragma unroll
+            for (int i = 0; i < KT / 16; ++i) {
+              const uint64_t dv = sw128_mnmajor_desc(v + i * 2048, KT * 128);
+              tc_mma_bf16_ta(tb + LY::t_o, p + 8 * i, dv, id_o, (x | i) != 0);
+              tc_mma_bf16_ta(tb + LY::t_o, p + 64 + 8 * i, dv, id_o, 1);
+              tc_mma_bf16_ta(tb + LY::t_o, px + 8 * i, dv, id_o, 1);
+            }
+            tc_commit(&o_full[0]);
+            tc_commit(&kv_empty[(2 * g + 1) % NS]);
+          }
+        }
+        tiles += n;
+        ++items;
+        c.u += n;
+        c.kt += n;
+        if (c.u < c.u1) c.next_item<KT>(a);
+      }
+      if (!ok && a.c.status) atomicOr(a.c.status, PG_TIMEOUT);
+      // TMEM is released only after every MMA issued here has finished
+      tc_commit(done);
+      wait_for(done, 0, kDrainNs);
+    }
+  } else if (warp >= 4) {
+    // ---- softmax of a stream: thread = query row
+    const int s = (warp - 4) >> 2, r = threadIdx.x & 127;
+    const uint32_t lrow = (uint32_t)((warp & 3) * 32) << 16;
+    PagedCursor c = paged_cursor<KT>(a, st);
+    int tiles = 0, mine = 0;  // of the CTA; of this stream
+    int ends = 0;             // items whose end this stream has waited for
+    bool bad = false;
+    auto wait = [&](uint64_t* bar, int n) {
+      if (!bad) bad = !__all_sync(0xffffffffu, wait_for(bar, n, a.wait_ns));
+    };
+    while (c.u < c.u1) {
+      const int n = (int)min((long long)(c.nkt - c.kt), c.u1 - c.u);
+      const bool first = c.kt == 0, whole = first && n == c.nkt;
+      const int tok0 = c.rt * a.tpt + s * half;              // of this stream's row tile
+      const int ntok = min(max(c.s.nb - tok0, 0), half), rows = ntok * a.gq;
+      const bool live = r < rows;
+      const int tok = c.s.lo + tok0 + r / a.gq, head = c.kvh * a.gq + r % a.gq;
+      const int lim = !live           ? 0
+                      : a.prefix_pass ? c.limit
+                                      : min(max(c.s.base + tok0 + r / a.gq + 1, 0), c.s.len);
+      // q into shared memory, K-major with 128-byte swizzling: 16-byte units of 8 columns
+      {
+        const size_t at = (size_t)tok * a.ldq + (size_t)head * HD;
+        uint8_t* row = sm + (NT == 1 ? s * LY::kQ1 : 0) + (r >> 3) * 1024 + (r & 7) * 128;
+#pragma unroll 8
+        for (int u = 0; u < HD / 8; ++u) {
+          const uint32_t off = (u >> 3) * (128 * 128) + (((u & 7) ^ (r & 7)) << 4);
+          if constexpr (NT == 1) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (live)
+              v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at) + u);
+            *reinterpret_cast<uint4*>(row + off) = v;
+          } else {
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+            if (live) {
+              const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at) + 2 * u;
+              x = __ldg(p);
+              y = __ldg(p + 1);
+            }
+            uint32_t h[4], m[4], l[4];
+            split3(x.x, x.y, h[0], m[0], l[0]);
+            split3(x.z, x.w, h[1], m[1], l[1]);
+            split3(y.x, y.y, h[2], m[2], l[2]);
+            split3(y.z, y.w, h[3], m[3], l[3]);
+            *reinterpret_cast<uint4*>(row + off) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(row + LY::kQ1 + off) = make_uint4(m[0], m[1], m[2], m[3]);
+            *reinterpret_cast<uint4*>(row + 2 * LY::kQ1 + off) = make_uint4(l[0], l[1], l[2], l[3]);
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cta(q_full);
+      }
+      float m = -INFINITY, l = 0.f;
+      const uint32_t to = tb + LY::t_o + 128 * s + lrow;
+      for (int x = 0; x < (rows > 0 ? n : 0); ++x, ++mine) {
+        const int g = tiles + x, buf = NT == 1 ? s : g & 1;
+        const uint32_t ts = tb + 128 * buf + lrow;
+        wait(&s_full[buf], NT == 1 ? mine : g >> 1);
+        tc_fence_after();
+        const int k0 = (c.kt + x) * KT;
+        if (k0 + KT > c.limit && s == 0) {
+          // values behind the last key are whatever the page held: cleared (0 * NaN is NaN)
+          wait(&kv_full[(2 * g + 1) % NS], (2 * g + 1) / NS);
+          if (k0 + r >= c.limit) {
+            uint4* v = reinterpret_cast<uint4*>(sm + LY::off_ring + ((2 * g + 1) % NS) * LY::kTile + r * 128);
+#pragma unroll
+            for (int cb = 0; cb < QA; ++cb)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[cb * (KT * 8) + i] = make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        // Half a row of scores at a time in registers: the second half is read for its maximum, given
+        // up, and read again for its weights; the first half stays (keys no row sees are -inf).
+        uint32_t sv[KT / 2];
+        const bool edge = k0 + KT > c.limit - a.tpt;
+        auto load_half = [&](int hf) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            tmem_ld16(ts + 64 * hf + 16 * i, *reinterpret_cast<uint32_t(*)[16]>(sv + 16 * i));
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_regs_ready(*reinterpret_cast<uint32_t(*)[16]>(sv + 16 * i));
+          if (edge) {
+#pragma unroll
+            for (int j = 0; j < 64; ++j)
+              if (k0 + 64 * hf + j >= lim) sv[j] = 0xff800000u;  // -inf
+          }
+        };
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto max_half = [&] {
+#pragma unroll
+          for (int j = 0; j < 64; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], __uint_as_float(sv[j]));
+        };
+        load_half(1);
+        max_half();
+        load_half(0);
+        max_half();
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.scale_log2;
+        const float mn = mx > m + 8.f ? mx : m;  // a row without a key yet keeps -inf
+        const float mu = mn == -INFINITY ? 0.f : mn;
+        const float alpha = paged_exp2(m - mu);
+        // the weights, 32 keys at a time, into TMEM. They overwrite columns of S that have been read:
+        // 16 i .. 16 i + 15 after keys 32 i .. 32 i + 31 (NT = 1); with NT = 3 both terms' columns
+        // cover S, so the second half waits in registers of its own
+        float ps[4] = {0.f, 0.f, 0.f, 0.f};
+        auto weights = [&](const uint32_t* v, int i) {
+          float p[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            p[e] = paged_exp2(fmaf(__uint_as_float(v[e]), a.scale_log2, -mu));
+            ps[e & 3] += p[e];
+          }
+          uint32_t ph[16];
+          if constexpr (NT == 1) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) ph[e] = paged_pack(p[2 * e], p[2 * e + 1]);
+            tmem_st16(ts + 16 * i, ph);
+          } else {
+            uint32_t pm[16], pl[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) split3(p[2 * e], p[2 * e + 1], ph[e], pm[e], pl[e]);
+            tmem_st16(ts + 16 * i, ph);
+            tmem_st16(ts + 64 + 16 * i, pm);
+            tmem_st16(tb + LY::t_x + 64 * buf + lrow + 16 * i, pl);
+          }
+        };
+        if constexpr (NT == 1) {
+          weights(sv, 0);
+          weights(sv + 32, 1);
+          load_half(1);
+          weights(sv, 2);
+          weights(sv + 32, 3);
+        } else {
+          uint32_t first_half[KT / 2];
+#pragma unroll
+          for (int j = 0; j < KT / 2; ++j) first_half[j] = sv[j];
+          load_half(1);
+          weights(first_half, 0);
+          weights(first_half + 32, 1);
+          weights(sv, 2);
+          weights(sv + 32, 3);
+        }
+        l = l * alpha + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
+        if (NT == 3 && x > 0) wait(&o_full[0], g - 1);  // (NT = 1: before s_full of this tile)
+        if (x > 0 && __any_sync(0xffffffffu, mn != m)) {
+          tc_fence_after();
+#pragma unroll 1
+          for (int d = 0; d < HD; d += 16) {
+            uint32_t o[16];
+            tmem_ld16(to + d, o);
+            tmem_ld_wait();
+            tmem_regs_ready(o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st16(to + d, o);
+          }
+        }
+        m = mn;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cta(&p_full[NT == 1 ? s : 0]);
+      }
+      if (rows > 0) {
+        if constexpr (NT == 1)
+          wait(&o_full[s], ends++);
+        else
+          wait(&o_full[0], tiles + n - 1);
+        tc_fence_after();
+        if (whole && a.pre.whole_o && !a.prefix_pass) pdl_wait();  // the prefix's records
+        const size_t slot = (size_t)(2 * blockIdx.x + (first ? 1 : 0)) * a.slots.rows + s * half * a.gq + r;
+#pragma unroll 1
+        for (int d = 0; d < HD; d += 16) {
+          uint32_t o[16];
+          tmem_ld16(to + d, o);
+          tmem_ld_wait();
+          tmem_regs_ready(o);
+          if (!live) continue;
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            PagedAcc acc;
+            acc.m = m;
+            acc.l = l;
+            acc.o = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                                __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+            if (whole)
+              paged_emit(a, HD, tok, head, d + e, acc);
+            else
+              *reinterpret_cast<float4*>(a.slots.o + slot * HD + d + e) = acc.o;
+          }
+        }
+        if (live && !whole) a.slots.ml[slot] = make_float2(m, l);
+        tc_fence_before();
+      }
+      if (!whole && first && s == 0 && r == 0 && !a.prefix_pass) {  // the joining kernel's work
+        const long long begin = c.u - c.kt;
+        a.splits[blockIdx.x] = PagedSplit{(int)((begin + c.nkt - 1) / c.per), c.s.lo + c.rt * a.tpt,
+                                          min(a.tpt, c.s.nb - c.rt * a.tpt) * a.gq, c.kvh * a.gq};
+      }
+      tiles += n;
+      c.u += n;
+      c.kt += n;
+      if (c.u < c.u1) c.next_item<KT>(a);
+    }
+    if (bad && lane == 0 && a.c.status) atomicOr(a.c.status, PG_TIMEOUT);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tb, 512);
+  }
+  pdl_wait();
+}
+
+// Joins the records of the items that a launch split: CTA (x, y) takes rows y, y + gridDim.y, ..
+// (4 at a time) of the item that begins in CTA x.
+template <int HD>
+__global__ void __launch_bounds__(HD) paged_join_kernel(const __grid_constant__ PagedAttnArgs a) {
+  constexpr int V4 = HD / 4;  // threads of a row
+  pdl_wait();
+  const PagedSplit sp = a.splits[blockIdx.x];
+  if (sp.c1 < 0) return;
+  const int d = threadIdx.x % V4 * 4;
+  for (int r = blockIdx.y * 4 + threadIdx.x / V4; r < sp.rows; r += gridDim.y * 4) {
+    PagedAcc acc;
+    paged_join_slots(a.slots, HD, blockIdx.x, sp.c1, r, d, acc);
+    paged_emit(a, HD, sp.token + r / a.gq, sp.head + r % a.gq, d, acc);
+  }
+}
+
+template <class... P, class... Args>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, uint32_t smem, bool pdl, cudaStream_t s,
+                   const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int HD, int NT>
+cudaError_t launch_tc(const PagedAttnArgs& a, int grid, bool pdl, cudaStream_t s) {
+  CUtensorMap tk, tv;
+  const uint64_t rows = (uint64_t)a.c.n_pages * a.c.nkv << a.c.page_shift;
+  const uint32_t box = std::min(KT, 1 << a.c.page_shift);
+  if (!make_tmap_bf16_2d(&tk, a.c.k_pages, rows, HD, box) ||
+      !make_tmap_bf16_2d(&tv, a.c.v_pages, rows, HD, box))
+    return cudaErrorInvalidValue;
+  cudaError_t e = launch(paged_attn_tc_kernel<HD, NT>, dim3(grid), TcLayout<HD, NT>::kThreads,
+                         TcLayout<HD, NT>::bytes, pdl, s, a, tk, tv);
+  if (e == cudaSuccess && !a.prefix_pass)
+    e = launch(paged_join_kernel<HD>, dim3(grid, 8), HD, 0, false, s, a);
+  return e;
+}
+template <int HD>
+cudaError_t set_attributes_hd() {
+  cudaError_t e = cudaFuncSetAttribute(paged_attn_tc_kernel<HD, 1>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)TcLayout<HD, 1>::bytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(paged_attn_tc_kernel<HD, 3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)TcLayout<HD, 3>::bytes);
+  return e;
+}
+
+}  // namespace
+
+int paged_tc_rows(bool act_bf16) { return act_bf16 ? 256 : 128; }
+
+cudaError_t launch_paged_tc(const PagedAttnArgs& a, int hd, int grid, bool pdl, cudaStream_t s) {
+  if (hd == 64) return a.act_bf16 ? launch_tc<64, 1>(a, grid, pdl, s) : launch_tc<64, 3>(a, grid, pdl, s);
+  return a.act_bf16 ? launch_tc<128, 1>(a, grid, pdl, s) : launch_tc<128, 3>(a, grid, pdl, s);
+}
+
+cudaError_t set_paged_tc_attributes() {
+  cudaError_t e = set_attributes_hd<64>();
+  return e == cudaSuccess ? set_attributes_hd<128>() : e;
+}
+
+}  // namespace qw

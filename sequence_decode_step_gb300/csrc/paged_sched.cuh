@@ -6,12 +6,13 @@
 // lengths live on the device, so every CTA forms the same prefix sums of the sequences' units
 // and finds its own start. The load is even to one key tile whatever the lengths are, and only the
 // items at a CTA's ends are split: at most two partial records per CTA, slot 2c for an item that
-// began in an earlier CTA and slot 2c + 1 for one that goes on in the next. The CTAs of a split
-// item count their arrivals at counters[first CTA]; the last one joins the records in CTA order,
-// so results do not depend on who is last.
+// began in an earlier CTA and slot 2c + 1 for one that goes on in the next. Records are joined in
+// CTA order, so results do not depend on which CTA is last: small ones by the last CTA to arrive
+// (counters[first CTA]), 128-row ones by a kernel of their own.
 //
 // The shared prefix is the same line with one pseudo-sequence: all the batch's tokens, every one
-// of which sees all prefix_len keys.
+// of which sees all prefix_len keys. Its records are not joined by its own launch: the launch over
+// the sequences' own keys adds them, row by row, to the rows it writes.
 #pragma once
 #include "paged.h"
 #include "qw_ptx.cuh"
@@ -220,20 +221,58 @@ __device__ __forceinline__ uint32_t paged_pack(float a, float b) {  // bf16, a i
   return r;
 }
 
-// Writes one float4 (columns d..d+3) of query row (token, head): the prefix's record in the
-// prefix pass, else the output after the prefix's record is joined; a row without a key is 0.
+// Adds records of slots c0 .. c1 (row r, columns 4 i4 ..) to acc, in CTA order.
+__device__ __forceinline__ void paged_join_slots(const PagedSlots& sl, int hd, int c0, int c1, int r,
+                                                 int d, PagedAcc& acc) {
+  float top = acc.m;
+  for (int x = c0; x <= c1; ++x)
+    top = fmaxf(top, __ldcg(sl.ml + (size_t)(2 * x + (x == c0)) * sl.rows + r).x);
+  const float mu = top == -INFINITY ? 0.f : top;
+  const float f = paged_exp2(acc.m - mu);
+  acc.m = top;
+  acc.l *= f, acc.o.x *= f, acc.o.y *= f, acc.o.z *= f, acc.o.w *= f;
+#pragma unroll 4
+  for (int x = c0; x <= c1; ++x) {
+    const size_t row = (size_t)(2 * x + (x == c0)) * sl.rows + r;
+    const float2 ml = __ldcg(sl.ml + row);
+    acc.add(paged_exp2(ml.x - mu), ml.y, __ldcg(reinterpret_cast<const float4*>(sl.o + row * hd + d)));
+  }
+}
+
+// Adds the prefix's record(s) of (token, head) to acc.
+__device__ __forceinline__ void paged_join_prefix(const PagedAttnArgs& a, int hd, int token, int head,
+                                                  int d, PagedAcc& acc) {
+  const PagedPrefix& p = a.pre;
+  const int end = min(max(__ldg(a.c.q_start + a.c.n_seqs), 0), a.n_tokens);
+  const int lo = min(max(__ldg(a.c.q_start), 0), end);
+  const int t = token - lo, nrt = (end - lo + p.tpt - 1) / p.tpt;
+  const int nkt = (a.c.prefix_len + p.kt - 1) / p.kt;
+  const int kvh = head / a.gq, rt = t / p.tpt;
+  const long long units = (long long)a.c.nkv * nrt * nkt;
+  const long long per = (units + p.grid - 1) / p.grid;
+  const long long begin = ((long long)kvh * nrt + rt) * nkt;
+  const int c0 = (int)(begin / per), c1 = (int)((begin + nkt - 1) / per);
+  if (c0 == c1) {
+    const size_t row = (size_t)token * a.nq + head;
+    const float2 ml = __ldcg(p.whole_ml + row);
+    acc.join(ml.x, ml.y, __ldcg(reinterpret_cast<const float4*>(p.whole_o + row * hd + d)));
+  } else {
+    paged_join_slots(p.slots, hd, c0, c1, (t - rt * p.tpt) * a.gq + (head - kvh * a.gq), d, acc);
+  }
+}
+
+// Writes one float4 (columns d..d+3) of query row (token, head): in the prefix pass the record of an
+// item that was not split, else the output after the prefix's records are joined; a row without
+// a key is 0.
 __device__ __forceinline__ void paged_emit(const PagedAttnArgs& a, int hd, int token, int head, int d,
                                            PagedAcc& acc) {
   const size_t row = (size_t)token * a.nq + head;
   if (a.prefix_pass) {
-    *reinterpret_cast<float4*>(a.pre_o + row * hd + d) = acc.o;
-    if (d == 0) a.pre_ml[row] = make_float2(acc.m, acc.l);
+    *reinterpret_cast<float4*>(a.pre.whole_o + row * hd + d) = acc.o;
+    if (d == 0) a.pre.whole_ml[row] = make_float2(acc.m, acc.l);
     return;
   }
-  if (a.pre_o) {
-    const float2 ml = __ldcg(a.pre_ml + row);
-    acc.join(ml.x, ml.y, __ldcg(reinterpret_cast<const float4*>(a.pre_o + row * hd + d)));
-  }
+  if (a.pre.whole_o) paged_join_prefix(a, hd, token, head, d, acc);
   const float inv = acc.l > 0.f || acc.l != acc.l ? 1.f / acc.l : 0.f;
   const float4 o = make_float4(acc.o.x * inv, acc.o.y * inv, acc.o.z * inv, acc.o.w * inv);
   if (a.act_bf16)

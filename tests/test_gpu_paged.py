@@ -120,6 +120,42 @@ def test_long_split_sequences(act, kv):
         assert torch.equal(c.attend(q), got)
 
 
+@pytest.mark.parametrize("act,kv", [("f32", "f32"), ("f32", "bf16"), ("bf16", "bf16")])
+@pytest.mark.parametrize("nq,nkv,hd,page", [(8, 2, 64, 16), (4, 2, 128, 64), (6, 2, 128, 32), (1, 1, 64, 256)])
+def test_long_chunks(act, kv, nq, nkv, hd, page):
+    # several row tiles per sequence, diagonals inside and across key tiles, short ones beside them
+    b = Batch([(300, 10), (129, 0), (1, 500), (64, 200), (0, 30), (2, 127)], nq, nkv, hd, page, act, kv,
+              seed=61)
+    c = b.cache()
+    got = c.attend(b.q.cuda(), max_new=300)
+    attend_close(b, got)
+    assert torch.equal(c.attend(b.q.cuda(), max_new=300), got)
+    c.check()
+
+
+@pytest.mark.parametrize("act,kv", [("f32", "f32"), ("f32", "bf16"), ("bf16", "bf16")])
+@pytest.mark.parametrize("nq,nkv,hd", [(16, 2, 64), (2, 1, 128)])
+def test_prefix_of_a_large_batch(act, kv, nq, nkv, hd):
+    # many row tiles share the prefix; most of its items are split over several CTAs
+    b = Batch([(1, i % 40) for i in range(100)] + [(0, 3), (3, 0)], nq, nkv, hd, 16, act, kv, prefix=1037,
+              pad=1, seed=67)
+    c = b.cache()
+    got = c.attend(b.q.cuda())
+    attend_close(b, got)
+    for _ in range(2):
+        assert torch.equal(c.attend(b.q.cuda())[:b.tokens], got[:b.tokens])
+    c.check()
+
+
+def test_chunk_of_one_long_sequence():
+    # few items, each split over many CTAs and joined by a kernel of its own
+    for act in ("f32", "bf16"):
+        b = Batch([(40, 2500)], 2, 1, 128, 64, act, "bf16", seed=71)
+        c = b.cache()
+        attend_close(b, c.attend(b.q.cuda(), max_new=40))
+        c.check()
+
+
 def test_padding_rows_are_left_and_strides():
     for act, kv in TYPES:
         b = Batch([(2, 9), (1, 40)], 4, 2, 64, 16, act, kv, pad=3, seed=13)
