@@ -48,14 +48,12 @@ struct PagedSlots {
   float2* ml;
   int rows;
 };
-// The prefix launch's results as the launch over the sequences' own keys finds them: an item
-// that one CTA did whole is in `whole` (a record per (token, query head)), a split one in the
-// slots of CTAs c0 .. c1, which follow from the launch's shape.
+// The prefix's record of every (token, query head): written by the prefix launch for items that one
+// CTA did whole and by the kernel that joins the records of split ones, read by the launch over the
+// sequences' own keys.
 struct PagedPrefix {
-  PagedSlots slots;
-  float* whole_o;      // [n_tokens][nq][hd], nullptr without a prefix
-  float2* whole_ml;    // [n_tokens][nq]
-  int tpt, kt, grid;   // tokens per row tile, keys per tile, CTAs
+  float* o;      // [n_tokens][nq][hd], nullptr without a prefix
+  float2* ml;    // [n_tokens][nq]
 };
 struct PagedSplit {    // a split item of a CTA, for the kernel that joins its records
   int c1;              // last CTA, -1: this CTA begins no split item
@@ -72,7 +70,7 @@ struct PagedAttnArgs {
   float scale_log2;         // log2(e) / sqrt(hd)
   PagedSlots slots;         // of this launch
   int* counters;            // [grid] arrivals of split items, 0 between launches
-  PagedSplit* splits;       // [grid] (kernels whose records a second kernel joins)
+  PagedSplit* splits;       // [grid], for the joining kernel (prefix and tensor-core launches)
   int prefix_pass;          // 1: this launch reads the prefix's keys
   PagedPrefix pre;
   uint64_t wait_ns;
@@ -92,6 +90,8 @@ cudaError_t set_paged_attributes();
 constexpr int kPagedTcKeys = 128;  // keys per tile
 int paged_tc_rows(bool act_bf16);  // query rows per item
 cudaError_t launch_paged_tc(const PagedAttnArgs& a, int hd, int grid, bool pdl, cudaStream_t s);
+// Joins the records of the items that the launch before it (`grid` CTAs) has split.
+cudaError_t launch_paged_join(const PagedAttnArgs& a, int hd, int grid, int item_rows, cudaStream_t s);
 cudaError_t set_paged_tc_attributes();
 
 }  // namespace qw

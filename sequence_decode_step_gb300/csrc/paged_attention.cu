@@ -78,23 +78,33 @@ __device__ __forceinline__ void produce(const PagedAttnArgs& a, const CUtensorMa
                                             : piece * prow * HD * ES);
   PagedCursor c = paged_cursor<KT>(a, st);
   int issued = 0;
-  bool ok = true;
+  bool ok = true, more = true;
   auto page_of = [&](const PagedCursor& x) {
     const int key = x.kt * KT + piece * prow;
     return key < x.limit ? paged_page(a, x.b, key) : -1;
   };
-  int page = c.u < c.u1 ? page_of(c) : -1;
-  while (c.u < c.u1) {
+  // the item's q rows (gq heads of a token lie together) into L1 for the consumers
+  auto fetch_q = [&](const PagedCursor& x) {
+    const int bytes = a.gq * HD * (a.act_bf16 ? 2 : 4), tok0 = x.rt * a.tpt;
+    const int lines = (bytes + 127) / 128, n = min(a.tpt, x.s.nb - tok0);
+    for (int i = lane; i < n * lines; i += 32) {
+      const char* p = static_cast<const char*>(a.q) +
+                      ((size_t)(x.s.lo + tok0 + i / lines) * a.ldq + (size_t)x.kvh * a.gq * HD) *
+                          (a.act_bf16 ? 2 : 4) + i % lines * 128;
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
+    }
+  };
+  int page = page_of(c);
+  while (more) {
     const int stage = issued % NS;
     const int key = c.kt * KT + piece * prow, kvh = c.kvh, now = page;
     const int pieces = min(np, (max(c.limit - c.kt * KT, 0) + prow - 1) / prow);
     // the next unit's pages, before waiting for this unit's stage
-    ++c.u;
-    ++c.kt;
-    if (c.u < c.u1) {
-      if (c.kt == c.nkt) c.next_item<KT>(a);
-      page = page_of(c);
+    if (++c.kt == c.kend) {
+      more = c.next<KT>(a);
+      if (more) fetch_q(c);
     }
+    if (more) page = page_of(c);
     if (issued >= NS && !mbar_wait(&empty[stage], (uint32_t)((issued / NS - 1) & 1), a.wait_ns)) {
       ok = false;
       break;
@@ -124,8 +134,8 @@ __device__ __forceinline__ void produce(const PagedAttnArgs& a, const CUtensorMa
 // a split one goes to this CTA's slot and the last CTA to arrive joins all of them in order.
 template <int HD, int R>
 __device__ __forceinline__ void finish_segment(const PagedAttnArgs& a, const PagedCursor& c,
-                                               bool first, bool whole, const float* join,
-                                               const float2* row_ml, int* flag) {
+                                               const float* join, const float2* row_ml,
+                                               int* flag) {
   const int tid = threadIdx.x;
   constexpr int V4 = HD / 4, N = R * V4;
   const int tok0 = c.rt * a.tpt, ntok = min(a.tpt, c.s.nb - tok0), rows = ntok * a.gq;
@@ -134,8 +144,8 @@ __device__ __forceinline__ void finish_segment(const PagedAttnArgs& a, const Pag
     const float4 y = *reinterpret_cast<const float4*>(join + R * HD + i * 4);
     return make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
   };
-  if (a.pre.whole_o && !a.prefix_pass) pdl_wait();  // the prefix's records, before any is read
-  if (whole) {
+  if (a.pre.o && !a.prefix_pass) pdl_wait();  // the prefix's records, before any is read
+  if (c.whole()) {
     for (int i = tid; i < N; i += kConsumers * 32) {
       const int r = i / V4;
       if (r >= rows) break;
@@ -147,13 +157,16 @@ __device__ __forceinline__ void finish_segment(const PagedAttnArgs& a, const Pag
     }
     return;
   }
-  const long long begin = c.u - c.kt;  // the item's first unit
-  const int c0 = (int)(begin / c.per), c1 = (int)((begin + c.nkt - 1) / c.per);
-  const size_t slot = (size_t)(2 * blockIdx.x + (first ? 1 : 0)) * a.slots.rows;
+  const int c0 = c.first_cta(), c1 = c.last_cta();
+  const size_t slot = (size_t)(2 * blockIdx.x + (c.first() ? 1 : 0)) * a.slots.rows;
   for (int i = tid; i < rows * V4; i += kConsumers * 32)
     __stcg(reinterpret_cast<float4*>(a.slots.o + slot * HD) + i, local(i));
   if (tid < rows) __stcg(a.slots.ml + slot + tid, row_ml[tid]);
-  if (a.prefix_pass) return;  // joined by the next launch
+  if (a.prefix_pass) {  // joined by the next launch
+    if (c.first() && tid == 0)
+      a.splits[blockIdx.x] = PagedSplit{c1, c.s.lo + tok0, rows, c.kvh * a.gq};
+    return;
+  }
   __threadfence();
   consumer_sync();
   if (tid == 0) {
@@ -167,7 +180,7 @@ __device__ __forceinline__ void finish_segment(const PagedAttnArgs& a, const Pag
     for (int i = tid; i < rows * V4; i += kConsumers * 32) {
       const int r = i / V4, d = (i % V4) * 4;
       PagedAcc acc;
-      paged_join_slots(a.slots, HD, c0, c1, r, d, acc);
+      paged_join_slots<HD>(a.slots, c0, c1, r, d, acc);
       paged_emit(a, HD, c.s.lo + tok0 + r / a.gq, c.kvh * a.gq + r % a.gq, d, acc);
     }
   }
@@ -186,10 +199,11 @@ __device__ __forceinline__ bool open_cta(const PagedAttnArgs& a, uint8_t* sm) {
       mbar_init(&empty[i], kConsumers);
     }
     fence_barrier_init();
+    if (a.prefix_pass) a.splits[blockIdx.x].c1 = -1;
   }
   if (a.prefix_pass) pdl_launch_dependents();
   paged_find_start<KT, kThreads>(a, st, reinterpret_cast<long long*>(sm + LY::off_start + 64));
-  return st->u < st->u1;
+  return st->any;
 }
 
 // Join of the four warps: common maximum per row, then the weights every warp scales its o with.
@@ -283,9 +297,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   PagedCursor c = paged_cursor<KT>(a, st);
   int seen = 0;      // tiles taken from the ring
   bool bad = false;  // a wait gave up: no more waits, the barriers are still kept
-  while (c.u < c.u1) {
-    const int n = (int)min((long long)(c.nkt - c.kt), c.u1 - c.u);
-    const bool first = c.kt == 0, whole = first && n == c.nkt;
+  do {
+    const int n = c.kend - c.kt;
     const int tok0 = c.rt * a.tpt, rows = min(a.tpt, c.s.nb - tok0) * a.gq;
     // q as A fragments: rows g (and g + 8), columns 16 ks + q2 + {0, 1} (and + 8)
     uint32_t qa[KS][4], ql[NT == 3 ? KS : 1][2];
@@ -444,12 +457,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     consumer_sync();
     if (warp < 2) put(true);
     consumer_sync();
-    finish_segment<HD, R>(a, c, first, whole, join, row_ml, flag);
+    finish_segment<HD, R>(a, c, join, row_ml, flag);
     consumer_sync();  // join and row_ml are free again
-    c.u += n;
-    c.kt += n;
-    if (c.u < c.u1) c.next_item<KT>(a);
-  }
+  } while (c.next<KT>(a));
   if (bad && lane == 0 && a.c.status) atomicOr(a.c.status, PG_TIMEOUT);
 }
 
@@ -496,9 +506,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   PagedCursor c = paged_cursor<KT>(a, st);
   int seen = 0;
   bool bad = false;
-  while (c.u < c.u1) {
-    const int n = (int)min((long long)(c.nkt - c.kt), c.u1 - c.u);
-    const bool first = c.kt == 0, whole = first && n == c.nkt;
+  do {
+    const int n = c.kend - c.kt;
     const int tok0 = c.rt * a.tpt, rows = min(a.tpt, c.s.nb - tok0) * a.gq;
     float q[R][E], o[R][E], m[R], l[R];
     int lim[R];
@@ -598,12 +607,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     consumer_sync();
     if (warp < 2) put(true);
     consumer_sync();
-    finish_segment<HD, R>(a, c, first, whole, join, row_ml, flag);
+    finish_segment<HD, R>(a, c, join, row_ml, flag);
     consumer_sync();
-    c.u += n;
-    c.kt += n;
-    if (c.u < c.u1) c.next_item<KT>(a);
-  }
+  } while (c.next<KT>(a));
   if (bad && lane == 0 && a.c.status) atomicOr(a.c.status, PG_TIMEOUT);
 }
 
@@ -671,12 +677,13 @@ int slot_rows(int n_tokens) {
   return std::max(16, (int)std::min<long long>(kMaxRows, (8LL * n_tokens + 15) / 16 * 16));
 }
 struct Workspace {
-  size_t counters = 0, splits, ml[2], o[2], whole_ml, whole_o, total;
+  size_t counters = 0, splits[2], ml[2], o[2], whole_ml, whole_o, total;
   Workspace(int n_tokens, int nq, int hd, bool prefix) {
     // an item of more than 16 rows belongs to one CTA per SM, smaller ones to two
     const size_t rows = (size_t)2 * std::max(kMaxSms * slot_rows(n_tokens), 2 * kMaxSms * 16);
-    splits = align256(2 * kMaxSms * 4);
-    size_t at = splits + align256(2 * kMaxSms * sizeof(PagedSplit));
+    splits[0] = align256(2 * kMaxSms * 4);
+    splits[1] = splits[0] + align256(2 * kMaxSms * sizeof(PagedSplit));
+    size_t at = splits[1] + align256(2 * kMaxSms * sizeof(PagedSplit));
     for (int i = 0; i < (prefix ? 2 : 1); ++i) {
       ml[i] = at;
       o[i] = at + align256(rows * 8);
@@ -724,9 +731,9 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& base, int hd, int max_ne
   const Workspace w(a.n_tokens, a.nq, hd, prefix);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.counters = reinterpret_cast<int*>(ws);
-  a.splits = reinterpret_cast<PagedSplit*>(ws + w.splits);
   auto run = [&](const PagedPlan& p, int i, bool pdl) {
     a.tpt = p.rows > 128 ? 2 * (128 / a.gq) : p.rows / a.gq;
+    a.splits = reinterpret_cast<PagedSplit*>(ws + w.splits[i]);
     a.slots.ml = reinterpret_cast<float2*>(ws + w.ml[i]);
     a.slots.o = reinterpret_cast<float*>(ws + w.o[i]);
     a.slots.rows = p.tc ? slot_rows(a.n_tokens) : p.rows;
@@ -734,17 +741,14 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& base, int hd, int max_ne
   };
   const long long cap = 1 << 20;  // row counts only choose a kernel
   if (prefix) {
-    a.pre.whole_ml = reinterpret_cast<float2*>(ws + w.whole_ml);
-    a.pre.whole_o = reinterpret_cast<float*>(ws + w.whole_o);
+    a.pre.ml = reinterpret_cast<float2*>(ws + w.whole_ml);
+    a.pre.o = reinterpret_cast<float*>(ws + w.whole_o);
     a.prefix_pass = 1;
     const PagedPlan p = plan_paged_pass(a, hd, (int)std::min(cap, (long long)a.n_tokens * a.gq), sms);
-    const cudaError_t e = run(p, 1, false);
+    cudaError_t e = run(p, 1, false);
+    if (e == cudaSuccess) e = launch_paged_join(a, hd, p.grid, p.rows, s);
     if (e != cudaSuccess) return e;
     a.prefix_pass = 0;
-    a.pre.slots = a.slots;
-    a.pre.tpt = a.tpt;
-    a.pre.kt = p.kt;
-    a.pre.grid = p.grid;
   }
   const int rows = (int)std::min(cap, (long long)std::min(max_new, a.n_tokens) * a.gq);
   return run(plan_paged_pass(a, hd, rows, sms), 0, prefix);

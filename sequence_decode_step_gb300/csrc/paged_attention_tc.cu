@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
     }
     mbar_init(done, 1);
     fence_barrier_init();
-    if (!a.prefix_pass) a.splits[blockIdx.x].c1 = -1;
+    a.splits[blockIdx.x].c1 = -1;
   }
   if (warp == 1) {
     tmem_alloc(tslot, 512);
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
   tc_fence_after();
   const uint32_t tb = *tslot;
   const int half = 128 / a.gq;  // tokens of a row tile
-  const bool idle = st->u >= st->u1;
+  const bool idle = !st->any;
 
   if (idle) {
   } else if (warp == 0) {
@@ -131,16 +131,12 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
       return key < x.limit ? paged_page(a, x.b, key) : -1;
     };
     int page = page_of(c), issued = 0;
-    bool ok = true;
-    while (ok && c.u < c.u1) {
+    bool ok = true, more = true;
+    while (ok && more) {
       const int key = c.kt * KT + piece * prow, kvh = c.kvh, now = page;
       const int pieces = min(np, (max(c.limit - c.kt * KT, 0) + prow - 1) / prow);
-      ++c.u;
-      ++c.kt;
-      if (c.u < c.u1) {
-        if (c.kt == c.nkt) c.next_item<KT>(a);
-        page = page_of(c);
-      }
+      if (++c.kt == c.kend) more = c.next<KT>(a);
+      if (more) page = page_of(c);
 #pragma unroll 1
       for (int t = 0; t < 2; ++t) {
         const int slot = issued % NS;
@@ -186,8 +182,8 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
       auto kv_wait = [&](int use) { return wait(&kv_full[use % NS], use / NS); };
       auto slot_at = [&](int use) { return ring + (uint32_t)(use % NS) * LY::kTile; };
       bool ok = true;
-      while (ok && c.u < c.u1) {
-        const int n = (int)min((long long)(c.nkt - c.kt), c.u1 - c.u);
+      do {
+        const int n = c.kend - c.kt;
         const bool two = NT == 1 && c.s.nb - c.rt * a.tpt > half;  // the second stream has rows
         ok = wait(q_full, items) && kv_wait(2 * tiles);
         if (!ok) break;
@@ -257,10 +253,7 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
         }
         tiles += n;
         ++items;
-        c.u += n;
-        c.kt += n;
-        if (c.u < c.u1) c.next_item<KT>(a);
-      }
+      } while (ok && c.next<KT>(a));
       if (!ok && a.c.status) atomicOr(a.c.status, PG_TIMEOUT);
       // TMEM is released only after every MMA issued here has finished
       tc_commit(done);
@@ -277,9 +270,9 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
     auto wait = [&](uint64_t* bar, int n) {
       if (!bad) bad = !__all_sync(0xffffffffu, wait_for(bar, n, a.wait_ns));
     };
-    while (c.u < c.u1) {
-      const int n = (int)min((long long)(c.nkt - c.kt), c.u1 - c.u);
-      const bool first = c.kt == 0, whole = first && n == c.nkt;
+    do {
+      const int n = c.kend - c.kt;
+      const bool first = c.first(), whole = c.whole();
       const int tok0 = c.rt * a.tpt + s * half;              // of this stream's row tile
       const int ntok = min(max(c.s.nb - tok0, 0), half), rows = ntok * a.gq;
       const bool live = r < rows;
@@ -439,7 +432,7 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
         else
           wait(&o_full[0], tiles + n - 1);
         tc_fence_after();
-        if (whole && a.pre.whole_o && !a.prefix_pass) pdl_wait();  // the prefix's records
+        if (whole && a.pre.o && !a.prefix_pass) pdl_wait();  // the prefix's records
         const size_t slot = (size_t)(2 * blockIdx.x + (first ? 1 : 0)) * a.slots.rows + s * half * a.gq + r;
 #pragma unroll 1
         for (int d = 0; d < HD; d += 16) {
@@ -464,16 +457,11 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
         if (live && !whole) a.slots.ml[slot] = make_float2(m, l);
         tc_fence_before();
       }
-      if (!whole && first && s == 0 && r == 0 && !a.prefix_pass) {  // the joining kernel's work
-        const long long begin = c.u - c.kt;
-        a.splits[blockIdx.x] = PagedSplit{(int)((begin + c.nkt - 1) / c.per), c.s.lo + c.rt * a.tpt,
+      if (!whole && first && s == 0 && r == 0)  // the joining kernel's work
+        a.splits[blockIdx.x] = PagedSplit{c.last_cta(), c.s.lo + c.rt * a.tpt,
                                           min(a.tpt, c.s.nb - c.rt * a.tpt) * a.gq, c.kvh * a.gq};
-      }
       tiles += n;
-      c.u += n;
-      c.kt += n;
-      if (c.u < c.u1) c.next_item<KT>(a);
-    }
+    } while (c.next<KT>(a));
     if (bad && lane == 0 && a.c.status) atomicOr(a.c.status, PG_TIMEOUT);
   }
   tc_fence_before();
@@ -485,20 +473,19 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
   pdl_wait();
 }
 
-// Joins the records of the items that a launch split: CTA (x, y) takes rows y, y + gridDim.y, ..
-// (4 at a time) of the item that begins in CTA x.
+// Joins the records of the items that a launch split: CTA (x, y) takes the 4 rows from 4 y on (8
+// with head_dim 64) of the item that begins in CTA x, a row by hd/4 lanes.
 template <int HD>
-__global__ void __launch_bounds__(HD) paged_join_kernel(const __grid_constant__ PagedAttnArgs a) {
-  constexpr int V4 = HD / 4;  // threads of a row
+__global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedAttnArgs a) {
+  constexpr int V4 = HD / 4, RB = 128 / V4;
+  if (a.prefix_pass) pdl_launch_dependents();
   pdl_wait();
   const PagedSplit sp = a.splits[blockIdx.x];
-  if (sp.c1 < 0) return;
-  const int d = threadIdx.x % V4 * 4;
-  for (int r = blockIdx.y * 4 + threadIdx.x / V4; r < sp.rows; r += gridDim.y * 4) {
-    PagedAcc acc;
-    paged_join_slots(a.slots, HD, blockIdx.x, sp.c1, r, d, acc);
-    paged_emit(a, HD, sp.token + r / a.gq, sp.head + r % a.gq, d, acc);
-  }
+  const int r = blockIdx.y * RB + threadIdx.x / V4, d = threadIdx.x % V4 * 4;
+  if (sp.c1 < 0 || r >= sp.rows) return;
+  PagedAcc acc;
+  paged_join_slots<HD>(a.slots, blockIdx.x, sp.c1, r, d, acc);
+  paged_emit(a, HD, sp.token + r / a.gq, sp.head + r % a.gq, d, acc);
 }
 
 template <class... P, class... Args>
@@ -527,8 +514,7 @@ cudaError_t launch_tc(const PagedAttnArgs& a, int grid, bool pdl, cudaStream_t s
     return cudaErrorInvalidValue;
   cudaError_t e = launch(paged_attn_tc_kernel<HD, NT>, dim3(grid), TcLayout<HD, NT>::kThreads,
                          TcLayout<HD, NT>::bytes, pdl, s, a, tk, tv);
-  if (e == cudaSuccess && !a.prefix_pass)
-    e = launch(paged_join_kernel<HD>, dim3(grid, 8), HD, 0, false, s, a);
+  if (e == cudaSuccess && !a.prefix_pass) e = launch_paged_join(a, HD, grid, paged_tc_rows(NT == 1), s);
   return e;
 }
 template <int HD>
@@ -549,6 +535,13 @@ int paged_tc_rows(bool act_bf16) { return act_bf16 ? 256 : 128; }
 cudaError_t launch_paged_tc(const PagedAttnArgs& a, int hd, int grid, bool pdl, cudaStream_t s) {
   if (hd == 64) return a.act_bf16 ? launch_tc<64, 1>(a, grid, pdl, s) : launch_tc<64, 3>(a, grid, pdl, s);
   return a.act_bf16 ? launch_tc<128, 1>(a, grid, pdl, s) : launch_tc<128, 3>(a, grid, pdl, s);
+}
+
+cudaError_t launch_paged_join(const PagedAttnArgs& a, int hd, int grid, int item_rows, cudaStream_t s) {
+  const int rb = 512 / hd;  // rows of a CTA
+  const dim3 g(grid, (std::min(item_rows, a.slots.rows) + rb - 1) / rb);
+  return hd == 64 ? launch(paged_join_kernel<64>, g, 128, 0, true, s, a)
+                  : launch(paged_join_kernel<128>, g, 128, 0, true, s, a);
 }
 
 cudaError_t set_paged_tc_attributes() {

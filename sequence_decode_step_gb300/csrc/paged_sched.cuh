@@ -7,17 +7,29 @@
 // and finds its own start. The load is even to one key tile whatever the lengths are, and only the
 // items at a CTA's ends are split: at most two partial records per CTA, slot 2c for an item that
 // began in an earlier CTA and slot 2c + 1 for one that goes on in the next. Records are joined in
-// CTA order, so results do not depend on which CTA is last: small ones by the last CTA to arrive
-// (counters[first CTA]), 128-row ones by a kernel of their own.
+// CTA order, so results do not depend on which CTA is last: those of a decode step's launch by the
+// last CTA to arrive (counters[first CTA]), those of a prefix or of tensor-core tiles by a kernel
+// of their own (many rows: one CTA would read them for 5-10 us).
+//
+// An item costs a CTA about kPagedItemUnits tiles beside its keys (q, the join, the output), so on
+// the line it is that much longer; the units before its first tile are empty.
 //
 // The shared prefix is the same line with one pseudo-sequence: all the batch's tokens, every one
-// of which sees all prefix_len keys. Its records are not joined by its own launch: the launch over
-// the sequences' own keys adds them, row by row, to the rows it writes.
+// of which sees all prefix_len keys.
 #pragma once
 #include "paged.h"
 #include "qw_ptx.cuh"
 
 namespace qw {
+
+constexpr int kPagedItemUnits = 1;
+constexpr int kPagedLeastUnits = 2;  // least share of a CTA: fewer records of a short line to join
+
+// Quotient of two line positions: 32-bit where both fit, as they do for any real batch.
+__device__ __forceinline__ long long paged_div(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
 
 struct PagedSeq {  // one sequence's share of the line
   int lo, nb;      // first token row and tokens
@@ -58,24 +70,35 @@ __device__ __forceinline__ int paged_tiles(int limit) {
 template <int KT>
 __device__ __forceinline__ long long paged_head_units(const PagedAttnArgs& a, const PagedSeq& s) {
   long long n = 0;
-  for (int rt = 0; rt < s.nrt; ++rt) n += paged_tiles<KT>(paged_limit(a, s, rt));
+  for (int rt = 0; rt < s.nrt; ++rt) n += kPagedItemUnits + paged_tiles<KT>(paged_limit(a, s, rt));
   return n;
 }
 
 struct PagedCursor {  // a place on the line
-  long long u, u1, per;
-  int b, kvh, rt, kt;  // current item and key tile
-  int nkt, limit;      // of the current item
+  long long item, u1, per;  // the current item's first unit; end of the CTA's share
+  int b, kvh, rt;           // current item
+  int kt, kend;             // this CTA's tiles of it
+  int nkt, limit;           // all its tiles; its keys
   PagedSeq s;
 
+  __device__ __forceinline__ bool first() const { return kt == 0; }
+  __device__ __forceinline__ bool whole() const { return kt == 0 && kend == nkt; }
+  // CTAs that share the item's tiles
+  __device__ __forceinline__ int first_cta() const { return (int)paged_div(item + kPagedItemUnits, per); }
+  __device__ __forceinline__ int last_cta() const {
+    return (int)paged_div(item + kPagedItemUnits + nkt - 1, per);
+  }
   template <int KT>
   __device__ __forceinline__ void enter(const PagedAttnArgs& a) {
     limit = paged_limit(a, s, rt);
     nkt = paged_tiles<KT>(limit);
+    kend = (int)min((long long)nkt, u1 - item - kPagedItemUnits);
   }
-  // To the next item (only called while u < u1, so there is one).
+  // To the CTA's next item; false when its share ends before that item's first tile.
   template <int KT>
-  __device__ __forceinline__ void next_item(const PagedAttnArgs& a) {
+  __device__ __forceinline__ bool next(const PagedAttnArgs& a) {
+    item += kPagedItemUnits + nkt;
+    if (item + kPagedItemUnits >= u1) return false;
     kt = 0;
     if (++rt == s.nrt) {
       rt = 0;
@@ -86,15 +109,17 @@ struct PagedCursor {  // a place on the line
       }
     }
     enter<KT>(a);
+    return true;
   }
 };
 
 struct PagedStart {  // in shared memory: where this CTA starts
-  long long u, u1, per;
+  long long item, u1, per;
   int b, kvh, rt, kt;
+  int any;           // 0: nothing to do
 };
 
-// Block-wide: fills *st (st->u >= st->u1: nothing to do). warp_sums: one long long per warp.
+// Block-wide: fills *st. warp_sums: one long long per warp.
 template <int KT, int THREADS>
 __device__ void paged_find_start(const PagedAttnArgs& a, PagedStart* st, long long* warp_sums) {
   constexpr int W = THREADS / 32;
@@ -114,7 +139,7 @@ __device__ void paged_find_start(const PagedAttnArgs& a, PagedStart* st, long lo
     if (lane >= o) scan += v;
   }
   if (lane == 31) warp_sums[warp] = scan;
-  if (threadIdx.x == 0) st->u = 0, st->u1 = 0;
+  if (threadIdx.x == 0) st->any = 0;
   __syncthreads();
   long long before = scan - mine, total = 0;
 #pragma unroll
@@ -122,7 +147,7 @@ __device__ void paged_find_start(const PagedAttnArgs& a, PagedStart* st, long lo
     if (w < warp) before += warp_sums[w];
     total += warp_sums[w];
   }
-  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  const long long per = max(paged_div(total + gridDim.x - 1, gridDim.x), (long long)kPagedLeastUnits);
   const long long u0 = per * blockIdx.x;
   if (u0 < total && before <= u0 && u0 < before + mine) {
     long long r = u0 - before;
@@ -134,21 +159,22 @@ __device__ void paged_find_start(const PagedAttnArgs& a, PagedStart* st, long lo
       s = paged_seq(a, ++b);
       hu = paged_head_units<KT>(a, s);
     }
-    const int kvh = (int)(r / hu);
+    const int kvh = (int)paged_div(r, hu);
     r -= hu * kvh;
     int rt = 0;
     for (;; ++rt) {
-      const int t = paged_tiles<KT>(paged_limit(a, s, rt));
+      const int t = kPagedItemUnits + paged_tiles<KT>(paged_limit(a, s, rt));
       if (r < t) break;
       r -= t;
     }
-    st->u = u0;
+    st->item = u0 - r;
     st->u1 = min(u0 + per, total);
     st->per = per;
     st->b = b;
     st->kvh = kvh;
     st->rt = rt;
-    st->kt = (int)r;
+    st->kt = max((int)r - kPagedItemUnits, 0);
+    st->any = u0 - r + kPagedItemUnits < st->u1;  // the share has a tile
   }
   __syncthreads();
 }
@@ -156,17 +182,15 @@ __device__ void paged_find_start(const PagedAttnArgs& a, PagedStart* st, long lo
 template <int KT>
 __device__ __forceinline__ PagedCursor paged_cursor(const PagedAttnArgs& a, const PagedStart* st) {
   PagedCursor c;
-  c.u = st->u;
+  c.item = st->item;
   c.u1 = st->u1;
-  if (c.u < c.u1) {
-    c.per = st->per;
-    c.b = st->b;
-    c.kvh = st->kvh;
-    c.rt = st->rt;
-    c.kt = st->kt;
-    c.s = paged_seq(a, c.b);
-    c.enter<KT>(a);
-  }
+  c.per = st->per;
+  c.b = st->b;
+  c.kvh = st->kvh;
+  c.rt = st->rt;
+  c.kt = st->kt;
+  c.s = paged_seq(a, c.b);
+  c.enter<KT>(a);
   return c;
 }
 
@@ -221,58 +245,52 @@ __device__ __forceinline__ uint32_t paged_pack(float a, float b) {  // bf16, a i
   return r;
 }
 
-// Adds records of slots c0 .. c1 (row r, columns 4 i4 ..) to acc, in CTA order.
-__device__ __forceinline__ void paged_join_slots(const PagedSlots& sl, int hd, int c0, int c1, int r,
-                                                 int d, PagedAcc& acc) {
-  float top = acc.m;
-  for (int x = c0; x <= c1; ++x)
-    top = fmaxf(top, __ldcg(sl.ml + (size_t)(2 * x + (x == c0)) * sl.rows + r).x);
-  const float mu = top == -INFINITY ? 0.f : top;
-  const float f = paged_exp2(acc.m - mu);
-  acc.m = top;
-  acc.l *= f, acc.o.x *= f, acc.o.y *= f, acc.o.z *= f, acc.o.w *= f;
-#pragma unroll 4
-  for (int x = c0; x <= c1; ++x) {
-    const size_t row = (size_t)(2 * x + (x == c0)) * sl.rows + r;
-    const float2 ml = __ldcg(sl.ml + row);
-    acc.add(paged_exp2(ml.x - mu), ml.y, __ldcg(reinterpret_cast<const float4*>(sl.o + row * hd + d)));
+// Adds records c0 .. c1 of row r to acc (columns d .. d+3 of hd), in CTA order. The hd/4 lanes of a
+// row call it together: each loads the statistics of some records, the weights go round by
+// shuffles, and the records' loads are independent.
+template <int HD>
+__device__ __forceinline__ void paged_join_slots(const PagedSlots& sl, int c0, int c1, int r, int d,
+                                                 PagedAcc& acc) {
+  constexpr int W = HD / 4;  // lanes of a row: a warp or half of one
+  const int lane = threadIdx.x & 31, sub = lane % W;
+  const unsigned mask = W == 32 ? 0xffffffffu : 0xffffu << (lane / W * W);
+  for (int x0 = c0; x0 <= c1; x0 += W) {
+    const int x = x0 + sub, n = min(W, c1 + 1 - x0);
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (sub < n) ml = __ldcg(sl.ml + (size_t)(2 * x + (x == c0)) * sl.rows + r);
+    float top = ml.x;
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(mask, top, o));
+    top = fmaxf(top, acc.m);
+    const float mu = top == -INFINITY ? 0.f : top;
+    const float f = paged_exp2(acc.m - mu);
+    acc.m = top;
+    acc.l *= f, acc.o.x *= f, acc.o.y *= f, acc.o.z *= f, acc.o.w *= f;
+    const float w = paged_exp2(ml.x - mu), wl = ml.y;
+    const float4* o = reinterpret_cast<const float4*>(sl.o + ((size_t)2 * x0 * sl.rows + r) * HD + d);
+    const size_t step = (size_t)2 * sl.rows * (HD / 4);
+    const size_t skip = (size_t)sl.rows * (HD / 4);  // the first record is in its CTA's other slot
+#pragma unroll 8
+    for (int i = 0; i < n; ++i)
+      acc.add(__shfl_sync(mask, w, i, W), __shfl_sync(mask, wl, i, W),
+              __ldcg(o + i * step + (x0 + i == c0 ? skip : 0)));
   }
 }
 
-// Adds the prefix's record(s) of (token, head) to acc.
-__device__ __forceinline__ void paged_join_prefix(const PagedAttnArgs& a, int hd, int token, int head,
-                                                  int d, PagedAcc& acc) {
-  const PagedPrefix& p = a.pre;
-  const int end = min(max(__ldg(a.c.q_start + a.c.n_seqs), 0), a.n_tokens);
-  const int lo = min(max(__ldg(a.c.q_start), 0), end);
-  const int t = token - lo, nrt = (end - lo + p.tpt - 1) / p.tpt;
-  const int nkt = (a.c.prefix_len + p.kt - 1) / p.kt;
-  const int kvh = head / a.gq, rt = t / p.tpt;
-  const long long units = (long long)a.c.nkv * nrt * nkt;
-  const long long per = (units + p.grid - 1) / p.grid;
-  const long long begin = ((long long)kvh * nrt + rt) * nkt;
-  const int c0 = (int)(begin / per), c1 = (int)((begin + nkt - 1) / per);
-  if (c0 == c1) {
-    const size_t row = (size_t)token * a.nq + head;
-    const float2 ml = __ldcg(p.whole_ml + row);
-    acc.join(ml.x, ml.y, __ldcg(reinterpret_cast<const float4*>(p.whole_o + row * hd + d)));
-  } else {
-    paged_join_slots(p.slots, hd, c0, c1, (t - rt * p.tpt) * a.gq + (head - kvh * a.gq), d, acc);
-  }
-}
-
-// Writes one float4 (columns d..d+3) of query row (token, head): in the prefix pass the record of an
-// item that was not split, else the output after the prefix's records are joined; a row without
-// a key is 0.
+// Writes one float4 (columns d..d+3) of query row (token, head): the prefix's record in its
+// launches, else the output after that record is joined; a row without a key is 0.
 __device__ __forceinline__ void paged_emit(const PagedAttnArgs& a, int hd, int token, int head, int d,
                                            PagedAcc& acc) {
   const size_t row = (size_t)token * a.nq + head;
   if (a.prefix_pass) {
-    *reinterpret_cast<float4*>(a.pre.whole_o + row * hd + d) = acc.o;
-    if (d == 0) a.pre.whole_ml[row] = make_float2(acc.m, acc.l);
+    *reinterpret_cast<float4*>(a.pre.o + row * hd + d) = acc.o;
+    if (d == 0) a.pre.ml[row] = make_float2(acc.m, acc.l);
     return;
   }
-  if (a.pre.whole_o) paged_join_prefix(a, hd, token, head, d, acc);
+  if (a.pre.o) {
+    const float2 ml = __ldcg(a.pre.ml + row);
+    acc.join(ml.x, ml.y, __ldcg(reinterpret_cast<const float4*>(a.pre.o + row * hd + d)));
+  }
   const float inv = acc.l > 0.f || acc.l != acc.l ? 1.f / acc.l : 0.f;
   const float4 o = make_float4(acc.o.x * inv, acc.o.y * inv, acc.o.z * inv, acc.o.w * inv);
   if (a.act_bf16)
