@@ -132,7 +132,7 @@ __device__ __forceinline__ void produce(const PagedAttnArgs& a, const CUtensorMa
 // ------------------------------------------------------------------ end of an item's segment
 // The four warps' records are in join[0] + join[1] (o) and row_ml (m, l). A whole item is emitted;
 // a split one goes to this CTA's slot and the last CTA to arrive joins all of them in order.
-template <int HD, int R>
+template <int HD, int KT, int R>
 __device__ __forceinline__ void finish_segment(const PagedAttnArgs& a, const PagedCursor& c,
                                                const float* join, const float2* row_ml,
                                                int* flag) {
@@ -157,7 +157,7 @@ __device__ __forceinline__ void finish_segment(const PagedAttnArgs& a, const Pag
     }
     return;
   }
-  const int c0 = c.first_cta(), c1 = c.last_cta();
+  const int c0 = c.first_cta<KT>(), c1 = c.last_cta<KT>();
   const size_t slot = (size_t)(2 * blockIdx.x + (c.first() ? 1 : 0)) * a.slots.rows;
   for (int i = tid; i < rows * V4; i += kConsumers * 32)
     __stcg(reinterpret_cast<float4*>(a.slots.o + slot * HD) + i, local(i));
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     consumer_sync();
     if (warp < 2) put(true);
     consumer_sync();
-    finish_segment<HD, R>(a, c, join, row_ml, flag);
+    finish_segment<HD, KT, R>(a, c, join, row_ml, flag);
     consumer_sync();  // join and row_ml are free again
   } while (c.next<KT>(a));
   if (bad && lane == 0 && a.c.status) atomicOr(a.c.status, PG_TIMEOUT);
@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     consumer_sync();
     if (warp < 2) put(true);
     consumer_sync();
-    finish_segment<HD, R>(a, c, join, row_ml, flag);
+    finish_segment<HD, KT, R>(a, c, join, row_ml, flag);
     consumer_sync();
   } while (c.next<KT>(a));
   if (bad && lane == 0 && a.c.status) atomicOr(a.c.status, PG_TIMEOUT);

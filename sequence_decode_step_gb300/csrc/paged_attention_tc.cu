@@ -16,7 +16,7 @@
 // f32 activations (NT = 3): q and P as three bf16 terms each (24 bits, f32 results), six products
 // per tile, one stream with two S buffers; the tensor core is the bound by itself.
 //
-// Warps: 0 page look-up and TMA, 1 MMA issue, 4-7 (and 8-11) softmax; TMEM is S/P and O:
+// Warps: 0 page look-up and TMA, 1 MMA issue, 2-5 (and 6-9) softmax; TMEM is S/P and O:
 //   NT = 1: S_A, S_B (128 columns each), O_A, O_B
 //   NT = 3: S_0, S_1, O, X_0, X_1 (64 each); P's first two terms overwrite S_i, the third is in X_i
 // Work is shared as in paged_sched.cuh with one CTA per SM (its tiles fill the shared memory).
@@ -49,10 +49,27 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, int phase, uint64_t limi
   }
 }
 
+// Two f32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(const float2& a, const float2& b, const float2& c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)),
+        "l"(*reinterpret_cast<const uint64_t*>(&c)));
+  return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 add2(const float2& a, const float2& b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&r);
+}
+
 template <int HD, int NT>
 struct TcLayout {
   static constexpr int kStreams = NT == 1 ? 2 : 1;
-  static constexpr int kThreads = 128 + 128 * kStreams;
+  static constexpr int kThreads = 64 + 128 * kStreams;
   static constexpr uint32_t kQ1 = 128 * HD * 2;            // one term of a stream's q tile
   static constexpr uint32_t kQ = kQ1 * (NT == 1 ? 2 : 3);
   static constexpr uint32_t kTile = KT * HD * 2;           // a K or V tile
@@ -60,7 +77,7 @@ struct TcLayout {
   static constexpr uint32_t off_ring = kQ;
   static constexpr uint32_t off_start = off_ring + kSlots * kTile;
   static constexpr uint32_t off_bar = off_start + 64 + 128;
-  static constexpr int kBars = 2 * kSlots + 8;
+  static constexpr int kBars = 2 * kSlots + 10;
   static constexpr uint32_t off_tmem = off_bar + kBars * 8;
   static constexpr uint32_t bytes = off_tmem + 16;
   static constexpr uint32_t t_o = 256, t_x = 384;          // TMEM columns (t_x: NT = 3)
@@ -86,7 +103,8 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
   uint64_t* q_full = kv_empty + NS;
   uint64_t* s_full = q_full + 1;   // NT = 1: of each stream; NT = 3: of each S buffer
   uint64_t* p_full = s_full + 2;   // NT = 1: of each stream; NT = 3: p_full[0]
-  uint64_t* o_full = p_full + 2;   // NT = 1: the end of an item, of each stream; NT = 3: every tile
+  uint64_t* p_half = p_full + 2;   // NT = 1: the first 64 keys' weights of each stream
+  uint64_t* o_full = p_half + 2;   // NT = 1: the end of an item, of each stream; NT = 3: every tile
   uint64_t* done = o_full + 2;     // every MMA of this CTA has finished
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + LY::off_tmem);
   PagedStart* st = reinterpret_cast<PagedStart*>(sm + LY::off_start);
@@ -96,12 +114,13 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&kv_full[i], 1);
-      mbar_init(&kv_empty[i], 1);
+      mbar_init(&kv_empty[i], NT == 1 ? 2 : 1);  // the streams' softmax warps, or a commit
     }
     mbar_init(q_full, 4 * ST);  // one arrival per softmax warp
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
+      mbar_init(&p_half[i], 4);
       mbar_init(&o_full[i], 1);
     }
     mbar_init(done, 1);
@@ -158,110 +177,132 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
     for (int i = max(0, issued - NS); i < issued; ++i)  // the copies have landed
       wait_for(&kv_full[i % NS], i / NS, kDrainNs);
   } else if (warp == 1) {
-    // ---- MMA issue
-    if (lane == 0) {
-      constexpr uint32_t id_s = idesc_bf16_f32(128, KT);
-      constexpr uint32_t id_o = idesc_bf16_f32(128, HD) | kIdescBMnMajor;
-      const uint32_t qs = smem_addr(sm), ring = smem_addr(sm + LY::off_ring);
-      auto issue_s = [&](uint32_t q, uint32_t k, uint32_t d) {  // d = q . k^T (all terms of q)
+    // ---- MMA issue: the whole warp walks in step, so that addresses and descriptors live in uniform
+    // registers, and one elected lane issues. The queue behind it is short, so every wait, fence and
+    // commit between two groups of MMAs costs the tensor core 50-100 cycles: a stream's turn has
+    // few of them, and the tiles' slots are given back by the softmax warps. The MMAs of a group are
+    // unrolled: a rolled loop takes 82 cycles for each, the tensor core 64
+    constexpr uint32_t id_s = idesc_bf16_f32(128, KT);
+    constexpr uint32_t id_o = idesc_bf16_f32(128, HD) | kIdescBMnMajor;
+    const uint32_t tm = __shfl_sync(0xffffffffu, tb, 0);
+    const bool lead = elect_one();
+    // operand descriptors of the first k-step; a step adds to the address field (16-byte units)
+    const uint64_t dq = sw128_kmajor_desc(smem_addr(sm));
+    const uint64_t dk = sw128_kmajor_desc(smem_addr(sm + LY::off_ring));
+    const uint64_t dv = sw128_mnmajor_desc(smem_addr(sm + LY::off_ring), KT * 128);
+    auto slot_at = [&](int use) { return (uint64_t)((uint32_t)(use % NS) * (LY::kTile >> 4)); };
+    auto issue_s = [&](uint64_t q, uint64_t k, uint32_t d) {  // d = q . k^T (all terms of q)
+      if (lead) {
 #pragma unroll
-        for (int c = 0; c < QA; ++c)
+        for (int i = 0; i < HD / 16; ++i) {
+          const int at = (i >> 2) * (128 * 128) + (i & 3) * 32;  // k-step i of q and of k alike
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint64_t dk = sw128_kmajor_desc(k + c * (KT * 128) + i * 32);
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-              tc_mma_bf16(d, sw128_kmajor_desc(q + t * LY::kQ1 + c * (128 * 128) + i * 32), dk, id_s,
-                          (c | i | t) != 0);
-          }
-      };
-      PagedCursor c = paged_cursor<KT>(a, st);
-      int items = 0, tiles = 0;  // of this CTA so far; tile g uses slots 2g (K), 2g + 1 (V)
-      int turns[2] = {0, 0};     // tiles of each stream
-      auto wait = [&](uint64_t* bar, int n) { return wait_for(bar, n, a.wait_ns); };
-      auto kv_wait = [&](int use) { return wait(&kv_full[use % NS], use / NS); };
-      auto slot_at = [&](int use) { return ring + (uint32_t)(use % NS) * LY::kTile; };
-      bool ok = true;
-      do {
-        const int n = c.kend - c.kt;
-        const bool two = NT == 1 && c.s.nb - c.rt * a.tpt > half;  // the second stream has rows
-        ok = wait(q_full, items) && kv_wait(2 * tiles);
-        if (!ok) break;
-        tc_fence_after();
-        if constexpr (NT == 1) {
-          issue_s(qs, slot_at(2 * tiles), tb);
-          tc_commit(&s_full[0]);
-          if (two) {
-            issue_s(qs + LY::kQ1, slot_at(2 * tiles), tb + 128);
-            tc_commit(&s_full[1]);
-          }
-          tc_commit(&kv_empty[(2 * tiles) % NS]);
-          for (int x = 0; x < n; ++x) {
-            const int g = tiles + x;
-            ok = kv_wait(2 * g + 1);
-            for (int s = 0; ok && s < (two ? 2 : 1); ++s) {
-              ok = wait(&p_full[s], turns[s]++);
-              if (!ok) break;
+          for (int t = 0; t < NT; ++t)
+            tc_mma_bf16(d, q + ((t * LY::kQ1 + at) >> 4), k + (at >> 4), id_s, (i | t) != 0);
+        }
+      }
+      __syncwarp();
+    };
+    auto commit = [&](uint64_t* bar) {
+      if (lead) tc_commit(bar);
+      __syncwarp();
+    };
+    PagedCursor c = paged_cursor<KT>(a, st);
+    int items = 0, tiles = 0;  // of this CTA so far; tile g uses slots 2g (K), 2g + 1 (V)
+    int turns[2] = {0, 0};     // tiles of each stream (NT = 1)
+    auto wait = [&](uint64_t* bar, int n) {
+      return __all_sync(0xffffffffu, wait_for(bar, n, a.wait_ns)) != 0;
+    };
+    auto kv_wait = [&](int use) { return wait(&kv_full[use % NS], use / NS); };
+    bool ok = true;
+    do {
+      const int n = __shfl_sync(0xffffffffu, c.kend - c.kt, 0);
+      const int streams =  // the second stream may have no rows in this item
+          __shfl_sync(0xffffffffu, NT == 1 && c.s.nb - c.rt * a.tpt > half ? 2 : 1, 0);
+      ok = wait(q_full, items) && kv_wait(2 * tiles);
+      if (!ok) break;
+      tc_fence_after();
+      if constexpr (NT == 1) {
+#pragma unroll 1
+        for (int s = 0; s < streams; ++s) {
+          issue_s(dq + s * (LY::kQ1 >> 4), dk + slot_at(2 * tiles), tm + 128 * s);
+          commit(&s_full[s]);
+        }
+#pragma unroll 1
+        for (int x = 0; ok && x < n; ++x) {
+          const int g = tiles + x;
+          const uint64_t v = dv + slot_at(2 * g + 1), k = dk + slot_at(2 * g + 2);
+          const bool last = x + 1 == n;
+          ok = kv_wait(2 * g + 1);
+#pragma unroll 1
+          for (int s = 0; ok && s < streams; ++s) {
+            const uint32_t p = tm + 128 * s;
+            auto issue_pv = [&](int i0) {  // half of the tile's keys
               tc_fence_after();
-              const uint32_t v = slot_at(2 * g + 1), p = tb + 128 * s;
+              if (lead) {
 #pragma unroll
-              for (int i = 0; i < KT / 16; ++i)
-                tc_mma_bf16_ta(tb + LY::t_o + 128 * s, p + 8 * i,
-                               sw128_mnmajor_desc(v + i * 2048, KT * 128), id_o, (x | i) != 0);
-              if (x + 1 < n) {  // the stream's next scores, into the columns P leaves
-                if (s == 0) ok = kv_wait(2 * g + 2);
-                if (!ok) break;
-                issue_s(qs + s * LY::kQ1, slot_at(2 * g + 2), p);
-                tc_commit(&s_full[s]);
-              } else {
-                tc_commit(&o_full[s]);
+                for (int i = 0; i < KT / 32; ++i)
+                  tc_mma_bf16_ta(p + LY::t_o, p + 8 * (i0 + i), v + ((i0 + i) * 2048 >> 4), id_o,
+                                 (x | i0 | i) != 0);
               }
-            }
+              __syncwarp();
+            };
+            ok = wait(&p_half[s], turns[s]);
             if (!ok) break;
-            tc_commit(&kv_empty[(2 * g + 1) % NS]);
-            if (x + 1 < n) tc_commit(&kv_empty[(2 * g + 2) % NS]);
-          }
-        } else {
-          issue_s(qs, slot_at(2 * tiles), tb + 128 * (tiles & 1));
-          tc_commit(&s_full[tiles & 1]);
-          tc_commit(&kv_empty[(2 * tiles) % NS]);
-          for (int x = 0; x < n; ++x) {
-            const int g = tiles + x;
-            if (x + 1 < n) {  // the next tile's scores while this one's weights are formed
-              ok = kv_wait(2 * g + 2);
+            issue_pv(0);
+            ok = wait(&p_full[s], turns[s]++);
+            if (!ok) break;
+            issue_pv(KT / 32);
+            if (!last) {
+              if (s == 0) ok = kv_wait(2 * g + 2);
               if (!ok) break;
-              tc_fence_after();
-              issue_s(qs, slot_at(2 * g + 2), tb + 128 * ((g + 1) & 1));
-              tc_commit(&s_full[(g + 1) & 1]);
-              tc_commit(&kv_empty[(2 * g + 2) % NS]);
+              issue_s(dq + s * (LY::kQ1 >> 4), k, p);  // into the columns P leaves
             }
-            ok = kv_wait(2 * g + 1) && wait(&p_full[0], g);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t v = slot_at(2 * g + 1), p = tb + 128 * (g & 1);
-            const uint32_t px = tb + LY::t_x + 64 * (g & 1);
-#pragma unroll
-            for (int i = 0; i < KT / 16; ++i) {
-              const uint64_t dv = sw128_mnmajor_desc(v + i * 2048, KT * 128);
-              tc_mma_bf16_ta(tb + LY::t_o, p + 8 * i, dv, id_o, (x | i) != 0);
-              tc_mma_bf16_ta(tb + LY::t_o, p + 64 + 8 * i, dv, id_o, 1);
-              tc_mma_bf16_ta(tb + LY::t_o, px + 8 * i, dv, id_o, 1);
-            }
-            tc_commit(&o_full[0]);
-            tc_commit(&kv_empty[(2 * g + 1) % NS]);
+            commit(last ? &o_full[s] : &s_full[s]);
           }
         }
-        tiles += n;
-        ++items;
-      } while (ok && c.next<KT>(a));
-      if (!ok && a.c.status) atomicOr(a.c.status, PG_TIMEOUT);
-      // TMEM is released only after every MMA issued here has finished
-      tc_commit(done);
-      wait_for(done, 0, kDrainNs);
-    }
-  } else if (warp >= 4) {
+      } else {
+        issue_s(dq, dk + slot_at(2 * tiles), tm + 128 * (tiles & 1));
+        commit(&s_full[tiles & 1]);
+        commit(&kv_empty[(2 * tiles) % NS]);
+        for (int x = 0; x < n; ++x) {
+          const int g = tiles + x;
+          if (x + 1 < n) {  // the next tile's scores while this one's weights are formed
+            ok = kv_wait(2 * g + 2);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(dq, dk + slot_at(2 * g + 2), tm + 128 * ((g + 1) & 1));
+            commit(&s_full[(g + 1) & 1]);
+            commit(&kv_empty[(2 * g + 2) % NS]);
+          }
+          ok = kv_wait(2 * g + 1) && wait(&p_full[0], g);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t v = dv + slot_at(2 * g + 1);
+          const uint32_t p = tm + 128 * (g & 1), px = tm + LY::t_x + 64 * (g & 1);
+          if (lead) {
+#pragma unroll
+            for (int i = 0; i < KT / 16; ++i) {
+              tc_mma_bf16_ta(tm + LY::t_o, p + 8 * i, v + (i * 2048 >> 4), id_o, (x | i) != 0);
+              tc_mma_bf16_ta(tm + LY::t_o, p + 64 + 8 * i, v + (i * 2048 >> 4), id_o, 1);
+              tc_mma_bf16_ta(tm + LY::t_o, px + 8 * i, v + (i * 2048 >> 4), id_o, 1);
+            }
+          }
+          __syncwarp();
+          commit(&o_full[0]);
+          commit(&kv_empty[(2 * g + 1) % NS]);
+        }
+      }
+      tiles += n;
+      ++items;
+    } while (ok && c.next<KT>(a));
+    if (!ok && lead && a.c.status) atomicOr(a.c.status, PG_TIMEOUT);
+    // TMEM is released only after every MMA issued here has finished
+    commit(done);
+    wait_for(done, 0, kDrainNs);
+  } else {
     // ---- softmax of a stream: thread = query row
-    const int s = (warp - 4) >> 2, r = threadIdx.x & 127;
+    const int s = (warp - 2) >> 2, r = (warp & 3) * 32 + lane;  // a warp reaches 32 lanes of TMEM
     const uint32_t lrow = (uint32_t)((warp & 3) * 32) << 16;
     PagedCursor c = paged_cursor<KT>(a, st);
     int tiles = 0, mine = 0;  // of the CTA; of this stream
@@ -276,37 +317,52 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
       const int tok0 = c.rt * a.tpt + s * half;              // of this stream's row tile
       const int ntok = min(max(c.s.nb - tok0, 0), half), rows = ntok * a.gq;
       const bool live = r < rows;
-      const int tok = c.s.lo + tok0 + r / a.gq, head = c.kvh * a.gq + r % a.gq;
       const int lim = !live           ? 0
                       : a.prefix_pass ? c.limit
                                       : min(max(c.s.base + tok0 + r / a.gq + 1, 0), c.s.len);
-      // q into shared memory, K-major with 128-byte swizzling: 16-byte units of 8 columns
+      // q into shared memory, K-major with 128-byte swizzling: the warp's 32 rows, whole rows at a
+      // time (16-byte units of 8 columns; a unit of f32 activations comes as two loads)
       {
-        const size_t at = (size_t)tok * a.ldq + (size_t)head * HD;
-        uint8_t* row = sm + (NT == 1 ? s * LY::kQ1 : 0) + (r >> 3) * 1024 + (r & 7) * 128;
-#pragma unroll 8
-        for (int u = 0; u < HD / 8; ++u) {
-          const uint32_t off = (u >> 3) * (128 * 128) + (((u & 7) ^ (r & 7)) << 4);
-          if constexpr (NT == 1) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (live)
-              v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at) + u);
-            *reinterpret_cast<uint4*>(row + off) = v;
-          } else {
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-            if (live) {
-              const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at) + 2 * u;
-              x = __ldg(p);
-              y = __ldg(p + 1);
+        constexpr int RU = HD / 8, RPI = 32 / RU, NB = 8;  // units of a row, rows per load, loads in flight
+        const int u = lane % RU, sub = lane / RU;
+        uint8_t* base = sm + (NT == 1 ? s * LY::kQ1 : 0);
+        const uint32_t col = (uint32_t)(u >> 3) * (128 * 128);
+#pragma unroll 1
+        for (int i0 = 0; i0 < 32 / RPI; i0 += NB) {
+          uint4 v[NB], w[NT == 3 ? NB : 1];
+#pragma unroll
+          for (int i = 0; i < NB; ++i) {
+            const int rr = (warp & 3) * 32 + (i0 + i) * RPI + sub;
+            const size_t at = (size_t)(c.s.lo + tok0 + rr / a.gq) * a.ldq +
+                              (size_t)(c.kvh * a.gq + rr % a.gq) * HD + u * 8;
+            v[i] = make_uint4(0, 0, 0, 0);
+            if constexpr (NT == 1) {
+              if (rr < rows) v[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at));
+            } else {
+              w[i] = v[i];
+              if (rr < rows) {
+                const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(a.q) + at);
+                v[i] = __ldg(p);
+                w[i] = __ldg(p + 1);
+              }
             }
-            uint32_t h[4], m[4], l[4];
-            split3(x.x, x.y, h[0], m[0], l[0]);
-            split3(x.z, x.w, h[1], m[1], l[1]);
-            split3(y.x, y.y, h[2], m[2], l[2]);
-            split3(y.z, y.w, h[3], m[3], l[3]);
-            *reinterpret_cast<uint4*>(row + off) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4*>(row + LY::kQ1 + off) = make_uint4(m[0], m[1], m[2], m[3]);
-            *reinterpret_cast<uint4*>(row + 2 * LY::kQ1 + off) = make_uint4(l[0], l[1], l[2], l[3]);
+          }
+#pragma unroll
+          for (int i = 0; i < NB; ++i) {
+            const int rr = (warp & 3) * 32 + (i0 + i) * RPI + sub;
+            uint8_t* to = base + col + (rr >> 3) * 1024 + (rr & 7) * 128 + (((u & 7) ^ (rr & 7)) << 4);
+            if constexpr (NT == 1) {
+              *reinterpret_cast<uint4*>(to) = v[i];
+            } else {
+              uint32_t h[4], m[4], l[4];
+              split3(__uint_as_float(v[i].x), __uint_as_float(v[i].y), h[0], m[0], l[0]);
+              split3(__uint_as_float(v[i].z), __uint_as_float(v[i].w), h[1], m[1], l[1]);
+              split3(__uint_as_float(w[i].x), __uint_as_float(w[i].y), h[2], m[2], l[2]);
+              split3(__uint_as_float(w[i].z), __uint_as_float(w[i].w), h[3], m[3], l[3]);
+              *reinterpret_cast<uint4*>(to) = make_uint4(h[0], h[1], h[2], h[3]);
+              *reinterpret_cast<uint4*>(to + LY::kQ1) = make_uint4(m[0], m[1], m[2], m[3]);
+              *reinterpret_cast<uint4*>(to + 2 * LY::kQ1) = make_uint4(l[0], l[1], l[2], l[3]);
+            }
           }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -321,9 +377,14 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
         const uint32_t ts = tb + 128 * buf + lrow;
         wait(&s_full[buf], NT == 1 ? mine : g >> 1);
         tc_fence_after();
+        if (NT == 1 && (warp & 3) == 0 && lane == 0) {  // S_g and P V of tile g - 1 have finished
+          mbar_arrive_cta(&kv_empty[(2 * g) % NS]);
+          if (x > 0) mbar_arrive_cta(&kv_empty[(2 * g - 1) % NS]);
+        }
         const int k0 = (c.kt + x) * KT;
-        if (k0 + KT > c.limit && s == 0) {
-          // values behind the last key are whatever the page held: cleared (0 * NaN is NaN)
+        if (k0 + KT > c.limit) {
+          // values behind the last key are whatever the page held: cleared (0 * NaN is NaN), by both
+          // streams alike, each before its own products
           wait(&kv_full[(2 * g + 1) % NS], (2 * g + 1) / NS);
           if (k0 + r >= c.limit) {
             uint4* v = reinterpret_cast<uint4*>(sm + LY::off_ring + ((2 * g + 1) % NS) * LY::kTile + r * 128);
@@ -334,81 +395,31 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
-        // Half a row of scores at a time in registers: the second half is read for its maximum, given
-        // up, and read again for its weights; the first half stays (keys no row sees are -inf).
-        uint32_t sv[KT / 2];
-        const bool edge = k0 + KT > c.limit - a.tpt;
-        auto load_half = [&](int hf) {
+        uint32_t sv[KT];  // the row's scores; keys it does not see are -inf
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            tmem_ld16(ts + 64 * hf + 16 * i, *reinterpret_cast<uint32_t(*)[16]>(sv + 16 * i));
-          tmem_ld_wait();
+        for (int i = 0; i < KT / 16; ++i)
+          tmem_ld16(ts + 16 * i, *reinterpret_cast<uint32_t(*)[16]>(sv + 16 * i));
+        tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_regs_ready(*reinterpret_cast<uint32_t(*)[16]>(sv + 16 * i));
-          if (edge) {
+        for (int i = 0; i < KT / 16; ++i) tmem_regs_ready(*reinterpret_cast<uint32_t(*)[16]>(sv + 16 * i));
+        if (k0 + KT > c.limit - a.tpt) {
 #pragma unroll
-            for (int j = 0; j < 64; ++j)
-              if (k0 + 64 * hf + j >= lim) sv[j] = 0xff800000u;  // -inf
-          }
-        };
+          for (int j = 0; j < KT; ++j)
+            if (k0 + j >= lim) sv[j] = 0xff800000u;
+        }
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        auto max_half = [&] {
 #pragma unroll
-          for (int j = 0; j < 64; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], __uint_as_float(sv[j]));
-        };
-        load_half(1);
-        max_half();
-        load_half(0);
-        max_half();
+        for (int j = 0; j < KT; j += 2)
+          mx4[j / 2 & 3] = fmaxf(fmaxf(mx4[j / 2 & 3], __uint_as_float(sv[j])), __uint_as_float(sv[j + 1]));
         const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.scale_log2;
         const float mn = mx > m + 8.f ? mx : m;  // a row without a key yet keeps -inf
         const float mu = mn == -INFINITY ? 0.f : mn;
         const float alpha = paged_exp2(m - mu);
-        // the weights, 32 keys at a time, into TMEM. They overwrite columns of S that have been read:
-        // 16 i .. 16 i + 15 after keys 32 i .. 32 i + 31 (NT = 1); with NT = 3 both terms' columns
-        // cover S, so the second half waits in registers of its own
-        float ps[4] = {0.f, 0.f, 0.f, 0.f};
-        auto weights = [&](const uint32_t* v, int i) {
-          float p[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            p[e] = paged_exp2(fmaf(__uint_as_float(v[e]), a.scale_log2, -mu));
-            ps[e & 3] += p[e];
+        if (x > 0 && __any_sync(0xffffffffu, mn != m)) {  // O moves to the new reference
+          if (NT == 3) {  // (NT = 1: P V of the last tile was done before s_full of this one)
+            wait(&o_full[0], g - 1);
+            tc_fence_after();
           }
-          uint32_t ph[16];
-          if constexpr (NT == 1) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) ph[e] = paged_pack(p[2 * e], p[2 * e + 1]);
-            tmem_st16(ts + 16 * i, ph);
-          } else {
-            uint32_t pm[16], pl[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) split3(p[2 * e], p[2 * e + 1], ph[e], pm[e], pl[e]);
-            tmem_st16(ts + 16 * i, ph);
-            tmem_st16(ts + 64 + 16 * i, pm);
-            tmem_st16(tb + LY::t_x + 64 * buf + lrow + 16 * i, pl);
-          }
-        };
-        if constexpr (NT == 1) {
-          weights(sv, 0);
-          weights(sv + 32, 1);
-          load_half(1);
-          weights(sv, 2);
-          weights(sv + 32, 3);
-        } else {
-          uint32_t first_half[KT / 2];
-#pragma unroll
-          for (int j = 0; j < KT / 2; ++j) first_half[j] = sv[j];
-          load_half(1);
-          weights(first_half, 0);
-          weights(first_half + 32, 1);
-          weights(sv, 2);
-          weights(sv + 32, 3);
-        }
-        l = l * alpha + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
-        if (NT == 3 && x > 0) wait(&o_full[0], g - 1);  // (NT = 1: before s_full of this tile)
-        if (x > 0 && __any_sync(0xffffffffu, mn != m)) {
-          tc_fence_after();
 #pragma unroll 1
           for (int d = 0; d < HD; d += 16) {
             uint32_t o[16];
@@ -421,44 +432,102 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
           }
         }
         m = mn;
+        // the weights, 32 keys at a time, into TMEM over columns of S, which is in registers
+        const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), mu2 = make_float2(-mu, -mu);
+        float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int i = 0; i < KT / 32; ++i) {
+          float2 p[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 z = fma2(make_float2(__uint_as_float(sv[32 * i + 2 * e]),
+                                              __uint_as_float(sv[32 * i + 2 * e + 1])), sc2, mu2);
+            p[e] = make_float2(paged_exp2(z.x), paged_exp2(z.y));
+            ps[e & 1] = add2(ps[e & 1], p[e]);
+          }
+          uint32_t ph[16];
+          if constexpr (NT == 1) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) ph[e] = paged_pack(p[e].x, p[e].y);
+            tmem_st16(ts + 16 * i, ph);
+            if (i == KT / 64 - 1) {  // half of P V starts while the other half's weights are formed
+              tmem_st_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cta(&p_half[s]);
+            }
+          } else {
+            uint32_t pm[16], pl[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) split3(p[e].x, p[e].y, ph[e], pm[e], pl[e]);
+            tmem_st16(ts + 16 * i, ph);
+            tmem_st16(ts + 64 + 16 * i, pm);
+            tmem_st16(tb + LY::t_x + 64 * buf + lrow + 16 * i, pl);
+          }
+        }
+        l = l * alpha + ((ps[0].x + ps[0].y) + (ps[1].x + ps[1].y));
+        // every phase of o_full is waited for before the next can end: a parity skipped could be
+        // taken for the one before it
+        if (NT == 3 && x > 0) wait(&o_full[0], g - 1);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cta(&p_full[NT == 1 ? s : 0]);
       }
+      if (NT == 1 && rows == 0 && (warp & 3) == 0) {  // a stream without rows lets the tiles pass
+        for (int u = 2 * tiles; u < 2 * (tiles + n); ++u) {
+          wait(&kv_full[u % NS], u / NS);
+          if (lane == 0) mbar_arrive_cta(&kv_empty[u % NS]);
+        }
+      }
       if (rows > 0) {
-        if constexpr (NT == 1)
+        if constexpr (NT == 1) {
           wait(&o_full[s], ends++);
-        else
+          if ((warp & 3) == 0 && lane == 0) mbar_arrive_cta(&kv_empty[(2 * (tiles + n) - 1) % NS]);
+        } else {
           wait(&o_full[0], tiles + n - 1);
+        }
         tc_fence_after();
         if (whole && a.pre.o && !a.prefix_pass) pdl_wait();  // the prefix's records
-        const size_t slot = (size_t)(2 * blockIdx.x + (first ? 1 : 0)) * a.slots.rows + s * half * a.gq + r;
+        // O out through shared memory (the q tile's, which no MMA reads any more), 32 columns of the
+        // warp's 32 rows at a time, so that whole 128-byte lines leave
+        const size_t slot = (size_t)(2 * blockIdx.x + (first ? 1 : 0)) * a.slots.rows + s * half * a.gq;
+        float* stage = reinterpret_cast<float*>(sm + s * LY::kQ1 + (warp & 3) * 4096);
+        const int lr = lane >> 3, lc = lane & 7;  // rows of 8 lanes
 #pragma unroll 1
-        for (int d = 0; d < HD; d += 16) {
-          uint32_t o[16];
-          tmem_ld16(to + d, o);
+        for (int d = 0; d < HD; d += 32) {
+          uint32_t o[2][16];
+          tmem_ld16(to + d, o[0]);
+          tmem_ld16(to + d + 16, o[1]);
           tmem_ld_wait();
-          tmem_regs_ready(o);
-          if (!live) continue;
+          tmem_regs_ready(o[0]);
+          tmem_regs_ready(o[1]);
 #pragma unroll
-          for (int e = 0; e < 16; e += 4) {
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<uint4*>(stage + lane * 32 + ((e ^ (lane & 7)) << 2)) =
+                make_uint4(o[e >> 2][4 * (e & 3)], o[e >> 2][4 * (e & 3) + 1], o[e >> 2][4 * (e & 3) + 2],
+                           o[e >> 2][4 * (e & 3) + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int q = 4 * i + lr, rr = (warp & 3) * 32 + q;  // row in the warp, in the tile
             PagedAcc acc;
-            acc.m = m;
-            acc.l = l;
-            acc.o = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
-                                __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+            acc.m = __shfl_sync(0xffffffffu, m, q);
+            acc.l = __shfl_sync(0xffffffffu, l, q);
+            acc.o = *reinterpret_cast<const float4*>(stage + q * 32 + ((lc ^ (q & 7)) << 2));
+            if (rr >= rows) continue;
             if (whole)
-              paged_emit(a, HD, tok, head, d + e, acc);
+              paged_emit(a, HD, c.s.lo + tok0 + rr / a.gq, c.kvh * a.gq + rr % a.gq, d + 4 * lc, acc);
             else
-              *reinterpret_cast<float4*>(a.slots.o + slot * HD + d + e) = acc.o;
+              __stcg(reinterpret_cast<float4*>(a.slots.o + (slot + rr) * HD + d + 4 * lc), acc.o);
           }
+          __syncwarp();
         }
-        if (live && !whole) a.slots.ml[slot] = make_float2(m, l);
+        if (live && !whole) a.slots.ml[slot + r] = make_float2(m, l);
         tc_fence_before();
       }
       if (!whole && first && s == 0 && r == 0)  // the joining kernel's work
-        a.splits[blockIdx.x] = PagedSplit{c.last_cta(), c.s.lo + c.rt * a.tpt,
+        a.splits[blockIdx.x] = PagedSplit{c.last_cta<KT>(), c.s.lo + c.rt * a.tpt,
                                           min(a.tpt, c.s.nb - c.rt * a.tpt) * a.gq, c.kvh * a.gq};
       tiles += n;
     } while (c.next<KT>(a));

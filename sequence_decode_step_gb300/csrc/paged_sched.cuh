@@ -11,8 +11,8 @@
 // last CTA to arrive (counters[first CTA]), those of a prefix or of tensor-core tiles by a kernel
 // of their own (many rows: one CTA would read them for 5-10 us).
 //
-// An item costs a CTA about kPagedItemUnits tiles beside its keys (q, the join, the output), so on
-// the line it is that much longer; the units before its first tile are empty.
+// An item costs a CTA some tiles beside its keys (q, the join, the output), so on the line it is
+// that much longer (paged_item_units); the units before its first tile are empty.
 //
 // The shared prefix is the same line with one pseudo-sequence: all the batch's tokens, every one
 // of which sees all prefix_len keys.
@@ -22,7 +22,12 @@
 
 namespace qw {
 
-constexpr int kPagedItemUnits = 1;
+// Tiles that an item's q, first product and output take: 4 us against 1.5 us for a tensor-core tile
+// of 128 keys, about one tile of 32 or 64 keys elsewhere.
+template <int KT>
+__host__ __device__ constexpr int paged_item_units() {
+  return KT == kPagedTcKeys ? 3 : 1;
+}
 constexpr int kPagedLeastUnits = 2;  // least share of a CTA: fewer records of a short line to join
 
 // Quotient of two line positions: 32-bit where both fit, as they do for any real batch.
@@ -70,7 +75,7 @@ __device__ __forceinline__ int paged_tiles(int limit) {
 template <int KT>
 __device__ __forceinline__ long long paged_head_units(const PagedAttnArgs& a, const PagedSeq& s) {
   long long n = 0;
-  for (int rt = 0; rt < s.nrt; ++rt) n += kPagedItemUnits + paged_tiles<KT>(paged_limit(a, s, rt));
+  for (int rt = 0; rt < s.nrt; ++rt) n += paged_item_units<KT>() + paged_tiles<KT>(paged_limit(a, s, rt));
   return n;
 }
 
@@ -84,21 +89,25 @@ struct PagedCursor {  // a place on the line
   __device__ __forceinline__ bool first() const { return kt == 0; }
   __device__ __forceinline__ bool whole() const { return kt == 0 && kend == nkt; }
   // CTAs that share the item's tiles
-  __device__ __forceinline__ int first_cta() const { return (int)paged_div(item + kPagedItemUnits, per); }
+  template <int KT>
+  __device__ __forceinline__ int first_cta() const {
+    return (int)paged_div(item + paged_item_units<KT>(), per);
+  }
+  template <int KT>
   __device__ __forceinline__ int last_cta() const {
-    return (int)paged_div(item + kPagedItemUnits + nkt - 1, per);
+    return (int)paged_div(item + paged_item_units<KT>() + nkt - 1, per);
   }
   template <int KT>
   __device__ __forceinline__ void enter(const PagedAttnArgs& a) {
     limit = paged_limit(a, s, rt);
     nkt = paged_tiles<KT>(limit);
-    kend = (int)min((long long)nkt, u1 - item - kPagedItemUnits);
+    kend = (int)min((long long)nkt, u1 - item - paged_item_units<KT>());
   }
   // To the CTA's next item; false when its share ends before that item's first tile.
   template <int KT>
   __device__ __forceinline__ bool next(const PagedAttnArgs& a) {
-    item += kPagedItemUnits + nkt;
-    if (item + kPagedItemUnits >= u1) return false;
+    item += paged_item_units<KT>() + nkt;
+    if (item + paged_item_units<KT>() >= u1) return false;
     kt = 0;
     if (++rt == s.nrt) {
       rt = 0;
@@ -163,7 +172,7 @@ __device__ void paged_find_start(const PagedAttnArgs& a, PagedStart* st, long lo
     r -= hu * kvh;
     int rt = 0;
     for (;; ++rt) {
-      const int t = kPagedItemUnits + paged_tiles<KT>(paged_limit(a, s, rt));
+      const int t = paged_item_units<KT>() + paged_tiles<KT>(paged_limit(a, s, rt));
       if (r < t) break;
       r -= t;
     }
@@ -173,8 +182,8 @@ __device__ void paged_find_start(const PagedAttnArgs& a, PagedStart* st, long lo
     st->b = b;
     st->kvh = kvh;
     st->rt = rt;
-    st->kt = max((int)r - kPagedItemUnits, 0);
-    st->any = u0 - r + kPagedItemUnits < st->u1;  // the share has a tile
+    st->kt = max((int)r - paged_item_units<KT>(), 0);
+    st->any = u0 - r + paged_item_units<KT>() < st->u1;  // the share has a tile
   }
   __syncthreads();
 }
