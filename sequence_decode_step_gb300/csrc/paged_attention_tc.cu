@@ -154,7 +154,19 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
     while (ok && more) {
       const int key = c.kt * KT + piece * prow, kvh = c.kvh, now = page;
       const int pieces = min(np, (max(c.limit - c.kt * KT, 0) + prow - 1) / prow);
-      if (++c.kt == c.kend) more = c.next<KT>(a);
+      if (++c.kt == c.kend) {
+        more = c.next<KT>(a);
+        if (more) {  // its q rows (gq heads of a token lie together) into L2
+          const int bytes = a.gq * HD * (NT == 1 ? 2 : 4), lines = bytes / 128;
+          const int n = min(a.tpt, c.s.nb - c.rt * a.tpt);
+          for (int i = lane; i < n * lines; i += 32) {
+            const char* q = static_cast<const char*>(a.q) +
+                            ((size_t)(c.s.lo + c.rt * a.tpt + i / lines) * a.ldq + (size_t)c.kvh * a.gq * HD) *
+                                (NT == 1 ? 2 : 4) + i % lines * 128;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+          }
+        }
+      }
       if (more) page = page_of(c);
 #pragma unroll 1
       for (int t = 0; t < 2; ++t) {
@@ -304,6 +316,9 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
     // ---- softmax of a stream: thread = query row
     const int s = (warp - 2) >> 2, r = (warp & 3) * 32 + lane;  // a warp reaches 32 lanes of TMEM
     const uint32_t lrow = (uint32_t)((warp & 3) * 32) << 16;
+    // row / gq for rows below 256 and gq <= 8
+    const uint32_t gmul = 65536u / a.gq + 1;
+    auto token_of = [&](int row) { return (int)((uint32_t)row * gmul >> 16); };
     PagedCursor c = paged_cursor<KT>(a, st);
     int tiles = 0, mine = 0;  // of the CTA; of this stream
     int ends = 0;             // items whose end this stream has waited for
@@ -319,7 +334,7 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
       const bool live = r < rows;
       const int lim = !live           ? 0
                       : a.prefix_pass ? c.limit
-                                      : min(max(c.s.base + tok0 + r / a.gq + 1, 0), c.s.len);
+                                      : min(max(c.s.base + tok0 + token_of(r) + 1, 0), c.s.len);
       // q into shared memory, K-major with 128-byte swizzling: the warp's 32 rows, whole rows at a
       // time (16-byte units of 8 columns; a unit of f32 activations comes as two loads)
       {
@@ -332,9 +347,9 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
           uint4 v[NB], w[NT == 3 ? NB : 1];
 #pragma unroll
           for (int i = 0; i < NB; ++i) {
-            const int rr = (warp & 3) * 32 + (i0 + i) * RPI + sub;
-            const size_t at = (size_t)(c.s.lo + tok0 + rr / a.gq) * a.ldq +
-                              (size_t)(c.kvh * a.gq + rr % a.gq) * HD + u * 8;
+            const int rr = (warp & 3) * 32 + (i0 + i) * RPI + sub, t = token_of(rr);
+            const size_t at = (size_t)(c.s.lo + tok0 + t) * a.ldq +
+                              (size_t)(c.kvh * a.gq + (rr - t * a.gq)) * HD + u * 8;
             v[i] = make_uint4(0, 0, 0, 0);
             if constexpr (NT == 1) {
               if (rr < rows) v[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at));
@@ -490,10 +505,41 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
         tc_fence_after();
         if (whole && a.pre.o && !a.prefix_pass) pdl_wait();  // the prefix's records
         // O out through shared memory (the q tile's, which no MMA reads any more), 32 columns of the
-        // warp's 32 rows at a time, so that whole 128-byte lines leave
+        // warp's 32 rows at a time, so that whole 128-byte lines leave. A row's factors and place are
+        // formed once: out = o wa + (the prefix's o) wb
         const size_t slot = (size_t)(2 * blockIdx.x + (first ? 1 : 0)) * a.slots.rows + s * half * a.gq;
         float* stage = reinterpret_cast<float*>(sm + s * LY::kQ1 + (warp & 3) * 4096);
         const int lr = lane >> 3, lc = lane & 7;  // rows of 8 lanes
+        const bool raw = !whole || a.prefix_pass, joins = whole && a.pre.o && !a.prefix_pass;
+        size_t at[8];
+        float wa[8], wb[8];
+        unsigned dead = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rr = (warp & 3) * 32 + 4 * i + lr, t = token_of(rr);
+          const size_t row = (size_t)(c.s.lo + tok0 + t) * a.nq + c.kvh * a.gq + (rr - t * a.gq);
+          const float rm = __shfl_sync(0xffffffffu, m, 4 * i + lr);
+          const float rl = __shfl_sync(0xffffffffu, l, 4 * i + lr);
+          at[i] = (whole ? row : slot + rr) * HD + 4 * lc;
+          wa[i] = raw ? 1.f : rl > 0.f || rl != rl ? 1.f / rl : 0.f;
+          wb[i] = 0.f;
+          if (rr >= rows) {
+            dead |= 1u << i;
+            at[i] = 0;
+          } else if (joins) {
+            const float2 ml = __ldcg(a.pre.ml + row);
+            const float top = fmaxf(rm, ml.x);
+            if (top != -INFINITY) {
+              const float f = paged_exp2(rm - top), g = paged_exp2(ml.x - top);
+              const float inv = 1.f / fmaf(rl, f, ml.y * g);
+              wa[i] = f * inv;
+              wb[i] = g * inv;
+            }
+          } else if (whole && a.prefix_pass && lc == 0) {
+            a.pre.ml[row] = make_float2(rm, rl);
+          }
+        }
+        float* const to_f = !whole ? a.slots.o : a.prefix_pass ? a.pre.o : static_cast<float*>(a.out);
 #pragma unroll 1
         for (int d = 0; d < HD; d += 32) {
           uint32_t o[2][16];
@@ -510,16 +556,20 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const int q = 4 * i + lr, rr = (warp & 3) * 32 + q;  // row in the warp, in the tile
-            PagedAcc acc;
-            acc.m = __shfl_sync(0xffffffffu, m, q);
-            acc.l = __shfl_sync(0xffffffffu, l, q);
-            acc.o = *reinterpret_cast<const float4*>(stage + q * 32 + ((lc ^ (q & 7)) << 2));
-            if (rr >= rows) continue;
-            if (whole)
-              paged_emit(a, HD, c.s.lo + tok0 + rr / a.gq, c.kvh * a.gq + rr % a.gq, d + 4 * lc, acc);
+            const int q = 4 * i + lr;
+            float4 x = *reinterpret_cast<const float4*>(stage + q * 32 + ((lc ^ (q & 7)) << 2));
+            x.x *= wa[i], x.y *= wa[i], x.z *= wa[i], x.w *= wa[i];
+            if (dead >> i & 1) continue;
+            if (joins) {
+              const float4 y = __ldcg(reinterpret_cast<const float4*>(a.pre.o + at[i] + d));
+              x.x = fmaf(wb[i], y.x, x.x), x.y = fmaf(wb[i], y.y, x.y);
+              x.z = fmaf(wb[i], y.z, x.z), x.w = fmaf(wb[i], y.w, x.w);
+            }
+            if (!raw && NT == 1)
+              *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at[i] + d) =
+                  make_uint2(paged_pack(x.x, x.y), paged_pack(x.z, x.w));
             else
-              __stcg(reinterpret_cast<float4*>(a.slots.o + (slot + rr) * HD + d + 4 * lc), acc.o);
+              *reinterpret_cast<float4*>(to_f + at[i] + d) = x;
           }
           __syncwarp();
         }
