@@ -38,7 +38,7 @@ struct AppendArgs {
   // theta^(-2j/hd) / 2 pi in two f32 terms
   float inv_hi[64], inv_lo[64];
 };
-cudaError_t launch_paged_append(const AppendArgs& a, int hd, bool act_bf16, cudaStream_t s);
+cudaError_t launch_paged_append(const AppendArgs& a, int hd, bool act_bf16, int sms, cudaStream_t s);
 
 // ---- attention ----
 // Partial records of query rows: [rows][hd] unnormalised outputs and their (reference maximum,

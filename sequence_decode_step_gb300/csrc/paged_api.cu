@@ -93,6 +93,8 @@ extern "C" int qw_paged_append(const qw_paged_kv* c, const void* qkv, uint32_t a
   if (!qkv || !q_out) return fail(QW_ERR_ARG, "qw_paged_append: null buffer");
   if (!q_norm != !k_norm)
     return fail(QW_ERR_ARG, "qw_paged_append: q_norm and k_norm come together or not at all");
+  if (((uintptr_t)q_norm | (uintptr_t)k_norm) & 3)
+    return fail(QW_ERR_ARG, "qw_paged_append: q_norm and k_norm must be 4-byte aligned");
   const int hd = c->head_dim, align = act_format == QW_ACT_BF16 ? 8 : 4;
   if (ld < (int64_t)(n_q_heads + 2 * (int64_t)c->n_kv_heads) * hd || ld % align)
     return fail(QW_ERR_ARG,
@@ -132,7 +134,10 @@ extern "C" int qw_paged_append(const qw_paged_kv* c, const void* qkv, uint32_t a
     a.inv_hi[j] = (float)f;
     a.inv_lo[j] = (float)(f - (double)a.inv_hi[j]);
   }
-  const cudaError_t e = qw::launch_paged_append(a, hd, act_format == QW_ACT_BF16, (cudaStream_t)stream);
+  int sms = 0;
+  cudaError_t e = device_sms(&sms);
+  if (e == cudaSuccess)
+    e = qw::launch_paged_append(a, hd, act_format == QW_ACT_BF16, sms, (cudaStream_t)stream);
   if (e != cudaSuccess) return fail(QW_ERR_CUDA, cudaGetErrorString(e));
   return QW_OK;
 }

@@ -21,7 +21,9 @@
 // pairs that rotate together, so a head is hd/8 threads of f32 (hd/16 of bf16), loads and stores
 // are 16 bytes wide, and the norm is a shuffle over those threads. A CTA takes `tb` whole tokens:
 // the cosines of a token are formed once in shared memory for all its heads (24 of them in the
-// 16/8-head models), and so is the token's place in the cache.
+// 16/8-head models), and so is the token's place in the cache. Few tokens get a CTA each, so that
+// the chain is all there is; many go 8 to a CTA, which shares the chain and its barriers among them,
+// and every thread has the next head's loads in flight while it works on one.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -55,16 +57,21 @@ struct Act;
 template <>
 struct Act<false> {
   static constexpr int V = 4;  // elements per 16 bytes
-  static __device__ __forceinline__ void load(const void* base, size_t i, float (&x)[4]) {
-    const float4 v = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(base) + i));
-    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+  static __device__ __forceinline__ uint4 load(const void* base, size_t i) {
+    return __ldcs(reinterpret_cast<const uint4*>(static_cast<const float*>(base) + i));
+  }
+  static __device__ __forceinline__ void widen(const uint4& v, float (&x)[4]) {
+    x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y);
+    x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
   }
 };
 template <>
 struct Act<true> {
   static constexpr int V = 8;
-  static __device__ __forceinline__ void load(const void* base, size_t i, float (&x)[8]) {
-    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i));
+  static __device__ __forceinline__ uint4 load(const void* base, size_t i) {
+    return __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i));
+  }
+  static __device__ __forceinline__ void widen(const uint4& v, float (&x)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -106,7 +113,7 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
                                                                 int tb) {
   constexpr int V = Act<BF>::V, HALF = HD / 2, LPH = HALF / V;  // lanes per head
   constexpr int HPP = kThreads / LPH;                          // heads per pass of the CTA
-  __shared__ float2 cs[kMaxTb][HALF];
+  __shared__ __align__(16) float2 cs[kMaxTb][HALF];
   __shared__ int row_s[kMaxTb];        // cache row, or INT_MIN: the token belongs to no sequence
   __shared__ long long place_s[kMaxTb];  // first row of the token's slot in the pool, or -1
   __shared__ int seq_s[kMaxTb];
@@ -117,23 +124,35 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
 
   // the first unit's loads leave before the lookups below
   int u = threadIdx.x / LPH;
-  float x0[V], x1[V];
+  uint4 n0, n1;
   auto load = [&](int unit) {
     const int t = unit / heads, h = unit - t * heads;
     const size_t i = (size_t)(t0 + t) * a.ld + (size_t)h * HD + j0;
-    Act<BF>::load(a.qkv, i, x0);
-    Act<BF>::load(a.qkv, i + HALF, x1);
+    n0 = Act<BF>::load(a.qkv, i);
+    n1 = Act<BF>::load(a.qkv, i + HALF);
   };
   if (u < units) load(u);
+  // this thread's gains, as bf16 pairs: of q, then of k, first and second half
+  uint32_t g[2][2][V / 2];
+  if (a.q_norm) {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      const int j = j0 / 2 + i;
+      g[0][0][i] = __ldg(reinterpret_cast<const uint32_t*>(a.q_norm) + j);
+      g[0][1][i] = __ldg(reinterpret_cast<const uint32_t*>(a.q_norm) + HALF / 2 + j);
+      g[1][0][i] = __ldg(reinterpret_cast<const uint32_t*>(a.k_norm) + j);
+      g[1][1][i] = __ldg(reinterpret_cast<const uint32_t*>(a.k_norm) + HALF / 2 + j);
+    }
+  }
 
   if (threadIdx.x < kMaxTb) row_s[threadIdx.x] = INT_MIN;
   __syncthreads();
   // each token's sequence: every thread looks at some sequences' ranges
   for (int b = threadIdx.x; b < a.c.n_seqs; b += kThreads) {
     const int lo = __ldg(a.c.q_start + b), hi = __ldg(a.c.q_start + b + 1);
+    const int len = __ldg(a.c.kv_len + b);
     const int first = max(lo, t0), last = min(hi, t0 + nt);
     if (first < last) {
-      const int len = __ldg(a.c.kv_len + b);
       for (int t = first; t < last; ++t) {
         row_s[t - t0] = len - (hi - t);
         seq_s[t - t0] = b;
@@ -177,8 +196,11 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
   for (; u < units;) {
     const int t = u / heads, h = u - t * heads;
     const bool is_q = h < a.nq, is_v = h >= a.nq + a.c.nkv;
+    float x0[V], x1[V];
+    Act<BF>::widen(n0, x0);
+    Act<BF>::widen(n1, x1);
+    if (u + HPP < units) load(u + HPP);
     if (!is_v) {
-      const uint16_t* g = is_q ? a.q_norm : a.k_norm;
       if (a.q_norm) {  // both gains or neither
         float ss = 0.f;
 #pragma unroll
@@ -190,17 +212,22 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
         for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
         const float r = rsqrtf(ss * (1.f / HD) + a.eps);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          x0[e] *= r * bf16f(__ldg(g + j0 + e));
-          x1[e] *= r * bf16f(__ldg(g + HALF + j0 + e));
+        for (int i = 0; i < V / 2; ++i) {
+          const uint32_t w0 = is_q ? g[0][0][i] : g[1][0][i], w1 = is_q ? g[0][1][i] : g[1][1][i];
+          x0[2 * i] *= r * __uint_as_float(w0 << 16);
+          x0[2 * i + 1] *= r * __uint_as_float(w0 & 0xffff0000u);
+          x1[2 * i] *= r * __uint_as_float(w1 << 16);
+          x1[2 * i + 1] *= r * __uint_as_float(w1 & 0xffff0000u);
         }
       }
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float2 w = cs[t][j0 + e];
-        const float y0 = x0[e] * w.x - x1[e] * w.y;
+      for (int e = 0; e < V; e += 2) {
+        const float4 w = *reinterpret_cast<const float4*>(&cs[t][j0 + e]);  // two pairs (cos, sin)
+        const float y0 = x0[e] * w.x - x1[e] * w.y, y1 = x0[e + 1] * w.z - x1[e + 1] * w.w;
         x1[e] = x1[e] * w.x + x0[e] * w.y;
+        x1[e + 1] = x1[e + 1] * w.z + x0[e + 1] * w.w;
         x0[e] = y0;
+        x0[e + 1] = y1;
       }
     }
     if (row_s[t] != INT_MIN) {
@@ -217,18 +244,18 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
       }
     }
     u += HPP;
-    if (u < units) load(u);
   }
 }
 
 }  // namespace
 
-cudaError_t launch_paged_append(const AppendArgs& a, int hd, bool act_bf16, cudaStream_t s) {
+cudaError_t launch_paged_append(const AppendArgs& a, int hd, bool act_bf16, int sms, cudaStream_t s) {
   if (a.n_tokens <= 0) return cudaSuccess;
   const int heads = a.nq + 2 * a.c.nkv;
   const int hpp = kThreads / (hd / 2 / (act_bf16 ? 8 : 4));
-  // a CTA of one token when its heads fill a pass; more tokens for narrow ones
-  const int tb = std::max(1, std::min(kMaxTb, hpp / heads));
+  // a CTA of one token while each finds an SM for itself (4 or so fit one); at least a pass of heads
+  const int narrow = std::max(1, hpp / heads), many = std::min(8, a.n_tokens / (4 * sms));
+  const int tb = std::min(kMaxTb, std::max(narrow, many));
   const int grid = (a.n_tokens + tb - 1) / tb;
   if (hd == 64)
     act_bf16 ? paged_append_kernel<64, true><<<grid, kThreads, 0, s>>>(a, tb)

@@ -10,11 +10,24 @@ import ctypes as C
 
 from . import _binding as B
 
-_FORMATS = {"torch.float32": 0, "torch.bfloat16": 1}  # QW_KV_* and QW_ACT_* alike
+# Filled at the first use: torch's element types, and the raw handle of its current stream
+# (torch.cuda.current_stream builds an object around it, which takes longer than the launch).
+_FORMATS: dict = {}
+_raw_stream = None
+
+
+def _torch():
+    global _raw_stream
+    import torch
+    if not _FORMATS:
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _FORMATS.update({torch.float32: 0, torch.bfloat16: 1})  # QW_KV_* and QW_ACT_* alike
+    return torch
 
 
 def _format(t, what: str) -> int:
-    f = _FORMATS.get(str(t.dtype))
+    f = _FORMATS.get(t.dtype)
     if f is None:
         raise ValueError(f"{what}: float32 or bfloat16 wanted, got {t.dtype}")
     return f
@@ -33,7 +46,7 @@ class PagedKV:
 
     def __init__(self, k_pages, v_pages, page_table, kv_len, q_start, prefix_pages=None,
                  prefix_len: int = 0):
-        import torch
+        torch = _torch()
         if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
             raise ValueError("k_pages and v_pages: two [n_pages, n_kv_heads, page_size, head_dim] "
                              "tensors of one type")
@@ -54,7 +67,7 @@ class PagedKV:
             raise ValueError("prefix_pages do not hold prefix_len keys")
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._keep = (k_pages, v_pages, page_table, kv_len, q_start, prefix_pages)
-        self._ws = None
+        self._ws, self._ws_bytes, self._ws_ptr = [], 0, None
         self._lib = B.lib()
         self.head_dim = k_pages.shape[3]
         self.n_kv_heads = k_pages.shape[1]
@@ -67,39 +80,38 @@ class PagedKV:
             q_start=q_start.data_ptr(), status=self.status.data_ptr(),
             prefix_pages=prefix_pages.data_ptr() if prefix_len > 0 else None)
         self._cref = C.byref(self.c)
+        self._index = self.device.index
+        self._current = torch.cuda.current_device
+        self._int32 = torch.int32
 
-    def _rows(self, t, what: str, width: int, rows=None):
-        """Checks an activation matrix of rows with unit inner stride; (format, row stride)."""
-        f = _format(t, what)
+    def _rows(self, t, what: str, width: int, rows: int):
+        """Row stride of an activation matrix [rows, width] or [rows, heads, head_dim] whose rows
+        are adjacent elements."""
+        shape, inner = t.shape, t.stride()
+        if len(shape) == 3:  # heads back to back
+            ok = shape[1] * shape[2] == width and inner[2] == 1 and (inner[1] == shape[2] or shape[1] == 1)
+        else:
+            ok = len(shape) == 2 and shape[1] == width and inner[1] == 1
+        if not ok or shape[0] != rows:
+            raise ValueError(f"{what}: {rows} rows of {width} adjacent elements wanted, got {tuple(shape)} "
+                             f"with strides {inner}")
         if t.device != self.device:
             raise ValueError(f"{what} is not on the cache's device")
-        inner = t.stride()
-        if t.dim() == 3:  # [rows, heads, head_dim], heads back to back
-            ok = t.shape[1] * t.shape[2] == width and inner[2] == 1 and \
-                (inner[1] == t.shape[2] or t.shape[1] == 1)
-        else:
-            ok = t.dim() == 2 and t.shape[1] == width and inner[1] == 1
-        if not ok or (rows is not None and t.shape[0] != rows):
-            raise ValueError(f"{what}: rows of {width} adjacent elements wanted, got {tuple(t.shape)} "
-                             f"with strides {inner}")
-        return f, (inner[0] if t.shape[0] > 1 else width)
+        return inner[0] if rows > 1 else width
 
-    def _out(self, out, like, n_q_heads: int, fmt: int):
-        import torch
+    def _out(self, out, like, n_q_heads: int):
         if out is None:
-            return torch.zeros(like.shape[0], n_q_heads, self.head_dim, dtype=like.dtype,
-                               device=self.device)
+            return _torch().zeros(like.shape[0], n_q_heads, self.head_dim, dtype=like.dtype,
+                                  device=self.device)
         width = n_q_heads * self.head_dim
-        f, ld = self._rows(out, "out", width, like.shape[0])
-        if f != fmt or ld != width:
+        if out.dtype != like.dtype or self._rows(out, "out", width, like.shape[0]) != width:
             raise ValueError("out: contiguous rows of the input's type wanted")
         return out
 
     def _stream(self):
-        import torch
-        if torch.cuda.current_device() != self.device.index:
+        if self._current() != self._index:
             raise ValueError("the cache's device is not the current one")
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(self._index)
 
     def append(self, qkv, n_q_heads: int, q_norm=None, k_norm=None, eps: float = 1e-6,
                rope_theta: float = 1e6, positions=None, sections=None, out=None):
@@ -110,15 +122,16 @@ class PagedKV:
         sections = (pairs of axis 0, 1, 2), or None for each token's place in the cache.
         """
         n = qkv.shape[0]
-        fmt, ld = self._rows(qkv, "qkv", (n_q_heads + 2 * self.n_kv_heads) * self.head_dim)
-        out = self._out(out, qkv, n_q_heads, fmt)
+        fmt = _format(qkv, "qkv")
+        ld = self._rows(qkv, "qkv", (n_q_heads + 2 * self.n_kv_heads) * self.head_dim, n)
+        out = self._out(out, qkv, n_q_heads)
         for t in (q_norm, k_norm):
             if t is not None and (t.element_size() != 2 or t.shape != (self.head_dim,) or
-                                  not t.is_contiguous() or t.device != self.device):
+                                  t.stride(0) != 1 or t.device != self.device):
                 raise ValueError("q_norm and k_norm: bfloat16 [head_dim] on the cache's device")
         if positions is not None:
             want = (n, 3) if sections is not None else (n,)
-            if str(positions.dtype) != "torch.int32" or positions.shape != want or \
+            if positions.dtype != self._int32 or positions.shape != want or \
                     not positions.is_contiguous() or positions.device != self.device:
                 raise ValueError(f"positions: contiguous int32 {want} wanted")
         sec = (C.c_int32 * 3)(*sections) if sections is not None else None
@@ -135,23 +148,39 @@ class PagedKV:
     def attend(self, q, max_new: int = 1, out=None):
         """Attention of the tokens' rotated queries [n_tokens, n_q_heads, head_dim] over their
         sequences' keys (and the shared prefix). max_new: the most new tokens of one sequence.
-        The workspace is the cache's own: calls of one PagedKV must not overlap on the GPU."""
-        import torch
+        The workspace is the cache's own: calls of one PagedKV (captured ones too) must not overlap on
+        the GPU, and it has to exist before a capture: call once before, or ``reserve``."""
         n = q.shape[0]
         width = q.shape[1] * q.shape[2] if q.dim() == 3 else q.shape[1]
         heads = width // self.head_dim
-        fmt, ld = self._rows(q, "q", heads * self.head_dim)
-        out = self._out(out, q, heads, fmt)
+        fmt = _format(q, "q")
+        ld = self._rows(q, "q", heads * self.head_dim, n)
+        out = self._out(out, q, heads)
         need = self._lib.qw_paged_attention_workspace_bytes(n, heads, self.head_dim,
                                                             self.c.prefix_len)
-        if self._ws is None or self._ws.numel() < need:
-            self._ws = torch.zeros(max(need, 1), dtype=torch.uint8, device=self.device)
+        if self._ws_bytes < need:
+            self._grow(need)
         rc = self._lib.qw_paged_attention(self._cref, q.data_ptr(), fmt, ld, n, heads, max_new,
-                                          out.data_ptr(), self._ws.data_ptr(), self._ws.numel(),
-                                          self._stream())
+                                          out.data_ptr(), self._ws_ptr, self._ws_bytes, self._stream())
         if rc:
             B.check("qw_paged_attention", rc)
         return out
+
+    def reserve(self, n_tokens: int, n_q_heads: int) -> None:
+        """Workspace for attention calls of up to n_tokens rows (as the first such call would)."""
+        need = self._lib.qw_paged_attention_workspace_bytes(n_tokens, n_q_heads, self.head_dim,
+                                                            self.c.prefix_len)
+        if self._ws_bytes < need:
+            self._grow(need)
+
+    def _grow(self, need: int) -> None:
+        torch = _torch()
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("the attention workspace is too small and cannot be made inside a graph "
+                               "capture: call reserve(n_tokens, n_q_heads) before it")
+        # smaller ones are kept: a captured graph may hold their address
+        self._ws.append(torch.zeros(need, dtype=torch.uint8, device=self.device))
+        self._ws_bytes, self._ws_ptr = need, self._ws[-1].data_ptr()
 
     def check(self) -> None:
         """Raises if a call so far met a bad page id or length or gave up a wait (synchronises)."""

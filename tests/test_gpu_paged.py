@@ -315,6 +315,27 @@ def test_captured_graph_replays_with_new_lengths():
     c.check()
 
 
+def test_capture_needs_its_workspace_and_keeps_it():
+    b = Batch([(1, 200), (1, 17)], 4, 2, 64, 16, "f32", "bf16", seed=73)
+    c = b.cache()
+    q, out = b.q.cuda(), torch.zeros(2, 4, 64, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with pytest.raises(RuntimeError, match="reserve"):
+        with torch.cuda.graph(g):
+            c.attend(q, out=out)
+    torch.cuda.synchronize()
+    c.reserve(2, 4)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.attend(q, out=out)
+    c.reserve(4096, 4)                            # a larger one must not take the graph's away
+    filler = [torch.full((1 << 20,), 7, dtype=torch.uint8, device="cuda") for _ in range(64)]
+    g.replay()
+    attend_close(b, out)
+    attend_close(b, c.attend(q))
+    del filler
+
+
 def test_other_streams():
     b = Batch([(1, 500), (1, 3)], 8, 2, 128, 16, "bf16", "bf16", seed=43)
     c = b.cache()

@@ -62,7 +62,7 @@ def test_short_struct(L):
 
 
 @pytest.mark.parametrize("bad", [dict(act=2), dict(n=-1), dict(nq=0), dict(qkv=None), dict(out=None),
-                                 dict(qn=16), dict(kn=16), dict(ld=8 * 64 - 1), dict(ld=8 * 64 + 1),
+                                 dict(qn=16), dict(kn=16), dict(qn=16, kn=18), dict(ld=8 * 64 - 1), dict(ld=8 * 64 + 1),
                                  dict(qkv=24), dict(out=8), dict(theta=0.0), dict(theta=float("inf")),
                                  dict(theta=float("nan")), dict(eps=-1.0), dict(sec=(8, 8, 16)),
                                  dict(sec=(8, 8, 8), pos=16), dict(sec=(-8, 20, 20), pos=16)])
