@@ -45,12 +45,12 @@ struct PgLayout {
   static constexpr uint32_t kTile = (uint32_t)KT * HD * ES;     // K or V of one stage
   static constexpr int kStages = kRing / (2 * kTile);
   static constexpr uint32_t off_join = kRing;
-  static constexpr uint32_t off_ml = off_join + 2u * R * HD * 4;  // [warps][R] (m, l)
+  static constexpr uint32_t off_ml = off_join + 2u * R * HD * 4 + R * 4;  // [warps][R] (m, l)
   static constexpr uint32_t off_row = off_ml + kConsumers * R * 8;  // [R] joined (m, l)
   static constexpr uint32_t off_start = off_row + R * 8;
-  static constexpr uint32_t off_bar = off_start + 64 + 48;
+  static constexpr uint32_t off_bar = off_start + 96 + 48;
   static constexpr uint32_t bytes = off_bar + 2u * kStages * 8;
-  static_assert(sizeof(PagedStart) <= 64, "start words");
+  static_assert(sizeof(PagedStart) <= 96, "start words");
 };
 
 __device__ __forceinline__ void consumer_sync() {
@@ -132,10 +132,9 @@ __device__ __forceinline__ void produce(const PagedAttnArgs& a, const CUtensorMa
 // ------------------------------------------------------------------ end of an item's segment
 // The four warps' records are in join[0] + join[1] (o) and row_ml (m, l). A whole item is emitted;
 // a split one goes to this CTA's slot and the last CTA to arrive joins all of them in order.
-template <int HD, int KT, int R>
+template <int HD, int R>
 __device__ __forceinline__ void finish_segment(const PagedAttnArgs& a, const PagedCursor& c,
-                                               const float* join, const float2* row_ml,
-                                               int* flag) {
+                                               float* join, float2* row_ml, int* flag) {
   const int tid = threadIdx.x;
   constexpr int V4 = HD / 4, N = R * V4;
   const int tok0 = c.rt * a.tpt, ntok = min(a.tpt, c.s.nb - tok0), rows = ntok * a.gq;
@@ -157,7 +156,7 @@ __device__ __forceinline__ void finish_segment(const PagedAttnArgs& a, const Pag
     }
     return;
   }
-  const int c0 = c.first_cta<KT>(), c1 = c.last_cta<KT>();
+  const int c0 = c.first_cta(), c1 = c.last_cta();
   const size_t slot = (size_t)(2 * blockIdx.x + (c.first() ? 1 : 0)) * a.slots.rows;
   for (int i = tid; i < rows * V4; i += kConsumers * 32)
     __stcg(reinterpret_cast<float4*>(a.slots.o + slot * HD) + i, local(i));
@@ -175,14 +174,76 @@ __device__ __forceinline__ void finish_segment(const PagedAttnArgs& a, const Pag
     *flag = last;
   }
   consumer_sync();
-  if (*flag) {
-    __threadfence();
-    for (int i = tid; i < rows * V4; i += kConsumers * 32) {
-      const int r = i / V4, d = (i % V4) * 4;
-      PagedAcc acc;
-      paged_join_slots<HD>(a.slots, c0, c1, r, d, acc);
-      paged_emit(a, HD, c.s.lo + tok0 + r / a.gq, c.kvh * a.gq + r % a.gq, d, acc);
+  if (!*flag) return;
+  __threadfence();
+  // The last CTA: weights of a batch of records in shared memory (a warp per row), then every
+  // thread sums its columns over the batch with all loads of eight records in flight.
+  constexpr int NB = 2 * HD, WR = R < kConsumers ? 1 : R / kConsumers, NI = (N + 127) / 128;
+  const int warp = tid >> 5, lane = tid & 31;
+  float* wgt = join;  // [records][R]
+  PagedAcc acc[NI];
+  for (int x0 = c0; x0 <= c1; x0 += NB) {
+    const int nb = min(NB, c1 + 1 - x0);
+    if (x0 > c0) consumer_sync();
+#pragma unroll
+    for (int j = 0; j < WR; ++j) {
+      const int r = warp + j * kConsumers;
+      if (r >= R) break;
+      float2 ml[NB / 32];
+      float top = x0 > c0 ? row_ml[r].x : -INFINITY;
+      const float old = top;
+#pragma unroll
+      for (int k = 0; k < NB / 32; ++k) {
+        const int x = x0 + 32 * k + lane;
+        ml[k] = make_float2(-INFINITY, 0.f);
+        if (32 * k + lane < nb && r < rows) ml[k] = __ldcg(a.slots.ml + (size_t)(2 * x + (x == c0)) * R + r);
+        top = fmaxf(top, ml[k].x);
+      }
+      top = warp_max(top);
+      const float mu = top == -INFINITY ? 0.f : top;
+      float den = 0.f;
+#pragma unroll
+      for (int k = 0; k < NB / 32; ++k) {
+        if (32 * k >= nb) break;
+        const float w = paged_exp2(ml[k].x - mu);
+        if (32 * k + lane < nb) wgt[(32 * k + lane) * R + r] = w;
+        den = fmaf(w, ml[k].y, den);
+      }
+      den = warp_sum(den);
+      __syncwarp();
+      if (lane == 0) {  // y: the sum; the batches before are scaled by 2^(old - top)
+        if (x0 > c0) den = fmaf(row_ml[r].y, paged_exp2(old - mu), den);
+        row_ml[r] = make_float2(top, den);
+      }
+      if (x0 > c0 && lane == 0) wgt[nb * R + r] = paged_exp2(old - mu);
     }
+    consumer_sync();
+#pragma unroll
+    for (int k = 0; k < NI; ++k) {
+      const int i = tid + 128 * k, r = i / V4;
+      if (x0 > c0 && i < rows * V4) {
+        const float f = wgt[nb * R + r];
+        acc[k].o.x *= f, acc[k].o.y *= f, acc[k].o.z *= f, acc[k].o.w *= f;
+      }
+    }
+#pragma unroll 8
+    for (int x = 0; x < nb; ++x) {
+      const size_t sl = (size_t)(2 * (x0 + x) + (x0 + x == c0)) * R * HD;
+#pragma unroll
+      for (int k = 0; k < NI; ++k) {
+        const int i = tid + 128 * k;
+        if (i < rows * V4)
+          acc[k].add(wgt[x * R + i / V4], 0.f, __ldcg(reinterpret_cast<const float4*>(a.slots.o + sl) + i));
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < NI; ++k) {
+    const int i = tid + 128 * k, r = i / V4;
+    if (i >= rows * V4) break;
+    acc[k].m = row_ml[r].x;
+    acc[k].l = row_ml[r].y;
+    paged_emit(a, HD, c.s.lo + tok0 + r / a.gq, c.kvh * a.gq + r % a.gq, (i % V4) * 4, acc[k]);
   }
 }
 
@@ -202,7 +263,7 @@ __device__ __forceinline__ bool open_cta(const PagedAttnArgs& a, uint8_t* sm) {
     if (a.prefix_pass) a.splits[blockIdx.x].c1 = -1;
   }
   if (a.prefix_pass) pdl_launch_dependents();
-  paged_find_start<KT, kThreads>(a, st, reinterpret_cast<long long*>(sm + LY::off_start + 64));
+  paged_find_start<KT, kThreads>(a, st, reinterpret_cast<long long*>(sm + LY::off_start + 96));
   return st->any;
 }
 
@@ -284,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   float* join = reinterpret_cast<float*>(sm + LY::off_join);
   float2* ml_s = reinterpret_cast<float2*>(sm + LY::off_ml);
   float2* row_ml = reinterpret_cast<float2*>(sm + LY::off_row);
-  int* flag = reinterpret_cast<int*>(sm + LY::off_start + 64 + 40);
+  int* flag = reinterpret_cast<int*>(sm + LY::off_start + 96 + 40);
 
   const int g = lane >> 2, q2 = (lane & 3) * 2;
   // ldmatrix rows of this lane. K (plain): keys 16 warp + (matrix / 2) * 8 + row, chunk matrix % 2.
@@ -338,9 +399,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (!bad)
         bad = !__all_sync(0xffffffffu, mbar_wait(&full[stage], (uint32_t)((seen / NS) & 1), a.wait_ns));
       const uint32_t kb = ring + (uint32_t)stage * 2 * LY::kTile, vb = kb + LY::kTile;
-      float s[2][4];
+      float s[2][4], s2[2][4];  // even and odd k-steps: two chains of mma
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[0][i] = s[1][i] = 0.f;
+      for (int i = 0; i < 4; ++i) s[0][i] = s[1][i] = s2[0][i] = s2[1][i] = 0.f;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         const int ch = ks * 2 + kch;  // 16-byte chunk of the row; 8 of them per column block
@@ -348,10 +409,17 @@ __global__ void __launch_bounds__(kThreads, 2)
         ldsm4(kb + (ch >> 3) * (KT * 128) + krow * 128 + (((ch & 7) ^ (krow & 7)) << 4), kf);
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
-          mma16816(s[nt], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], kf[2 * nt], kf[2 * nt + 1]);
-          if constexpr (NT == 3) mma16816(s[nt], ql[ks][0], 0u, ql[ks][1], 0u, kf[2 * nt], kf[2 * nt + 1]);
+          float(&d)[4] = ks & 1 ? s2[nt] : s[nt];
+          mma16816(d, qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], kf[2 * nt], kf[2 * nt + 1]);
+        }
+        if constexpr (NT == 3) {
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+            mma16816(ks & 1 ? s[nt] : s2[nt], ql[ks][0], 0u, ql[ks][1], 0u, kf[2 * nt], kf[2 * nt + 1]);
         }
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[0][i] += s2[0][i], s[1][i] += s2[1][i];
       const int k0 = (c.kt + x) * KT + 16 * warp;  // this warp's first key
       const bool edge = k0 + 16 > c.limit - a.tpt;  // keys some row does not see
       float p[NRW][4];
@@ -457,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     consumer_sync();
     if (warp < 2) put(true);
     consumer_sync();
-    finish_segment<HD, KT, R>(a, c, join, row_ml, flag);
+    finish_segment<HD, R>(a, c, join, row_ml, flag);
     consumer_sync();  // join and row_ml are free again
   } while (c.next<KT>(a));
   if (bad && lane == 0 && a.c.status) atomicOr(a.c.status, PG_TIMEOUT);
@@ -501,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   float* join = reinterpret_cast<float*>(sm + LY::off_join);
   float2* ml_s = reinterpret_cast<float2*>(sm + LY::off_ml);
   float2* row_ml = reinterpret_cast<float2*>(sm + LY::off_row);
-  int* flag = reinterpret_cast<int*>(sm + LY::off_start + 64 + 40);
+  int* flag = reinterpret_cast<int*>(sm + LY::off_start + 96 + 40);
 
   PagedCursor c = paged_cursor<KT>(a, st);
   int seen = 0;
@@ -607,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     consumer_sync();
     if (warp < 2) put(true);
     consumer_sync();
-    finish_segment<HD, KT, R>(a, c, join, row_ml, flag);
+    finish_segment<HD, R>(a, c, join, row_ml, flag);
     consumer_sync();
   } while (c.next<KT>(a));
   if (bad && lane == 0 && a.c.status) atomicOr(a.c.status, PG_TIMEOUT);

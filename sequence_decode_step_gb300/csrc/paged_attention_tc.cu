@@ -76,11 +76,12 @@ struct TcLayout {
   static constexpr int kSlots = (224 * 1024 - kQ) / kTile > 10 ? 10 : (224 * 1024 - kQ) / kTile;
   static constexpr uint32_t off_ring = kQ;
   static constexpr uint32_t off_start = off_ring + kSlots * kTile;
-  static constexpr uint32_t off_bar = off_start + 64 + 128;
+  static constexpr uint32_t off_bar = off_start + 96 + 128;
   static constexpr int kBars = 2 * kSlots + 10;
   static constexpr uint32_t off_tmem = off_bar + kBars * 8;
   static constexpr uint32_t bytes = off_tmem + 16;
   static constexpr uint32_t t_o = 256, t_x = 384;          // TMEM columns (t_x: NT = 3)
+  static_assert(sizeof(PagedStart) <= 96, "start words");
   static_assert(bytes <= 227 * 1024, "tiles fit one CTA's shared memory");
 };
 
@@ -132,7 +133,7 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  paged_find_start<KT, LY::kThreads>(a, st, reinterpret_cast<long long*>(sm + LY::off_start + 64));
+  paged_find_start<KT, LY::kThreads>(a, st, reinterpret_cast<long long*>(sm + LY::off_start + 96));
   tc_fence_after();
   const uint32_t tb = *tslot;
   const int half = 128 / a.gq;  // tokens of a row tile
@@ -577,7 +578,7 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
         tc_fence_before();
       }
       if (!whole && first && s == 0 && r == 0)  // the joining kernel's work
-        a.splits[blockIdx.x] = PagedSplit{c.last_cta<KT>(), c.s.lo + c.rt * a.tpt,
+        a.splits[blockIdx.x] = PagedSplit{c.last_cta(), c.s.lo + c.rt * a.tpt,
                                           min(a.tpt, c.s.nb - c.rt * a.tpt) * a.gq, c.kvh * a.gq};
       tiles += n;
     } while (c.next<KT>(a));

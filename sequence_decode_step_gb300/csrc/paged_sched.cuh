@@ -12,7 +12,7 @@
 // of their own (many rows: one CTA would read them for 5-10 us).
 //
 // An item costs a CTA some tiles beside its keys (q, the join, the output), so on the line it is
-// that much longer (paged_item_units); the units before its first tile are empty.
+// that much longer (kPagedItemUnits); the units before its first tile are empty.
 //
 // The shared prefix is the same line with one pseudo-sequence: all the batch's tokens, every one
 // of which sees all prefix_len keys.
@@ -22,12 +22,9 @@
 
 namespace qw {
 
-// Tiles that an item's q, first product and output take: 4 us against 1.5 us for a tensor-core tile
-// of 128 keys, about one tile of 32 or 64 keys elsewhere.
-template <int KT>
-__host__ __device__ constexpr int paged_item_units() {
-  return KT == kPagedTcKeys ? 3 : 1;
-}
+// Tiles that an item's q, first product, join and output take: about 4 us, against 1.2 us for a
+// CTA's tile of 32 KB while HBM is the bound and 1.5 us for a tensor-core tile of 128 keys.
+constexpr int kPagedItemUnits = 3;
 constexpr int kPagedLeastUnits = 2;  // least share of a CTA: fewer records of a short line to join
 
 // Quotient of two line positions: 32-bit where both fit, as they do for any real batch.
@@ -75,7 +72,7 @@ __device__ __forceinline__ int paged_tiles(int limit) {
 template <int KT>
 __device__ __forceinline__ long long paged_head_units(const PagedAttnArgs& a, const PagedSeq& s) {
   long long n = 0;
-  for (int rt = 0; rt < s.nrt; ++rt) n += paged_item_units<KT>() + paged_tiles<KT>(paged_limit(a, s, rt));
+  for (int rt = 0; rt < s.nrt; ++rt) n += kPagedItemUnits + paged_tiles<KT>(paged_limit(a, s, rt));
   return n;
 }
 
@@ -89,25 +86,21 @@ struct PagedCursor {  // a place on the line
   __device__ __forceinline__ bool first() const { return kt == 0; }
   __device__ __forceinline__ bool whole() const { return kt == 0 && kend == nkt; }
   // CTAs that share the item's tiles
-  template <int KT>
-  __device__ __forceinline__ int first_cta() const {
-    return (int)paged_div(item + paged_item_units<KT>(), per);
-  }
-  template <int KT>
+  __device__ __forceinline__ int first_cta() const { return (int)paged_div(item + kPagedItemUnits, per); }
   __device__ __forceinline__ int last_cta() const {
-    return (int)paged_div(item + paged_item_units<KT>() + nkt - 1, per);
+    return (int)paged_div(item + kPagedItemUnits + nkt - 1, per);
   }
   template <int KT>
   __device__ __forceinline__ void enter(const PagedAttnArgs& a) {
     limit = paged_limit(a, s, rt);
     nkt = paged_tiles<KT>(limit);
-    kend = (int)min((long long)nkt, u1 - item - paged_item_units<KT>());
+    kend = (int)min((long long)nkt, u1 - item - kPagedItemUnits);
   }
   // To the CTA's next item; false when its share ends before that item's first tile.
   template <int KT>
   __device__ __forceinline__ bool next(const PagedAttnArgs& a) {
-    item += paged_item_units<KT>() + nkt;
-    if (item + paged_item_units<KT>() >= u1) return false;
+    item += kPagedItemUnits + nkt;
+    if (item + kPagedItemUnits >= u1) return false;
     kt = 0;
     if (++rt == s.nrt) {
       rt = 0;
@@ -126,6 +119,7 @@ struct PagedStart {  // in shared memory: where this CTA starts
   long long item, u1, per;
   int b, kvh, rt, kt;
   int any;           // 0: nothing to do
+  PagedSeq s;
 };
 
 // Block-wide: fills *st. warp_sums: one long long per warp.
@@ -136,10 +130,12 @@ __device__ void paged_find_start(const PagedAttnArgs& a, PagedStart* st, long lo
   const int spt = (n + THREADS - 1) / THREADS;
   const int b0 = min((int)threadIdx.x * spt, n), b1 = min(b0 + spt, n);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long mine = 0;
+  long long mine = 0, hu = 0;  // units of this thread's sequences; per KV head of the last one
+  PagedSeq s;
   for (int b = b0; b < b1; ++b) {
-    const PagedSeq s = paged_seq(a, b);
-    mine += paged_head_units<KT>(a, s) * a.c.nkv;
+    s = paged_seq(a, b);
+    hu = paged_head_units<KT>(a, s);
+    mine += hu * a.c.nkv;
   }
   long long scan = mine;
 #pragma unroll
@@ -161,18 +157,20 @@ __device__ void paged_find_start(const PagedAttnArgs& a, PagedStart* st, long lo
   if (u0 < total && before <= u0 && u0 < before + mine) {
     long long r = u0 - before;
     int b = b0;
-    PagedSeq s = paged_seq(a, b);
-    long long hu = paged_head_units<KT>(a, s);
-    while (r >= hu * a.c.nkv) {
-      r -= hu * a.c.nkv;
-      s = paged_seq(a, ++b);
+    if (b1 - b0 > 1) {
+      s = paged_seq(a, b);
       hu = paged_head_units<KT>(a, s);
+      while (r >= hu * a.c.nkv) {
+        r -= hu * a.c.nkv;
+        s = paged_seq(a, ++b);
+        hu = paged_head_units<KT>(a, s);
+      }
     }
     const int kvh = (int)paged_div(r, hu);
     r -= hu * kvh;
     int rt = 0;
     for (;; ++rt) {
-      const int t = paged_item_units<KT>() + paged_tiles<KT>(paged_limit(a, s, rt));
+      const int t = kPagedItemUnits + paged_tiles<KT>(paged_limit(a, s, rt));
       if (r < t) break;
       r -= t;
     }
@@ -182,8 +180,9 @@ __device__ void paged_find_start(const PagedAttnArgs& a, PagedStart* st, long lo
     st->b = b;
     st->kvh = kvh;
     st->rt = rt;
-    st->kt = max((int)r - paged_item_units<KT>(), 0);
-    st->any = u0 - r + paged_item_units<KT>() < st->u1;  // the share has a tile
+    st->s = s;
+    st->kt = max((int)r - kPagedItemUnits, 0);
+    st->any = u0 - r + kPagedItemUnits < st->u1;  // the share has a tile
   }
   __syncthreads();
 }
@@ -198,7 +197,7 @@ __device__ __forceinline__ PagedCursor paged_cursor(const PagedAttnArgs& a, cons
   c.kvh = st->kvh;
   c.rt = st->rt;
   c.kt = st->kt;
-  c.s = paged_seq(a, c.b);
+  c.s = st->s;
   c.enter<KT>(a);
   return c;
 }
