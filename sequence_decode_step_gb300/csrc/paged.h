@@ -6,6 +6,24 @@
 
 namespace qw {
 
+// A launch that may start while the kernel before it in the stream still runs; the kernel waits for
+// that one's end itself (griddepcontrol.wait).
+template <class... P, class... Args>
+cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, int threads, uint32_t smem, cudaStream_t s,
+                       const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // Bits of the caller's status word (the QW_PAGED_* values of qw.h).
 enum : int { PG_TIMEOUT = 1, PG_BAD_PAGE = 2, PG_BAD_LENGTH = 4 };
 
@@ -89,7 +107,7 @@ cudaError_t set_paged_attributes();
 // ---- tensor-core tiles (paged_attention_tc.cu) ----
 constexpr int kPagedTcKeys = 128;  // keys per tile
 int paged_tc_rows(bool act_bf16);  // query rows per item
-cudaError_t launch_paged_tc(const PagedAttnArgs& a, int hd, int grid, bool pdl, cudaStream_t s);
+cudaError_t launch_paged_tc(const PagedAttnArgs& a, int hd, int grid, cudaStream_t s);
 // Joins the records of the items that the launch before it (`grid` CTAs) has split.
 cudaError_t launch_paged_join(const PagedAttnArgs& a, int hd, int grid, int item_rows, cudaStream_t s);
 cudaError_t set_paged_tc_attributes();

@@ -122,6 +122,8 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
   const int sub = threadIdx.x % LPH, j0 = sub * V;
   const int page = 1 << a.c.page_shift;
 
+  pdl_wait();
+  pdl_launch_dependents();
   // the first unit's loads leave before the lookups below
   int u = threadIdx.x / LPH;
   uint4 n0, n1;
@@ -258,14 +260,10 @@ cudaError_t launch_paged_append(const AppendArgs& a, int hd, bool act_bf16, int 
   const int tb = std::min(kMaxTb, std::max(narrow, many));
   const int grid = (a.n_tokens + tb - 1) / tb;
   if (hd == 64)
-    act_bf16 ? paged_append_kernel<64, true><<<grid, kThreads, 0, s>>>(a, tb)
-             : paged_append_kernel<64, false><<<grid, kThreads, 0, s>>>(a, tb);
-  else if (hd == 128)
-    act_bf16 ? paged_append_kernel<128, true><<<grid, kThreads, 0, s>>>(a, tb)
-             : paged_append_kernel<128, false><<<grid, kThreads, 0, s>>>(a, tb);
-  else
-    return cudaErrorInvalidValue;
-  return cudaGetLastError();
+    return act_bf16 ? launch_pdl(paged_append_kernel<64, true>, dim3(grid), kThreads, 0, s, a, tb)
+                    : launch_pdl(paged_append_kernel<64, false>, dim3(grid), kThreads, 0, s, a, tb);
+  return act_bf16 ? launch_pdl(paged_append_kernel<128, true>, dim3(grid), kThreads, 0, s, a, tb)
+                  : launch_pdl(paged_append_kernel<128, false>, dim3(grid), kThreads, 0, s, a, tb);
 }
 
 }  // namespace qw

@@ -130,6 +130,15 @@ __device__ __forceinline__ void produce(const PagedAttnArgs& a, const CUtensorMa
 }
 
 // ------------------------------------------------------------------ end of an item's segment
+// A load that stays in front of what follows it (the compiler moves plain ones down to their uses,
+// one round trip each).
+__device__ __forceinline__ float4 ld_first(const float4* p) {
+  float4 v;
+  asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "l"(p));
+  return v;
+}
 // The four warps' records are in join[0] + join[1] (o) and row_ml (m, l). A whole item is emitted;
 // a split one goes to this CTA's slot and the last CTA to arrive joins all of them in order.
 template <int HD, int R>
@@ -177,7 +186,7 @@ __device__ __forceinline__ void finish_segment(const PagedAttnArgs& a, const Pag
   if (!*flag) return;
   __threadfence();
   // The last CTA: weights of a batch of records in shared memory (a warp per row), then every
-  // thread sums its columns over the batch with all loads of eight records in flight.
+  // thread sums its columns over the batch with 16 loads in flight.
   constexpr int NB = 2 * HD, WR = R < kConsumers ? 1 : R / kConsumers, NI = (N + 127) / 128;
   const int warp = tid >> 5, lane = tid & 31;
   float* wgt = join;  // [records][R]
@@ -226,14 +235,23 @@ __device__ __forceinline__ void finish_segment(const PagedAttnArgs& a, const Pag
         acc[k].o.x *= f, acc[k].o.y *= f, acc[k].o.z *= f, acc[k].o.w *= f;
       }
     }
-#pragma unroll 8
-    for (int x = 0; x < nb; ++x) {
-      const size_t sl = (size_t)(2 * (x0 + x) + (x0 + x == c0)) * R * HD;
+    constexpr int NL = 16 / NI;  // records per round of loads
+    const float4* o = reinterpret_cast<const float4*>(a.slots.o + (size_t)2 * x0 * R * HD);
+    for (int x = 0; x < nb; x += NL) {
+      float4 v[NL][NI];
 #pragma unroll
-      for (int k = 0; k < NI; ++k) {
-        const int i = tid + 128 * k;
-        if (i < rows * V4)
-          acc[k].add(wgt[x * R + i / V4], 0.f, __ldcg(reinterpret_cast<const float4*>(a.slots.o + sl) + i));
+      for (int y = 0; y < NL; ++y) {
+        const int xx = min(x + y, nb - 1);  // (no branch between the loads)
+        const float4* rec = o + (size_t)(2 * xx + (x0 + xx == c0)) * (R * V4);
+#pragma unroll
+        for (int k = 0; k < NI; ++k) v[y][k] = ld_first(rec + min(tid + 128 * k, N - 1));
+      }
+#pragma unroll
+      for (int y = 0; y < NL; ++y) {
+        if (x + y >= nb) break;
+#pragma unroll
+        for (int k = 0; k < NI; ++k)
+          acc[k].add(wgt[(x + y) * R + min((tid + 128 * k) / V4, R - 1)], 0.f, v[y][k]);
       }
     }
   }
@@ -260,9 +278,9 @@ __device__ __forceinline__ bool open_cta(const PagedAttnArgs& a, uint8_t* sm) {
       mbar_init(&empty[i], kConsumers);
     }
     fence_barrier_init();
-    if (a.prefix_pass) a.splits[blockIdx.x].c1 = -1;
   }
-  if (a.prefix_pass) pdl_launch_dependents();
+  paged_pdl_open(a);
+  if (a.prefix_pass && threadIdx.x == 0) a.splits[blockIdx.x].c1 = -1;
   paged_find_start<KT, kThreads>(a, st, reinterpret_cast<long long*>(sm + LY::off_start + 96));
   return st->any;
 }
@@ -681,23 +699,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (bad && lane == 0 && a.c.status) atomicOr(a.c.status, PG_TIMEOUT);
 }
 
-// One launch; with `pdl` it may start while the launch before it (the prefix's) still runs.
-template <class K, class... Args>
-cudaError_t launch(K kernel, int grid, uint32_t smem, bool pdl, cudaStream_t s, const Args&... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
 template <int HD, int NT>
-cudaError_t launch_mma(const PagedAttnArgs& a, int grid, bool pdl, cudaStream_t s) {
+cudaError_t launch_mma(const PagedAttnArgs& a, int grid, cudaStream_t s) {
   constexpr int R = NT == 1 ? 16 : 8;
   CUtensorMap tk, tv;
   const uint64_t rows = (uint64_t)a.c.n_pages * a.c.nkv << a.c.page_shift;
@@ -705,20 +708,21 @@ cudaError_t launch_mma(const PagedAttnArgs& a, int grid, bool pdl, cudaStream_t 
   if (!make_tmap_bf16_2d(&tk, a.c.k_pages, rows, HD, box) ||
       !make_tmap_bf16_2d(&tv, a.c.v_pages, rows, HD, box))
     return cudaErrorInvalidValue;
-  return launch(paged_attn_mma_kernel<HD, NT>, grid, PgLayout<HD, 64, 2, R>::bytes, pdl, s, a, tk, tv);
+  return launch_pdl(paged_attn_mma_kernel<HD, NT>, dim3(grid), kThreads, PgLayout<HD, 64, 2, R>::bytes, s,
+                    a, tk, tv);
 }
 template <int HD, int R>
-cudaError_t launch_fma(const PagedAttnArgs& a, int grid, bool pdl, cudaStream_t s) {
-  return launch(paged_attn_fma_kernel<HD, R>, grid, PgLayout<HD, 32, 4, R>::bytes, pdl, s, a);
+cudaError_t launch_fma(const PagedAttnArgs& a, int grid, cudaStream_t s) {
+  return launch_pdl(paged_attn_fma_kernel<HD, R>, dim3(grid), kThreads, PgLayout<HD, 32, 4, R>::bytes, s, a);
 }
 template <int HD>
-cudaError_t launch_pass(const PagedAttnArgs& a, const PagedPlan& p, bool pdl, cudaStream_t s) {
-  if (p.tc) return launch_paged_tc(a, HD, p.grid, pdl, s);
+cudaError_t launch_pass(const PagedAttnArgs& a, const PagedPlan& p, cudaStream_t s) {
+  if (p.tc) return launch_paged_tc(a, HD, p.grid, s);
   if (a.c.kv_bf16)
-    return a.act_bf16 ? launch_mma<HD, 1>(a, p.grid, pdl, s) : launch_mma<HD, 3>(a, p.grid, pdl, s);
-  if (p.rows == 2) return launch_fma<HD, 2>(a, p.grid, pdl, s);
-  if (p.rows == 4) return launch_fma<HD, 4>(a, p.grid, pdl, s);
-  return launch_fma<HD, 8>(a, p.grid, pdl, s);
+    return a.act_bf16 ? launch_mma<HD, 1>(a, p.grid, s) : launch_mma<HD, 3>(a, p.grid, s);
+  if (p.rows == 2) return launch_fma<HD, 2>(a, p.grid, s);
+  if (p.rows == 4) return launch_fma<HD, 4>(a, p.grid, s);
+  return launch_fma<HD, 8>(a, p.grid, s);
 }
 
 template <class K>
@@ -799,13 +803,13 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& base, int hd, int max_ne
   const Workspace w(a.n_tokens, a.nq, hd, prefix);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.counters = reinterpret_cast<int*>(ws);
-  auto run = [&](const PagedPlan& p, int i, bool pdl) {
+  auto run = [&](const PagedPlan& p, int i) {
     a.tpt = p.rows > 128 ? 2 * (128 / a.gq) : p.rows / a.gq;
     a.splits = reinterpret_cast<PagedSplit*>(ws + w.splits[i]);
     a.slots.ml = reinterpret_cast<float2*>(ws + w.ml[i]);
     a.slots.o = reinterpret_cast<float*>(ws + w.o[i]);
     a.slots.rows = p.tc ? slot_rows(a.n_tokens) : p.rows;
-    return hd == 64 ? launch_pass<64>(a, p, pdl, s) : launch_pass<128>(a, p, pdl, s);
+    return hd == 64 ? launch_pass<64>(a, p, s) : launch_pass<128>(a, p, s);
   };
   const long long cap = 1 << 20;  // row counts only choose a kernel
   if (prefix) {
@@ -813,13 +817,13 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& base, int hd, int max_ne
     a.pre.o = reinterpret_cast<float*>(ws + w.whole_o);
     a.prefix_pass = 1;
     const PagedPlan p = plan_paged_pass(a, hd, (int)std::min(cap, (long long)a.n_tokens * a.gq), sms);
-    cudaError_t e = run(p, 1, false);
+    cudaError_t e = run(p, 1);
     if (e == cudaSuccess) e = launch_paged_join(a, hd, p.grid, p.rows, s);
     if (e != cudaSuccess) return e;
     a.prefix_pass = 0;
   }
   const int rows = (int)std::min(cap, (long long)std::min(max_new, a.n_tokens) * a.gq);
-  return run(plan_paged_pass(a, hd, rows, sms), 0, prefix);
+  return run(plan_paged_pass(a, hd, rows, sms), 0);
 }
 
 }  // namespace qw

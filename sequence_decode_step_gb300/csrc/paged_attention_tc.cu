@@ -111,7 +111,6 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
   PagedStart* st = reinterpret_cast<PagedStart*>(sm + LY::off_start);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  if (a.prefix_pass) pdl_launch_dependents();
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&kv_full[i], 1);
@@ -126,12 +125,13 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
     }
     mbar_init(done, 1);
     fence_barrier_init();
-    a.splits[blockIdx.x].c1 = -1;
   }
   if (warp == 1) {
     tmem_alloc(tslot, 512);
     tmem_relinquish();
   }
+  paged_pdl_open(a);
+  if (threadIdx.x == 0) a.splits[blockIdx.x].c1 = -1;
   tc_fence_before();
   paged_find_start<KT, LY::kThreads>(a, st, reinterpret_cast<long long*>(sm + LY::off_start + 96));
   tc_fence_after();
@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
 template <int HD>
 __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedAttnArgs a) {
   constexpr int V4 = HD / 4, RB = 128 / V4;
-  if (a.prefix_pass) pdl_launch_dependents();
+  pdl_launch_dependents();
   pdl_wait();
   const PagedSplit sp = a.splits[blockIdx.x];
   const int r = blockIdx.y * RB + threadIdx.x / V4, d = threadIdx.x % V4 * 4;
@@ -608,32 +608,16 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   paged_emit(a, HD, sp.token + r / a.gq, sp.head + r % a.gq, d, acc);
 }
 
-template <class... P, class... Args>
-cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, uint32_t smem, bool pdl, cudaStream_t s,
-                   const Args&... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <int HD, int NT>
-cudaError_t launch_tc(const PagedAttnArgs& a, int grid, bool pdl, cudaStream_t s) {
+cudaError_t launch_tc(const PagedAttnArgs& a, int grid, cudaStream_t s) {
   CUtensorMap tk, tv;
   const uint64_t rows = (uint64_t)a.c.n_pages * a.c.nkv << a.c.page_shift;
   const uint32_t box = std::min(KT, 1 << a.c.page_shift);
   if (!make_tmap_bf16_2d(&tk, a.c.k_pages, rows, HD, box) ||
       !make_tmap_bf16_2d(&tv, a.c.v_pages, rows, HD, box))
     return cudaErrorInvalidValue;
-  cudaError_t e = launch(paged_attn_tc_kernel<HD, NT>, dim3(grid), TcLayout<HD, NT>::kThreads,
-                         TcLayout<HD, NT>::bytes, pdl, s, a, tk, tv);
+  cudaError_t e = launch_pdl(paged_attn_tc_kernel<HD, NT>, dim3(grid), TcLayout<HD, NT>::kThreads,
+                             TcLayout<HD, NT>::bytes, s, a, tk, tv);
   if (e == cudaSuccess && !a.prefix_pass) e = launch_paged_join(a, HD, grid, paged_tc_rows(NT == 1), s);
   return e;
 }
@@ -652,16 +636,16 @@ cudaError_t set_attributes_hd() {
 
 int paged_tc_rows(bool act_bf16) { return act_bf16 ? 256 : 128; }
 
-cudaError_t launch_paged_tc(const PagedAttnArgs& a, int hd, int grid, bool pdl, cudaStream_t s) {
-  if (hd == 64) return a.act_bf16 ? launch_tc<64, 1>(a, grid, pdl, s) : launch_tc<64, 3>(a, grid, pdl, s);
-  return a.act_bf16 ? launch_tc<128, 1>(a, grid, pdl, s) : launch_tc<128, 3>(a, grid, pdl, s);
+cudaError_t launch_paged_tc(const PagedAttnArgs& a, int hd, int grid, cudaStream_t s) {
+  if (hd == 64) return a.act_bf16 ? launch_tc<64, 1>(a, grid, s) : launch_tc<64, 3>(a, grid, s);
+  return a.act_bf16 ? launch_tc<128, 1>(a, grid, s) : launch_tc<128, 3>(a, grid, s);
 }
 
 cudaError_t launch_paged_join(const PagedAttnArgs& a, int hd, int grid, int item_rows, cudaStream_t s) {
   const int rb = 512 / hd;  // rows of a CTA
   const dim3 g(grid, (std::min(item_rows, a.slots.rows) + rb - 1) / rb);
-  return hd == 64 ? launch(paged_join_kernel<64>, g, 128, 0, true, s, a)
-                  : launch(paged_join_kernel<128>, g, 128, 0, true, s, a);
+  return hd == 64 ? launch_pdl(paged_join_kernel<64>, g, 128, 0, s, a)
+                  : launch_pdl(paged_join_kernel<128>, g, 128, 0, s, a);
 }
 
 cudaError_t set_paged_tc_attributes() {

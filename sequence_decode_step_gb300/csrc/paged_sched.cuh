@@ -33,6 +33,15 @@ __device__ __forceinline__ long long paged_div(long long a, long long b) {
   return a / b;
 }
 
+// Programmatic launches: every kernel here may start while the one before it still runs, and waits
+// for its end (griddepcontrol.wait) before it touches memory. The launch over the sequences' own keys
+// behind a prefix waits only before it reads the prefix's records: the prefix's launch lets it start
+// after its own wait, so everything older is done by then.
+__device__ __forceinline__ void paged_pdl_open(const PagedAttnArgs& a) {
+  if (a.prefix_pass || !a.pre.o) pdl_wait();
+  pdl_launch_dependents();
+}
+
 struct PagedSeq {  // one sequence's share of the line
   int lo, nb;      // first token row and tokens
   int base, len;   // keys before the first new token, all keys
