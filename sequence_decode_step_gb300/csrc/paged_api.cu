@@ -189,6 +189,10 @@ extern "C" int qw_paged_attention(const qw_paged_kv* c, const void* q, uint32_t 
   a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)hd));
   a.wait_ns = 1000000000ull;
   e = qw::launch_paged_attention(a, hd, max_new, workspace, sms, (cudaStream_t)stream);
+  if (e == cudaErrorInvalidValue)
+    return fail(QW_ERR_ARG,
+                "qw_paged_attention: tokens x keys beyond what one call counts (n_kv_heads x row tiles x "
+                "key tiles of the longest possible sequences must stay below 2^31), or an unaligned pool");
   if (e != cudaSuccess) return fail(QW_ERR_CUDA, cudaGetErrorString(e));
   return QW_OK;
 }

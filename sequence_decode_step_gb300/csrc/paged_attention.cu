@@ -130,138 +130,82 @@ __device__ __forceinline__ void produce(const PagedAttnArgs& a, const CUtensorMa
 }
 
 // ------------------------------------------------------------------ end of an item's segment
-// A load that stays in front of what follows it (the compiler moves plain ones down to their uses,
-// one round trip each).
-__device__ __forceinline__ float4 ld_first(const float4* p) {
-  float4 v;
-  asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "l"(p));
-  return v;
-}
 // The four warps' records are in join[0] + join[1] (o) and row_ml (m, l). A whole item is emitted;
 // a split one goes to this CTA's slot and the last CTA to arrive joins all of them in order.
 template <int HD, int R>
 __device__ __forceinline__ void finish_segment(const PagedAttnArgs& a, const PagedCursor& c,
-                                               float* join, float2* row_ml, int* flag) {
+                                               uint32_t gmul, const float* join, const float2* row_ml,
+                                               int* flag) {
   const int tid = threadIdx.x;
-  constexpr int V4 = HD / 4, N = R * V4;
-  const int tok0 = c.rt * a.tpt, ntok = min(a.tpt, c.s.nb - tok0), rows = ntok * a.gq;
-  auto local = [&](int i) {
-    const float4 x = *reinterpret_cast<const float4*>(join + i * 4);
-    const float4 y = *reinterpret_cast<const float4*>(join + R * HD + i * 4);
-    return make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-  };
-  if (a.pre.o && !a.prefix_pass) pdl_wait();  // the prefix's records, before any is read
-  if (c.whole()) {
-    for (int i = tid; i < N; i += kConsumers * 32) {
-      const int r = i / V4;
-      if (r >= rows) break;
-      PagedAcc acc;
-      acc.m = row_ml[r].x;
-      acc.l = row_ml[r].y;
-      acc.o = local(i);
-      paged_emit(a, HD, c.s.lo + tok0 + r / a.gq, c.kvh * a.gq + r % a.gq, (i % V4) * 4, acc);
-    }
-    return;
-  }
+  constexpr int V4 = HD / 4;
+  const int tok0 = c.rt * a.tpt, rows = min(a.tpt, c.s.nb - tok0) * a.gq;
   const int c0 = c.first_cta(), c1 = c.last_cta();
-  const size_t slot = (size_t)(2 * blockIdx.x + (c.first() ? 1 : 0)) * a.slots.rows;
-  for (int i = tid; i < rows * V4; i += kConsumers * 32)
-    __stcg(reinterpret_cast<float4*>(a.slots.o + slot * HD) + i, local(i));
-  if (tid < rows) __stcg(a.slots.ml + slot + tid, row_ml[tid]);
-  if (a.prefix_pass) {  // joined by the next launch
-    if (c.first() && tid == 0)
-      a.splits[blockIdx.x] = PagedSplit{c1, c.s.lo + tok0, rows, c.kvh * a.gq};
-    return;
-  }
-  __threadfence();
-  consumer_sync();
-  if (tid == 0) {
-    const int last = atomicAdd(a.counters + c0, 1) == c1 - c0;
-    if (last) a.counters[c0] = 0;  // ready for the next launch
-    *flag = last;
-  }
-  consumer_sync();
-  if (!*flag) return;
-  __threadfence();
-  // The last CTA: weights of a batch of records in shared memory (a warp per row), then every
-  // thread sums its columns over the batch with 16 loads in flight.
-  constexpr int NB = 2 * HD, WR = R < kConsumers ? 1 : R / kConsumers, NI = (N + 127) / 128;
-  const int warp = tid >> 5, lane = tid & 31;
-  float* wgt = join;  // [records][R]
-  PagedAcc acc[NI];
-  for (int x0 = c0; x0 <= c1; x0 += NB) {
-    const int nb = min(NB, c1 + 1 - x0);
-    if (x0 > c0) consumer_sync();
+  const bool whole = c.whole();
+  const size_t slot = (size_t)(2 * blockIdx.x + (c.first() ? 1 : 0)) * R;
+  if (a.pre.o && !a.prefix_pass) pdl_wait();  // the prefix's records, before any is read
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+    for (int i = tid; i < rows * V4; i += kConsumers * 32) {
+      const int r = i / V4, d = (i % V4) * 4;
+      PagedAcc acc;
+      if (pass == 0) {
+        const float4 x = *reinterpret_cast<const float4*>(join + i * 4);
+        const float4 y = *reinterpret_cast<const float4*>(join + R * HD + i * 4);
+        acc.o = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+        acc.m = row_ml[r].x;
+        acc.l = row_ml[r].y;
+        if (!whole) {
+          __stcg(reinterpret_cast<float4*>(a.slots.o + slot * HD) + i, acc.o);
+          if (d == 0) __stcg(a.slots.ml + slot + r, make_float2(acc.m, acc.l));
+          continue;
+        }
+      } else {
+        constexpr int NB = 4;  // records per round of loads
+#pragma unroll 1
+        for (int x = c0; x <= c1; x += NB) {
+          float2 ml[NB];
+          float4 o[NB];
+          float top = acc.m;
 #pragma unroll
-    for (int j = 0; j < WR; ++j) {
-      const int r = warp + j * kConsumers;
-      if (r >= R) break;
-      float2 ml[NB / 32];
-      float top = x0 > c0 ? row_ml[r].x : -INFINITY;
-      const float old = top;
+          for (int y = 0; y < NB; ++y) {
+            const int z = min(x + y, c1);
+            const size_t row = (size_t)(2 * z + (z == c0)) * R + r;
+            ml[y] = __ldcg(a.slots.ml + row);
+            o[y] = __ldcg(reinterpret_cast<const float4*>(a.slots.o + row * HD + d));
+          }
 #pragma unroll
-      for (int k = 0; k < NB / 32; ++k) {
-        const int x = x0 + 32 * k + lane;
-        ml[k] = make_float2(-INFINITY, 0.f);
-        if (32 * k + lane < nb && r < rows) ml[k] = __ldcg(a.slots.ml + (size_t)(2 * x + (x == c0)) * R + r);
-        top = fmaxf(top, ml[k].x);
-      }
-      top = warp_max(top);
-      const float mu = top == -INFINITY ? 0.f : top;
-      float den = 0.f;
+          for (int y = 0; y < NB; ++y) {
+            if (x + y > c1) ml[y].x = -INFINITY;
+            top = fmaxf(top, ml[y].x);
+          }
+          const float mu = top == -INFINITY ? 0.f : top;
+          const float f = paged_exp2(acc.m - mu);
+          acc.m = top;
+          acc.l *= f, acc.o.x *= f, acc.o.y *= f, acc.o.z *= f, acc.o.w *= f;
 #pragma unroll
-      for (int k = 0; k < NB / 32; ++k) {
-        if (32 * k >= nb) break;
-        const float w = paged_exp2(ml[k].x - mu);
-        if (32 * k + lane < nb) wgt[(32 * k + lane) * R + r] = w;
-        den = fmaf(w, ml[k].y, den);
+          for (int y = 0; y < NB; ++y) acc.add(paged_exp2(ml[y].x - mu), ml[y].y, o[y]);
+        }
       }
-      den = warp_sum(den);
-      __syncwarp();
-      if (lane == 0) {  // y: the sum; the batches before are scaled by 2^(old - top)
-        if (x0 > c0) den = fmaf(row_ml[r].y, paged_exp2(old - mu), den);
-        row_ml[r] = make_float2(top, den);
-      }
-      if (x0 > c0 && lane == 0) wgt[nb * R + r] = paged_exp2(old - mu);
+      const int t = paged_token(r, gmul);
+      paged_emit(a, HD, c.s.lo + tok0 + t, c.kvh * a.gq + r - t * a.gq, d, acc);
+    }
+    if (whole || pass == 1) break;
+    if (a.prefix_pass) {  // joined by the next launch
+      if (c.first() && tid == 0)
+        a.splits[blockIdx.x] = PagedSplit{c1, c.s.lo + tok0, rows, c.kvh * a.gq};
+      break;
+    }
+    __threadfence();
+    consumer_sync();
+    if (tid == 0) {
+      const int last = atomicAdd(a.counters + c0, 1) == c1 - c0;
+      if (last) a.counters[c0] = 0;  // ready for the next launch
+      *flag = last;
     }
     consumer_sync();
-#pragma unroll
-    for (int k = 0; k < NI; ++k) {
-      const int i = tid + 128 * k, r = i / V4;
-      if (x0 > c0 && i < rows * V4) {
-        const float f = wgt[nb * R + r];
-        acc[k].o.x *= f, acc[k].o.y *= f, acc[k].o.z *= f, acc[k].o.w *= f;
-      }
-    }
-    constexpr int NL = 16 / NI;  // records per round of loads
-    const float4* o = reinterpret_cast<const float4*>(a.slots.o + (size_t)2 * x0 * R * HD);
-    for (int x = 0; x < nb; x += NL) {
-      float4 v[NL][NI];
-#pragma unroll
-      for (int y = 0; y < NL; ++y) {
-        const int xx = min(x + y, nb - 1);  // (no branch between the loads)
-        const float4* rec = o + (size_t)(2 * xx + (x0 + xx == c0)) * (R * V4);
-#pragma unroll
-        for (int k = 0; k < NI; ++k) v[y][k] = ld_first(rec + min(tid + 128 * k, N - 1));
-      }
-#pragma unroll
-      for (int y = 0; y < NL; ++y) {
-        if (x + y >= nb) break;
-#pragma unroll
-        for (int k = 0; k < NI; ++k)
-          acc[k].add(wgt[(x + y) * R + min((tid + 128 * k) / V4, R - 1)], 0.f, v[y][k]);
-      }
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < NI; ++k) {
-    const int i = tid + 128 * k, r = i / V4;
-    if (i >= rows * V4) break;
-    acc[k].m = row_ml[r].x;
-    acc[k].l = row_ml[r].y;
-    paged_emit(a, HD, c.s.lo + tok0 + r / a.gq, c.kvh * a.gq + r % a.gq, (i % V4) * 4, acc[k]);
+    if (!*flag) break;
+    __threadfence();
   }
 }
 
@@ -281,35 +225,29 @@ __device__ __forceinline__ bool open_cta(const PagedAttnArgs& a, uint8_t* sm) {
   }
   paged_pdl_open(a);
   if (a.prefix_pass && threadIdx.x == 0) a.splits[blockIdx.x].c1 = -1;
-  paged_find_start<KT, kThreads>(a, st, reinterpret_cast<long long*>(sm + LY::off_start + 96));
+  paged_find_start<KT, kThreads>(a, st, reinterpret_cast<int*>(sm + LY::off_start + 96));
   return st->any;
 }
 
-// Join of the four warps: common maximum per row, then the weights every warp scales its o with.
-// Returns through `w` this thread's rows' weights. Rows of this thread: `NRW` of them at `rows`.
-template <int R, int NRW>
-__device__ __forceinline__ void join_rows(const float (&m)[NRW], const float (&l)[NRW],
-                                          const int (&row)[NRW], bool writer, int warp,
-                                          float2* ml_s, float2* row_ml, float (&w)[NRW]) {
-  if (writer)
-#pragma unroll
-    for (int i = 0; i < NRW; ++i) ml_s[warp * R + row[i]] = make_float2(m[i], l[i]);
+// Join of the four warps' (m, l) in ml_s [warp][R]: the rows' (m, l) into row_ml, and in ml_s[..].x
+// the factor of each warp's o.
+template <int R>
+__device__ __forceinline__ void join_rows(float2* ml_s, float2* row_ml) {
   consumer_sync();
+  if (threadIdx.x < R) {
+    float M = -INFINITY, den = 0.f;
 #pragma unroll
-  for (int i = 0; i < NRW; ++i) {
-    float M = -INFINITY;
-#pragma unroll
-    for (int x = 0; x < kConsumers; ++x) M = fmaxf(M, ml_s[x * R + row[i]].x);
+    for (int x = 0; x < kConsumers; ++x) M = fmaxf(M, ml_s[x * R + threadIdx.x].x);
     const float mu = M == -INFINITY ? 0.f : M;
-    w[i] = paged_exp2(m[i] - mu);
-    float den = 0.f;
 #pragma unroll
     for (int x = 0; x < kConsumers; ++x) {
-      const float2 v = ml_s[x * R + row[i]];
-      den = fmaf(paged_exp2(v.x - mu), v.y, den);
+      const float w = paged_exp2(ml_s[x * R + threadIdx.x].x - mu);
+      den = fmaf(w, ml_s[x * R + threadIdx.x].y, den);
+      ml_s[x * R + threadIdx.x].x = w;
     }
-    if (warp == 0 && writer) row_ml[row[i]] = make_float2(M, den);
+    row_ml[threadIdx.x] = make_float2(M, den);
   }
+  consumer_sync();
 }
 
 // ------------------------------------------------------------------ bf16 pages: mma.sync
@@ -373,38 +311,66 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int vrow = 16 * warp + (mat & 1) * 8 + mr, vch = mat >> 1;
   const uint32_t ring = smem_addr(sm);
 
+  const uint32_t gmul = 65536u / a.gq + 1;
   PagedCursor c = paged_cursor<KT>(a, st);
   int seen = 0;      // tiles taken from the ring
   bool bad = false;  // a wait gave up: no more waits, the barriers are still kept
   do {
     const int n = c.kend - c.kt;
     const int tok0 = c.rt * a.tpt, rows = min(a.tpt, c.s.nb - tok0) * a.gq;
-    // q as A fragments: rows g (and g + 8), columns 16 ks + q2 + {0, 1} (and + 8)
+    // q through shared memory (where the join works at the item's end) as A fragments: rows g and
+    // g + 8 of a 16-row tile; with NT = 3 "row" g + 8 is row g's second term, the third is in ql
+    constexpr uint32_t kPlane = 8 * HD * 2;
+    {
+      uint8_t* to = reinterpret_cast<uint8_t*>(join);
+#pragma unroll 1
+      for (int i = threadIdx.x; i < R * HD / 8; i += kConsumers * 32) {
+        const int r = i / (HD / 8), u = i % (HD / 8), t = paged_token(r, gmul);
+        const size_t at = (size_t)(c.s.lo + tok0 + t) * a.ldq + (size_t)(c.kvh * a.gq + r - t * a.gq) * HD + u * 8;
+        const uint32_t off = r * (HD * 2) + ((u ^ (r & 7)) << 4);
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if constexpr (NT == 1) {
+          if (r < rows) x = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at));
+          *reinterpret_cast<uint4*>(to + off) = x;
+        } else {
+          uint4 y = x;
+          if (r < rows) {
+            const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(a.q) + at);
+            x = __ldg(q);
+            y = __ldg(q + 1);
+          }
+          uint4 h, m, l;
+          split3(__uint_as_float(x.x), __uint_as_float(x.y), h.x, m.x, l.x);
+          split3(__uint_as_float(x.z), __uint_as_float(x.w), h.y, m.y, l.y);
+          split3(__uint_as_float(y.x), __uint_as_float(y.y), h.z, m.z, l.z);
+          split3(__uint_as_float(y.z), __uint_as_float(y.w), h.w, m.w, l.w);
+          *reinterpret_cast<uint4*>(to + off) = h;
+          *reinterpret_cast<uint4*>(to + kPlane + off) = m;
+          *reinterpret_cast<uint4*>(to + 2 * kPlane + off) = l;
+        }
+      }
+    }
+    consumer_sync();
     uint32_t qa[KS][4], ql[NT == 3 ? KS : 1][2];
+    {
+      const uint32_t from = smem_addr(join) + mr * (HD * 2);
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+        ldsm4(from + (mat & 1) * kPlane + (((ks * 2 + (mat >> 1)) ^ mr) << 4), qa[ks]);
+      if constexpr (NT == 3) {
+#pragma unroll
+        for (int ks = 0; ks < KS; ks += 2) {
+          uint32_t x[4];
+          ldsm4(from + 2 * kPlane + (((ks * 2 + mat) ^ mr) << 4), x);
+          ql[ks][0] = x[0], ql[ks][1] = x[1], ql[ks + 1][0] = x[2], ql[ks + 1][1] = x[3];
+        }
+      }
+    }
     int lim[NRW];
 #pragma unroll
     for (int i = 0; i < NRW; ++i) {
-      const int r = g + 8 * i, t = tok0 + r / a.gq;
-      lim[i] = a.prefix_pass ? c.limit : min(max(c.s.base + t + 1, 0), c.s.len);
-      const bool live = r < rows;
-      if (!live) lim[i] = 0;
-      const size_t at = (size_t)(c.s.lo + t) * a.ldq + (size_t)(c.kvh * a.gq + r % a.gq) * HD + q2;
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const size_t e = at + ks * 16 + hf * 8;
-          if constexpr (NT == 1) {
-            qa[ks][2 * hf + i] =
-                live ? __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) + e))
-                     : 0u;
-          } else {
-            const float2 x = live ? __ldg(reinterpret_cast<const float2*>(
-                                        static_cast<const float*>(a.q) + e))
-                                  : make_float2(0.f, 0.f);
-            split3(x.x, x.y, qa[ks][2 * hf], qa[ks][2 * hf + 1], ql[ks][hf]);
-          }
-        }
+      const int r = g + 8 * i, t = tok0 + paged_token(r, gmul);
+      lim[i] = r >= rows ? 0 : a.prefix_pass ? c.limit : min(max(c.s.base + t + 1, 0), c.s.len);
     }
     float o[DT][4], m[NRW], l[NRW];
 #pragma unroll
@@ -517,33 +483,32 @@ __global__ void __launch_bounds__(kThreads, 2)
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
     }
-    int row[NRW];
+    if ((lane & 3) == 0)
+#pragma unroll
+      for (int i = 0; i < NRW; ++i) ml_s[warp * R + g + 8 * i] = make_float2(m[i], l[i]);
+    join_rows<R>(ml_s, row_ml);
     float w[NRW];
 #pragma unroll
-    for (int i = 0; i < NRW; ++i) row[i] = g + 8 * i;
-    join_rows<R, NRW>(m, l, row, (lane & 3) == 0, warp, ml_s, row_ml, w);
-    float* mine = join + (warp & 1) * (R * HD);
-    auto put = [&](bool add) {
+    for (int i = 0; i < NRW; ++i) w[i] = ml_s[warp * R + g + 8 * i].x;
+    // warps 2 and 3 put their o down, warps 0 and 1 add theirs
+#pragma unroll 1
+    for (int step = 0; step < 2; ++step) {
+      if ((warp < 2) == (step == 1)) {
 #pragma unroll
-      for (int d = 0; d < DT; ++d)
+        for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int i = 0; i < NRW; ++i) {
-          float2* at = reinterpret_cast<float2*>(mine + (g + 8 * i) * HD + d * 8 + q2);
-          float2 v = NT == 3 ? make_float2(o[d][0] + o[d][2], o[d][1] + o[d][3])
-                             : make_float2(o[d][2 * i], o[d][2 * i + 1]);
-          v.x *= w[i], v.y *= w[i];
-          if (add) {
-            const float2 b = *at;
-            v.x += b.x, v.y += b.y;
+          for (int i = 0; i < NRW; ++i) {
+            float2* at = reinterpret_cast<float2*>(join + (warp & 1) * (R * HD) + (g + 8 * i) * HD + d * 8 + q2);
+            float2 b = make_float2(0.f, 0.f);
+            if (step) b = *at;
+            const float x = NT == 3 ? o[d][0] + o[d][2] : o[d][2 * i];
+            const float y = NT == 3 ? o[d][1] + o[d][3] : o[d][2 * i + 1];
+            *at = make_float2(fmaf(x, w[i], b.x), fmaf(y, w[i], b.y));
           }
-          *at = v;
-        }
-    };
-    if (warp >= 2) put(false);
-    consumer_sync();
-    if (warp < 2) put(true);
-    consumer_sync();
-    finish_segment<HD, R>(a, c, join, row_ml, flag);
+      }
+      consumer_sync();
+    }
+    finish_segment<HD, R>(a, c, gmul, join, row_ml, flag);
     consumer_sync();  // join and row_ml are free again
   } while (c.next<KT>(a));
   if (bad && lane == 0 && a.c.status) atomicOr(a.c.status, PG_TIMEOUT);
@@ -589,29 +554,40 @@ __global__ void __launch_bounds__(kThreads, 2)
   float2* row_ml = reinterpret_cast<float2*>(sm + LY::off_row);
   int* flag = reinterpret_cast<int*>(sm + LY::off_start + 96 + 40);
 
+  const uint32_t gmul = 65536u / a.gq + 1;
   PagedCursor c = paged_cursor<KT>(a, st);
   int seen = 0;
   bool bad = false;
   do {
     const int n = c.kend - c.kt;
     const int tok0 = c.rt * a.tpt, rows = min(a.tpt, c.s.nb - tok0) * a.gq;
+    // q, scaled, through shared memory (where the join works at the item's end) into registers
+#pragma unroll 1
+    for (int i = threadIdx.x; i < R * HD / 4; i += kConsumers * 32) {
+      const int r = i / (HD / 4), u = i % (HD / 4), t = paged_token(r, gmul);
+      const size_t at = (size_t)(c.s.lo + tok0 + t) * a.ldq + (size_t)(c.kvh * a.gq + r - t * a.gq) * HD + u * 4;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < rows) {
+        if (a.act_bf16)
+          x = KvElem<true>::load4(static_cast<const uint16_t*>(a.q) + at);
+        else
+          x = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at));
+      }
+      const float k = a.scale_log2;
+      *reinterpret_cast<float4*>(join + i * 4) = make_float4(x.x * k, x.y * k, x.z * k, x.w * k);
+    }
+    consumer_sync();
     float q[R][E], o[R][E], m[R], l[R];
     int lim[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int t = tok0 + r / a.gq;
+      const int t = tok0 + paged_token(r, gmul);
       lim[r] = r >= rows ? 0 : a.prefix_pass ? c.limit : min(max(c.s.base + t + 1, 0), c.s.len);
       m[r] = -INFINITY;
       l[r] = 0.f;
-      const size_t at = (size_t)(c.s.lo + t) * a.ldq + (size_t)(c.kvh * a.gq + r % a.gq) * HD + lane * E;
+      Lane<E>::load(join + r * HD + lane * E, q[r]);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        o[r][e] = 0.f;
-        q[r][e] = r >= rows       ? 0.f
-                  : a.act_bf16 ? bf16f(__ldg(static_cast<const uint16_t*>(a.q) + at + e))
-                               : __ldg(static_cast<const float*>(a.q) + at + e);
-        q[r][e] *= a.scale_log2;
-      }
+      for (int e = 0; e < E; ++e) o[r][e] = 0.f;
     }
     for (int x = 0; x < n; ++x, ++seen) {
       const int stage = seen % NS;
@@ -654,9 +630,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         p[r] = paged_exp2(s - mu);
         l[r] += p[r];  // this lane's key; the eight keys are added at the end
       }
-#pragma unroll
-      for (int k = 0; k < KW; ++k) {
-        if (k0 + k >= c.limit) break;  // behind the last key lies whatever the page held
+      const int kn = min(KW, c.limit - k0);  // behind the last key lies whatever the page held
+#pragma unroll 4
+      for (int k = 0; k < kn; ++k) {
         float vx[E];
         Lane<E>::load(vb + k * HD, vx);
 #pragma unroll
@@ -669,31 +645,27 @@ __global__ void __launch_bounds__(kThreads, 2)
       __syncwarp();
       if (lane == 0) mbar_arrive_cta(&empty[stage]);
     }
-    int row[R];
-    float w[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      row[r] = r;
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], d);
+      if (lane == 0) ml_s[warp * R + r] = make_float2(m[r], l[r]);
     }
-    join_rows<R, R>(m, l, row, lane == 0, warp, ml_s, row_ml, w);
-    float* mine = join + (warp & 1) * (R * HD) + lane * E;
-    auto put = [&](bool add) {
+    join_rows<R>(ml_s, row_ml);
+#pragma unroll 1
+    for (int step = 0; step < 2; ++step) {
+      if ((warp < 2) == (step == 1)) {
 #pragma unroll
-      for (int r = 0; r < R; ++r)
+        for (int r = 0; r < R; ++r) {
+          const float w = ml_s[warp * R + r].x;
+          float* at = join + (warp & 1) * (R * HD) + r * HD + lane * E;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          float* at = mine + r * HD + e;
-          const float v = o[r][e] * w[r];
-          *at = add ? *at + v : v;
+          for (int e = 0; e < E; ++e) at[e] = fmaf(o[r][e], w, step ? at[e] : 0.f);
         }
-    };
-    if (warp >= 2) put(false);
-    consumer_sync();
-    if (warp < 2) put(true);
-    consumer_sync();
-    finish_segment<HD, R>(a, c, join, row_ml, flag);
+      }
+      consumer_sync();
+    }
+    finish_segment<HD, R>(a, c, gmul, join, row_ml, flag);
     consumer_sync();
   } while (c.next<KT>(a));
   if (bad && lane == 0 && a.c.status) atomicOr(a.c.status, PG_TIMEOUT);
@@ -812,18 +784,26 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& base, int hd, int max_ne
     return hd == 64 ? launch_pass<64>(a, p, s) : launch_pass<128>(a, p, s);
   };
   const long long cap = 1 << 20;  // row counts only choose a kernel
+  // the line of a launch is counted in 32 bits
+  auto too_long = [&](const PagedPlan& p, long long tiles, long long seqs) {
+    const long long items = a.n_tokens / (p.rows / a.gq) + seqs;
+    return tiles / p.kt + 4 > INT32_MAX / a.c.nkv / items;
+  };
+  const int rows = (int)std::min(cap, (long long)std::min(max_new, a.n_tokens) * a.gq);
+  const PagedPlan own = plan_paged_pass(a, hd, rows, sms);
+  if (too_long(own, (long long)a.c.max_pages << a.c.page_shift, a.c.n_seqs)) return cudaErrorInvalidValue;
   if (prefix) {
     a.pre.ml = reinterpret_cast<float2*>(ws + w.whole_ml);
     a.pre.o = reinterpret_cast<float*>(ws + w.whole_o);
     a.prefix_pass = 1;
     const PagedPlan p = plan_paged_pass(a, hd, (int)std::min(cap, (long long)a.n_tokens * a.gq), sms);
+    if (too_long(p, a.c.prefix_len, 1)) return cudaErrorInvalidValue;
     cudaError_t e = run(p, 1);
     if (e == cudaSuccess) e = launch_paged_join(a, hd, p.grid, p.rows, s);
     if (e != cudaSuccess) return e;
     a.prefix_pass = 0;
   }
-  const int rows = (int)std::min(cap, (long long)std::min(max_new, a.n_tokens) * a.gq);
-  return run(plan_paged_pass(a, hd, rows, sms), 0);
+  return run(own, 0);
 }
 
 }  // namespace qw

@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
   paged_pdl_open(a);
   if (threadIdx.x == 0) a.splits[blockIdx.x].c1 = -1;
   tc_fence_before();
-  paged_find_start<KT, LY::kThreads>(a, st, reinterpret_cast<long long*>(sm + LY::off_start + 96));
+  paged_find_start<KT, LY::kThreads>(a, st, reinterpret_cast<int*>(sm + LY::off_start + 96));
   tc_fence_after();
   const uint32_t tb = *tslot;
   const int half = 128 / a.gq;  // tokens of a row tile

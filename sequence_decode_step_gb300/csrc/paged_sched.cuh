@@ -27,11 +27,10 @@ namespace qw {
 constexpr int kPagedItemUnits = 3;
 constexpr int kPagedLeastUnits = 2;  // least share of a CTA: fewer records of a short line to join
 
-// Quotient of two line positions: 32-bit where both fit, as they do for any real batch.
-__device__ __forceinline__ long long paged_div(long long a, long long b) {
-  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
-  return a / b;
-}
+// Units are counted in 32 bits (the host refuses calls whose line could be longer). The code of
+// these kernels is kept short on purpose: a decode step's weights sweep the instructions out of the
+// caches between two calls, and a cold line of 128 bytes costs 0.2 us from L2 and 0.7 us from HBM,
+// more than most of the work it holds.
 
 // Programmatic launches: every kernel here may start while the one before it still runs, and waits
 // for its end (griddepcontrol.wait) before it touches memory. The launch over the sequences' own keys
@@ -62,7 +61,6 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedAttnArgs& a, int b) {
     const long long cap = (long long)a.c.max_pages << a.c.page_shift;
     const int len = __ldg(a.c.kv_len + b);
     s.len = (int)min((long long)max(len, 0), cap);
-    if (len != s.len && a.c.status) atomicOr(a.c.status, PG_BAD_LENGTH);
     s.base = s.len - s.nb;
   }
   s.nrt = (s.nb + a.tpt - 1) / a.tpt;
@@ -79,14 +77,15 @@ __device__ __forceinline__ int paged_tiles(int limit) {
   return max(1, (limit + KT - 1) / KT);
 }
 template <int KT>
-__device__ __forceinline__ long long paged_head_units(const PagedAttnArgs& a, const PagedSeq& s) {
-  long long n = 0;
+__device__ __forceinline__ int paged_head_units(const PagedAttnArgs& a, const PagedSeq& s) {
+  int n = 0;
+#pragma unroll 1
   for (int rt = 0; rt < s.nrt; ++rt) n += kPagedItemUnits + paged_tiles<KT>(paged_limit(a, s, rt));
   return n;
 }
 
 struct PagedCursor {  // a place on the line
-  long long item, u1, per;  // the current item's first unit; end of the CTA's share
+  int item, u1, per;  // the current item's first unit; end of the CTA's share
   int b, kvh, rt;           // current item
   int kt, kend;             // this CTA's tiles of it
   int nkt, limit;           // all its tiles; its keys
@@ -95,15 +94,15 @@ struct PagedCursor {  // a place on the line
   __device__ __forceinline__ bool first() const { return kt == 0; }
   __device__ __forceinline__ bool whole() const { return kt == 0 && kend == nkt; }
   // CTAs that share the item's tiles
-  __device__ __forceinline__ int first_cta() const { return (int)paged_div(item + kPagedItemUnits, per); }
+  __device__ __forceinline__ int first_cta() const { return (item + kPagedItemUnits) / per; }
   __device__ __forceinline__ int last_cta() const {
-    return (int)paged_div(item + kPagedItemUnits + nkt - 1, per);
+    return (item + kPagedItemUnits + nkt - 1) / per;
   }
   template <int KT>
   __device__ __forceinline__ void enter(const PagedAttnArgs& a) {
     limit = paged_limit(a, s, rt);
     nkt = paged_tiles<KT>(limit);
-    kend = (int)min((long long)nkt, u1 - item - kPagedItemUnits);
+    kend = min(nkt, u1 - item - kPagedItemUnits);
   }
   // To the CTA's next item; false when its share ends before that item's first tile.
   template <int KT>
@@ -125,73 +124,78 @@ struct PagedCursor {  // a place on the line
 };
 
 struct PagedStart {  // in shared memory: where this CTA starts
-  long long item, u1, per;
+  int item, u1, per;
   int b, kvh, rt, kt;
   int any;           // 0: nothing to do
   PagedSeq s;
 };
 
-// Block-wide: fills *st. warp_sums: one long long per warp.
+// Block-wide: fills *st. warp_sums: an int per warp.
 template <int KT, int THREADS>
-__device__ void paged_find_start(const PagedAttnArgs& a, PagedStart* st, long long* warp_sums) {
+__device__ __forceinline__ void paged_find_start(const PagedAttnArgs& a, PagedStart* st, int* warp_sums) {
   constexpr int W = THREADS / 32;
   const int n = a.prefix_pass ? 1 : a.c.n_seqs;
   const int spt = (n + THREADS - 1) / THREADS;
   const int b0 = min((int)threadIdx.x * spt, n), b1 = min(b0 + spt, n);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long mine = 0, hu = 0;  // units of this thread's sequences; per KV head of the last one
-  PagedSeq s;
-  for (int b = b0; b < b1; ++b) {
-    s = paged_seq(a, b);
-    hu = paged_head_units<KT>(a, s);
-    mine += hu * a.c.nkv;
-  }
-  long long scan = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, scan, o);
-    if (lane >= o) scan += v;
-  }
-  if (lane == 31) warp_sums[warp] = scan;
-  if (threadIdx.x == 0) st->any = 0;
-  __syncthreads();
-  long long before = scan - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < W; ++w) {
-    if (w < warp) before += warp_sums[w];
-    total += warp_sums[w];
-  }
-  const long long per = max(paged_div(total + gridDim.x - 1, gridDim.x), (long long)kPagedLeastUnits);
-  const long long u0 = per * blockIdx.x;
-  if (u0 < total && before <= u0 && u0 < before + mine) {
-    long long r = u0 - before;
-    int b = b0;
-    if (b1 - b0 > 1) {
-      s = paged_seq(a, b);
-      hu = paged_head_units<KT>(a, s);
-      while (r >= hu * a.c.nkv) {
-        r -= hu * a.c.nkv;
-        s = paged_seq(a, ++b);
-        hu = paged_head_units<KT>(a, s);
+  // the thread's sequences, twice: their units, then (in the one that holds the CTA's start) the place
+  int mine = 0, before = 0, r = -1, per = 0, total = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+      const PagedSeq s = paged_seq(a, b);
+      const int hu = paged_head_units<KT>(a, s), units = hu * a.c.nkv;
+      if (pass == 0) {
+        if (blockIdx.x == 0 && !a.prefix_pass && a.c.status && (s.base < 0 || s.len != __ldg(a.c.kv_len + b)))
+          atomicOr(a.c.status, PG_BAD_LENGTH);
+        mine += units;
+        continue;
       }
+      if (r >= units) {
+        r -= units;
+        continue;
+      }
+      const int kvh = r / hu;
+      r -= hu * kvh;
+      int rt = 0;
+#pragma unroll 1
+      for (;; ++rt) {
+        const int t = kPagedItemUnits + paged_tiles<KT>(paged_limit(a, s, rt));
+        if (r < t) break;
+        r -= t;
+      }
+      const int u0 = per * blockIdx.x;
+      st->item = u0 - r;
+      st->u1 = min(u0 + per, total);
+      st->per = per;
+      st->b = b;
+      st->kvh = kvh;
+      st->rt = rt;
+      st->s = s;
+      st->kt = max(r - kPagedItemUnits, 0);
+      st->any = u0 - r + kPagedItemUnits < st->u1;  // the share has a tile
+      break;
     }
-    const int kvh = (int)paged_div(r, hu);
-    r -= hu * kvh;
-    int rt = 0;
-    for (;; ++rt) {
-      const int t = kPagedItemUnits + paged_tiles<KT>(paged_limit(a, s, rt));
-      if (r < t) break;
-      r -= t;
+    if (pass == 1) break;
+    int scan = mine;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += v;
     }
-    st->item = u0 - r;
-    st->u1 = min(u0 + per, total);
-    st->per = per;
-    st->b = b;
-    st->kvh = kvh;
-    st->rt = rt;
-    st->s = s;
-    st->kt = max((int)r - kPagedItemUnits, 0);
-    st->any = u0 - r + kPagedItemUnits < st->u1;  // the share has a tile
+    if (lane == 31) warp_sums[warp] = scan;
+    if (threadIdx.x == 0) st->any = 0;
+    __syncthreads();
+    before = scan - mine;
+#pragma unroll 1
+    for (int w = 0; w < W; ++w) {
+      if (w < warp) before += warp_sums[w];
+      total += warp_sums[w];
+    }
+    per = max((total + (int)gridDim.x - 1) / (int)gridDim.x, kPagedLeastUnits);
+    r = per * (int)blockIdx.x - before;
+    if (per * (int)blockIdx.x >= total || r < 0 || r >= mine) break;
   }
   __syncthreads();
 }
@@ -211,8 +215,8 @@ __device__ __forceinline__ PagedCursor paged_cursor(const PagedAttnArgs& a, cons
   return c;
 }
 
-// Page of key tile row `key` of the cursor's item; a page id outside the pool is reported and
-// read as page 0, so that no read leaves the pool.
+// Page of key tile row `key` of the cursor's item; a page id outside the pool is reported and read
+// as page 0, so that no read leaves the pool.
 __device__ __forceinline__ int paged_page(const PagedAttnArgs& a, int b, int key) {
   const int at = key >> a.c.page_shift;
   int pg = a.prefix_pass ? __ldg(a.c.prefix_pages + at)
@@ -287,34 +291,41 @@ __device__ __forceinline__ void paged_join_slots(const PagedSlots& sl, int c0, i
     const float4* o = reinterpret_cast<const float4*>(sl.o + ((size_t)2 * x0 * sl.rows + r) * HD + d);
     const size_t step = (size_t)2 * sl.rows * (HD / 4);
     const size_t skip = (size_t)sl.rows * (HD / 4);  // the first record is in its CTA's other slot
-#pragma unroll 8
+#pragma unroll 4
     for (int i = 0; i < n; ++i)
       acc.add(__shfl_sync(mask, w, i, W), __shfl_sync(mask, wl, i, W),
               __ldcg(o + i * step + (x0 + i == c0 ? skip : 0)));
   }
 }
 
+// row / gq for rows below 256 and gq <= 8, with gmul = 65536 / gq + 1.
+__device__ __forceinline__ int paged_token(int row, uint32_t gmul) {
+  return (int)((uint32_t)row * gmul >> 16);
+}
+
 // Writes one float4 (columns d..d+3) of query row (token, head): the prefix's record in its
 // launches, else the output after that record is joined; a row without a key is 0.
 __device__ __forceinline__ void paged_emit(const PagedAttnArgs& a, int hd, int token, int head, int d,
-                                           PagedAcc& acc) {
-  const size_t row = (size_t)token * a.nq + head;
+                                           PagedAcc acc) {
+  const size_t row = (size_t)token * a.nq + head, at = row * hd + d;
+  float* to = static_cast<float*>(a.out);
   if (a.prefix_pass) {
-    *reinterpret_cast<float4*>(a.pre.o + row * hd + d) = acc.o;
+    to = a.pre.o;
     if (d == 0) a.pre.ml[row] = make_float2(acc.m, acc.l);
-    return;
+  } else {
+    if (a.pre.o) {
+      const float2 ml = __ldcg(a.pre.ml + row);
+      acc.join(ml.x, ml.y, __ldcg(reinterpret_cast<const float4*>(a.pre.o + at)));
+    }
+    const float inv = acc.l > 0.f || acc.l != acc.l ? __frcp_rn(acc.l) : 0.f;
+    acc.o.x *= inv, acc.o.y *= inv, acc.o.z *= inv, acc.o.w *= inv;
+    if (a.act_bf16) {
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
+          make_uint2(paged_pack(acc.o.x, acc.o.y), paged_pack(acc.o.z, acc.o.w));
+      return;
+    }
   }
-  if (a.pre.o) {
-    const float2 ml = __ldcg(a.pre.ml + row);
-    acc.join(ml.x, ml.y, __ldcg(reinterpret_cast<const float4*>(a.pre.o + row * hd + d)));
-  }
-  const float inv = acc.l > 0.f || acc.l != acc.l ? 1.f / acc.l : 0.f;
-  const float4 o = make_float4(acc.o.x * inv, acc.o.y * inv, acc.o.z * inv, acc.o.w * inv);
-  if (a.act_bf16)
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * hd + d) =
-        make_uint2(paged_pack(o.x, o.y), paged_pack(o.z, o.w));
-  else
-    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * hd + d) = o;
+  *reinterpret_cast<float4*>(to + at) = acc.o;
 }
 
 }  // namespace qw
