@@ -85,6 +85,7 @@ struct PagedAttnArgs {
   int n_tokens, nq, gq;     // gq = nq / nkv
   int act_bf16;
   int tpt;                  // tokens per row tile
+  int item_units;           // tiles that an item costs beside its keys
   float scale_log2;         // log2(e) / sqrt(hd)
   PagedSlots slots;         // of this launch
   int* counters;            // [grid] arrivals of split items, 0 between launches
@@ -93,10 +94,11 @@ struct PagedAttnArgs {
   PagedPrefix pre;
   uint64_t wait_ns;
 };
-// Keys per tile, query rows per item and CTAs of a launch: a rule on types and row counts.
+// Keys per tile, query rows per item, CTAs and an item's own cost of a launch: a rule on types and
+// row counts.
 struct PagedPlan {
   bool tc;                  // paged_attention_tc.cu, else paged_attention.cu
-  int kt, rows, grid;
+  int kt, rows, grid, item_units;
 };
 PagedPlan plan_paged_pass(const PagedAttnArgs& a, int hd, int max_rows, int sms);
 size_t paged_attn_workspace_bytes(int n_tokens, int nq, int hd, bool prefix);

@@ -12,7 +12,7 @@
 // of their own (many rows: one CTA would read them for 5-10 us).
 //
 // An item costs a CTA some tiles beside its keys (q, the join, the output), so on the line it is
-// that much longer (kPagedItemUnits); the units before its first tile are empty.
+// that much longer (item_units); the units before its first tile are empty.
 //
 // The shared prefix is the same line with one pseudo-sequence: all the batch's tokens, every one
 // of which sees all prefix_len keys.
@@ -22,10 +22,7 @@
 
 namespace qw {
 
-// Tiles that an item's q, first product, join and output take: about 4 us, against 1.2 us for a
-// CTA's tile of 32 KB while HBM is the bound and 1.5 us for a tensor-core tile of 128 keys.
-constexpr int kPagedItemUnits = 3;
-constexpr int kPagedLeastUnits = 2;  // least share of a CTA: fewer records of a short line to join
+constexpr int kPagedLeastUnits = 4;  // least share of a CTA: fewer records of a short line to join
 
 // Units are counted in 32 bits (the host refuses calls whose line could be longer). The code of
 // these kernels is kept short on purpose: a decode step's weights sweep the instructions out of the
@@ -80,12 +77,13 @@ template <int KT>
 __device__ __forceinline__ int paged_head_units(const PagedAttnArgs& a, const PagedSeq& s) {
   int n = 0;
 #pragma unroll 1
-  for (int rt = 0; rt < s.nrt; ++rt) n += kPagedItemUnits + paged_tiles<KT>(paged_limit(a, s, rt));
+  for (int rt = 0; rt < s.nrt; ++rt) n += a.item_units + paged_tiles<KT>(paged_limit(a, s, rt));
   return n;
 }
 
 struct PagedCursor {  // a place on the line
-  int item, u1, per;  // the current item's first unit; end of the CTA's share
+  int item, u1, per;        // the current item's first unit; end of the CTA's share
+  int lead;                 // units of an item before its first tile
   int b, kvh, rt;           // current item
   int kt, kend;             // this CTA's tiles of it
   int nkt, limit;           // all its tiles; its keys
@@ -94,21 +92,21 @@ struct PagedCursor {  // a place on the line
   __device__ __forceinline__ bool first() const { return kt == 0; }
   __device__ __forceinline__ bool whole() const { return kt == 0 && kend == nkt; }
   // CTAs that share the item's tiles
-  __device__ __forceinline__ int first_cta() const { return (item + kPagedItemUnits) / per; }
+  __device__ __forceinline__ int first_cta() const { return (item + lead) / per; }
   __device__ __forceinline__ int last_cta() const {
-    return (item + kPagedItemUnits + nkt - 1) / per;
+    return (item + lead + nkt - 1) / per;
   }
   template <int KT>
   __device__ __forceinline__ void enter(const PagedAttnArgs& a) {
     limit = paged_limit(a, s, rt);
     nkt = paged_tiles<KT>(limit);
-    kend = min(nkt, u1 - item - kPagedItemUnits);
+    kend = min(nkt, u1 - item - lead);
   }
   // To the CTA's next item; false when its share ends before that item's first tile.
   template <int KT>
   __device__ __forceinline__ bool next(const PagedAttnArgs& a) {
-    item += kPagedItemUnits + nkt;
-    if (item + kPagedItemUnits >= u1) return false;
+    item += lead + nkt;
+    if (item + lead >= u1) return false;
     kt = 0;
     if (++rt == s.nrt) {
       rt = 0;
@@ -161,7 +159,7 @@ __device__ __forceinline__ void paged_find_start(const PagedAttnArgs& a, PagedSt
       int rt = 0;
 #pragma unroll 1
       for (;; ++rt) {
-        const int t = kPagedItemUnits + paged_tiles<KT>(paged_limit(a, s, rt));
+        const int t = a.item_units + paged_tiles<KT>(paged_limit(a, s, rt));
         if (r < t) break;
         r -= t;
       }
@@ -173,8 +171,8 @@ __device__ __forceinline__ void paged_find_start(const PagedAttnArgs& a, PagedSt
       st->kvh = kvh;
       st->rt = rt;
       st->s = s;
-      st->kt = max(r - kPagedItemUnits, 0);
-      st->any = u0 - r + kPagedItemUnits < st->u1;  // the share has a tile
+      st->kt = max(r - a.item_units, 0);
+      st->any = u0 - r + a.item_units < st->u1;  // the share has a tile
       break;
     }
     if (pass == 1) break;
@@ -203,6 +201,7 @@ __device__ __forceinline__ void paged_find_start(const PagedAttnArgs& a, PagedSt
 template <int KT>
 __device__ __forceinline__ PagedCursor paged_cursor(const PagedAttnArgs& a, const PagedStart* st) {
   PagedCursor c;
+  c.lead = a.item_units;
   c.item = st->item;
   c.u1 = st->u1;
   c.per = st->per;
