@@ -18,8 +18,12 @@
 // delivers the tile's 32 KB in ~1400. f32 activations keep f32 results: q and P enter as three
 // bf16 terms (24 bits), rows 0-7 of a fragment carrying the first and rows 8-15 the second term,
 // the third in a second mma, so R = 8 rows cost two mma instead of three.
-// f32 pages (kernel _fma): 32-key tiles and f32 FMAs, lanes splitting the head dimension (512
-// contiguous bytes of a row per load), scores summed by a transposing butterfly.
+// f32 pages, up to 8 query rows (kernel _fma): 32-key tiles and f32 FMAs, lanes splitting the head
+// dimension (512 contiguous bytes of a row per load), scores summed by a transposing butterfly.
+// f32 pages, more rows (kernel _mma32): tiles of 32 query rows x 32 keys on mma.sync with q, K, P and V
+// in three bf16 terms each and the six products above 2^-24. A warp takes 16 rows x 16 keys and splits
+// the keys and values in its registers: ~1000 instructions for 256 (row, key) pairs, where the FMA
+// kernel needs ~950 for 64.
 
 #include <cuda_runtime.h>
 #include <math.h>
@@ -37,11 +41,11 @@ namespace {
 
 constexpr int kConsumers = 4;                       // consumer warps
 constexpr int kThreads = (kConsumers + 1) * 32;     // and one producer warp
-constexpr uint32_t kRing = 96 * 1024;               // bytes of the tile ring
 
-// Shared memory: ring, two partial records of the join, then barriers and small words.
-template <int HD, int KT, int ES, int R>
+// Shared memory: tile ring, two partial records of the join, then barriers and small words.
+template <int HD, int KT, int ES, int R, int RING = 96 * 1024>
 struct PgLayout {
+  static constexpr uint32_t kRing = RING;
   static constexpr uint32_t kTile = (uint32_t)KT * HD * ES;     // K or V of one stage
   static constexpr int kStages = kRing / (2 * kTile);
   static constexpr uint32_t off_join = kRing;
@@ -58,24 +62,22 @@ __device__ __forceinline__ void consumer_sync() {
 }
 
 // ------------------------------------------------------------------ producer
-// Lane l of the producer copies one piece of a tile: pieces of a page's rows (and of 64 columns
-// for the swizzled tensor copies), K and V.
-template <int HD, int KT, bool BF>
+// Lane l of the producer copies one piece of a tile: pieces of a page's rows (and of 128 bytes of
+// columns for the swizzled tensor copies), K and V.
+template <class LY, int HD, int KT, int ES, bool TENSOR>
 __device__ __forceinline__ void produce(const PagedAttnArgs& a, const CUtensorMap* tk,
                                         const CUtensorMap* tv, const PagedStart* st, uint8_t* sm,
                                         uint64_t* full, uint64_t* empty) {
-  constexpr int ES = BF ? 2 : 4;
-  using LY = PgLayout<HD, KT, ES, 8>;  // ring part only: the same for every R
   constexpr int NS = LY::kStages;
-  constexpr int COLS = BF ? HD / 64 : 1;  // column blocks of a row
+  constexpr int COLS = TENSOR ? HD * ES / 128 : 1;  // column blocks of a row
   const int lane = threadIdx.x & 31;
   const int prow = min(KT, 1 << a.c.page_shift);  // rows of a piece
   const int np = KT / prow;                       // pieces of KT keys
   const int piece = lane % np, rest = lane / np;  // piece, then (K or V, column block)
   const bool mine = rest < 2 * COLS;
   const int kv = rest & 1, cb = rest >> 1;
-  const uint32_t dst = kv * LY::kTile + (BF ? cb * (KT * 128) + piece * prow * 128
-                                            : piece * prow * HD * ES);
+  const uint32_t dst = kv * LY::kTile + (TENSOR ? cb * (KT * 128) + piece * prow * 128
+                                                : piece * prow * HD * ES);
   PagedCursor c = paged_cursor<KT>(a, st);
   int issued = 0;
   bool ok = true, more = true;
@@ -115,8 +117,8 @@ __device__ __forceinline__ void produce(const PagedAttnArgs& a, const CUtensorMa
     if (mine && now >= 0) {
       const long long row = paged_row(a, now, kvh, key);
       uint8_t* to = sm + (uint32_t)stage * 2 * LY::kTile + dst;
-      if constexpr (BF)
-        tma_load_2d(to, kv ? tv : tk, cb * 64, (int)row, &full[stage]);
+      if constexpr (TENSOR)
+        tma_load_2d(to, kv ? tv : tk, cb * (128 / ES), (int)row, &full[stage]);
       else
         bulk_load(to, static_cast<const float*>(kv ? a.c.v_pages : a.c.k_pages) + row * HD,
                   (uint32_t)prow * HD * ES, &full[stage]);
@@ -229,18 +231,18 @@ __device__ __forceinline__ bool open_cta(const PagedAttnArgs& a, uint8_t* sm) {
   return st->any;
 }
 
-// Join of the four warps' (m, l) in ml_s [warp][R]: the rows' (m, l) into row_ml, and in ml_s[..].x
-// the factor of each warp's o.
-template <int R>
+// Join of the NW records' (m, l) in ml_s [record][R] (a warp's keys each): the rows' (m, l) into
+// row_ml, and in ml_s[..].x the factor of each record's o.
+template <int R, int NW = kConsumers>
 __device__ __forceinline__ void join_rows(float2* ml_s, float2* row_ml) {
   consumer_sync();
   if (threadIdx.x < R) {
     float M = -INFINITY, den = 0.f;
 #pragma unroll
-    for (int x = 0; x < kConsumers; ++x) M = fmaxf(M, ml_s[x * R + threadIdx.x].x);
+    for (int x = 0; x < NW; ++x) M = fmaxf(M, ml_s[x * R + threadIdx.x].x);
     const float mu = M == -INFINITY ? 0.f : M;
 #pragma unroll
-    for (int x = 0; x < kConsumers; ++x) {
+    for (int x = 0; x < NW; ++x) {
       const float w = paged_exp2(ml_s[x * R + threadIdx.x].x - mu);
       den = fmaf(w, ml_s[x * R + threadIdx.x].y, den);
       ml_s[x * R + threadIdx.x].x = w;
@@ -295,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (!open_cta<KT, LY>(a, sm)) return pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == kConsumers) {
-    produce<HD, KT, true>(a, &tk, &tv, st, sm, full, empty);
+    produce<LY, HD, KT, 2, true>(a, &tk, &tv, st, sm, full, empty);
     return pdl_wait();
   }
   float* join = reinterpret_cast<float*>(sm + LY::off_join);
@@ -514,6 +516,221 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (bad && lane == 0 && a.c.status) atomicOr(a.c.status, PG_TIMEOUT);
 }
 
+// ------------------------------------------------------------------ f32 pages, many rows: mma.sync
+// Warp (kh, rh) = (warp & 1, warp >> 1) takes keys 16 kh .. and rows 16 rh .. of every 32 x 32 tile.
+// Which of a fragment's k and n positions a column or a key takes is free as long as both operands
+// agree; the places below let every thread read 16 bytes at once without bank conflicts:
+//   scores:  k position 2q + e (8 + 2q + e) of a k-step is column 4q + e (4q + 2 + e); the staged q
+//            has its columns in that order; n position n is key n for even n, ((n - 1) ^ 4) + 1 for odd
+//   outputs: k positions are the scores' keys; n position n of tile 4 blk + j is column 32 blk + 4n + j
+template <int HD>
+using Mma32Layout = PgLayout<HD, 32, 4, 32, 64 * 1024>;
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 2)
+    paged_attn_mma32_kernel(const __grid_constant__ PagedAttnArgs a,
+                            const __grid_constant__ CUtensorMap tk,
+                            const __grid_constant__ CUtensorMap tv) {
+  constexpr int KT = 32, R = 32, KS = HD / 16, NB = HD / 32;
+  using LY = Mma32Layout<HD>;
+  constexpr int NS = LY::kStages;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + LY::off_bar);
+  uint64_t* empty = full + NS;
+  PagedStart* st = reinterpret_cast<PagedStart*>(sm + LY::off_start);
+  if (!open_cta<KT, LY>(a, sm)) return pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == kConsumers) {
+    produce<LY, HD, KT, 4, true>(a, &tk, &tv, st, sm, full, empty);
+    return pdl_wait();
+  }
+  float* join = reinterpret_cast<float*>(sm + LY::off_join);
+  float2* ml_s = reinterpret_cast<float2*>(sm + LY::off_ml);
+  float2* row_ml = reinterpret_cast<float2*>(sm + LY::off_row);
+  int* flag = reinterpret_cast<int*>(sm + LY::off_start + 96 + 40);
+
+  const int g = lane >> 2, q = lane & 3, mat = lane >> 3, mr = lane & 7;
+  const int kh = warp & 1, rh = warp >> 1;
+  const int key_n = g & 1 ? ((g - 1) ^ 4) + 1 : g;         // key of n position g
+  const int key_a = 2 * q, key_b = ((2 * q) ^ 4) + 1;      // of n (and k) positions 2q, 2q + 1
+  constexpr uint32_t kPlane = R * HD * 2;                  // a term of q
+  const uint32_t gmul = 65536u / a.gq + 1;
+  PagedCursor c = paged_cursor<KT>(a, st);
+  int seen = 0;
+  bool bad = false;
+  do {
+    const int n = c.kend - c.kt;
+    const int tok0 = c.rt * a.tpt, rows = min(a.tpt, c.s.nb - tok0) * a.gq;
+    {  // q's terms in shared memory (where the join works at the item's end)
+      uint8_t* to = reinterpret_cast<uint8_t*>(join);
+#pragma unroll 1
+      for (int i = threadIdx.x; i < R * HD / 8; i += kConsumers * 32) {
+        const int r = i / (HD / 8), u = i % (HD / 8), t = paged_token(r, gmul);
+        const size_t at = (size_t)(c.s.lo + tok0 + t) * a.ldq + (size_t)(c.kvh * a.gq + r - t * a.gq) * HD + u * 8;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+        if (r < rows) {
+          if (a.act_bf16) {
+            x = KvElem<true>::load4(static_cast<const uint16_t*>(a.q) + at);
+            y = KvElem<true>::load4(static_cast<const uint16_t*>(a.q) + at + 4);
+          } else {
+            x = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at));
+            y = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at + 4));
+          }
+        }
+        uint32_t t0[3], t1[3], t2[3], t3[3];  // terms of columns (0, 1), (2, 3), (4, 5), (6, 7)
+        split3(x.x, x.y, t0[0], t0[1], t0[2]);
+        split3(x.z, x.w, t1[0], t1[1], t1[2]);
+        split3(y.x, y.y, t2[0], t2[1], t2[2]);
+        split3(y.z, y.w, t3[0], t3[1], t3[2]);
+        uint8_t* row = to + r * (HD * 2) + (u & 1) * 8;
+        const int ch = u & ~1;
+#pragma unroll
+        for (int e = 0; e < 3; ++e) {
+          *reinterpret_cast<uint2*>(row + e * kPlane + ((ch ^ (r & 7)) << 4)) = make_uint2(t0[e], t2[e]);
+          *reinterpret_cast<uint2*>(row + e * kPlane + (((ch + 1) ^ (r & 7)) << 4)) = make_uint2(t1[e], t3[e]);
+        }
+      }
+    }
+    consumer_sync();
+    const uint32_t qrow = smem_addr(join) + (16 * rh + (mat & 1) * 8 + mr) * (HD * 2);
+    int lim[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = 16 * rh + g + 8 * i, t = tok0 + paged_token(r, gmul);
+      lim[i] = r >= rows ? 0 : a.prefix_pass ? c.limit : min(max(c.s.base + t + 1, 0), c.s.len);
+    }
+    float o[4 * NB][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int d = 0; d < 4 * NB; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
+
+    for (int x = 0; x < n; ++x, ++seen) {
+      const int stage = seen % NS;
+      if (!bad)
+        bad = !__all_sync(0xffffffffu, mbar_wait(&full[stage], (uint32_t)((seen / NS) & 1), a.wait_ns));
+      const uint8_t* kb = sm + (uint32_t)stage * 2 * LY::kTile;
+      const uint8_t* vb = kb + LY::kTile;
+      float s[2][4], s2[2][4];  // first products; the small ones
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[0][i] = s[1][i] = s2[0][i] = s2[1][i] = 0.f;
+#pragma unroll 2
+      for (int ks = 0; ks < KS; ++ks) {
+        uint32_t q0[4], q1[4], q2[4];
+        const uint32_t ch = ((ks * 2 + (mat >> 1)) ^ mr) << 4;
+        ldsm4(qrow + ch, q0);
+        ldsm4(qrow + kPlane + ch, q1);
+        ldsm4(qrow + 2 * kPlane + ch, q2);
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          const int row = 16 * kh + 8 * nt + key_n;
+          const float4 k = *reinterpret_cast<const float4*>(
+              kb + (ks >> 1) * (KT * 128) + row * 128 + ((((ks & 1) * 4 + q) ^ (row & 7)) << 4));
+          uint32_t b[3], d[3];
+          split3(k.x, k.y, b[0], b[1], b[2]);
+          split3(k.z, k.w, d[0], d[1], d[2]);
+          mma16816(s[nt], q0[0], q0[1], q0[2], q0[3], b[0], d[0]);
+          mma16816(s2[nt], q2[0], q2[1], q2[2], q2[3], b[0], d[0]);
+          mma16816(s2[nt], q1[0], q1[1], q1[2], q1[3], b[1], d[1]);
+          mma16816(s2[nt], q0[0], q0[1], q0[2], q0[3], b[2], d[2]);
+          mma16816(s2[nt], q1[0], q1[1], q1[2], q1[3], b[0], d[0]);
+          mma16816(s2[nt], q0[0], q0[1], q0[2], q0[3], b[1], d[1]);
+        }
+      }
+      const int k0 = (c.kt + x) * KT + 16 * kh;  // this warp's first key
+      const bool edge = k0 + 16 > c.limit - a.tpt;
+      float p[2][4], alpha[2];
+      bool moved = false;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int nt = e >> 1;
+          float v = (s[nt][2 * i + (e & 1)] + s2[nt][2 * i + (e & 1)]) * a.scale_log2;
+          if ((edge || rows < R) && k0 + nt * 8 + (e & 1 ? key_b : key_a) >= lim[i]) v = -INFINITY;
+          p[i][e] = v;
+          mx = fmaxf(mx, v);
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(m[i], mx);
+        const float mu = mn == -INFINITY ? 0.f : mn;
+        alpha[i] = paged_exp2(m[i] - mu);
+        moved = moved || mn != m[i];
+        m[i] = mn;
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          p[i][e] = paged_exp2(p[i][e] - mu);
+          sum += p[i][e];
+        }
+        l[i] = l[i] * alpha[i] + sum;
+      }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int d = 0; d < 4 * NB; ++d)
+          o[d][0] *= alpha[0], o[d][1] *= alpha[0], o[d][2] *= alpha[1], o[d][3] *= alpha[1];
+      }
+      uint32_t pt[3][4];  // P's terms as A fragments
+      split3(p[0][0], p[0][1], pt[0][0], pt[1][0], pt[2][0]);
+      split3(p[1][0], p[1][1], pt[0][1], pt[1][1], pt[2][1]);
+      split3(p[0][2], p[0][3], pt[0][2], pt[1][2], pt[2][2]);
+      split3(p[1][2], p[1][3], pt[0][3], pt[1][3], pt[2][3]);
+      const int left = c.limit - k0;  // behind the last key lies whatever the page held
+#pragma unroll
+      for (int blk = 0; blk < NB; ++blk) {
+        float v[4][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = (e & 1 ? key_b : key_a) + (e & 2 ? 8 : 0), row = 16 * kh + key;
+          const float4 f = *reinterpret_cast<const float4*>(vb + blk * (KT * 128) + row * 128 +
+                                                            ((g ^ (row & 7)) << 4));
+          const bool in = key < left;
+          v[e][0] = in ? f.x : 0.f, v[e][1] = in ? f.y : 0.f, v[e][2] = in ? f.z : 0.f, v[e][3] = in ? f.w : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t b[3], d[3];
+          split3(v[0][j], v[1][j], b[0], b[1], b[2]);
+          split3(v[2][j], v[3][j], d[0], d[1], d[2]);
+          float(&od)[4] = o[4 * blk + j];
+          mma16816(od, pt[2][0], pt[2][1], pt[2][2], pt[2][3], b[0], d[0]);
+          mma16816(od, pt[1][0], pt[1][1], pt[1][2], pt[1][3], b[1], d[1]);
+          mma16816(od, pt[0][0], pt[0][1], pt[0][2], pt[0][3], b[2], d[2]);
+          mma16816(od, pt[1][0], pt[1][1], pt[1][2], pt[1][3], b[0], d[0]);
+          mma16816(od, pt[0][0], pt[0][1], pt[0][2], pt[0][3], b[1], d[1]);
+          mma16816(od, pt[0][0], pt[0][1], pt[0][2], pt[0][3], b[0], d[0]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cta(&empty[stage]);
+    }
+    // the two key halves are the join's two records
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      if (q == 0) ml_s[kh * R + 16 * rh + g + 8 * i] = make_float2(m[i], l[i]);
+    }
+    join_rows<R, 2>(ml_s, row_ml);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = 16 * rh + g + 8 * i;
+      const float w = ml_s[kh * R + r].x;
+      float* at = join + kh * (R * HD) + r * HD + 8 * q;
+#pragma unroll
+      for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<float4*>(at + 32 * blk + 4 * e) =
+              make_float4(o[4 * blk][2 * i + e] * w, o[4 * blk + 1][2 * i + e] * w,
+                          o[4 * blk + 2][2 * i + e] * w, o[4 * blk + 3][2 * i + e] * w);
+    }
+    consumer_sync();
+    finish_segment<HD, R>(a, c, gmul, join, row_ml, flag);
+    consumer_sync();
+  } while (c.next<KT>(a));
+  if (bad && lane == 0 && a.c.status) atomicOr(a.c.status, PG_TIMEOUT);
+}
+
 // ------------------------------------------------------------------ f32 pages: FMAs
 template <int E>
 struct Lane;  // E consecutive floats of a lane
@@ -546,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (!open_cta<KT, LY>(a, sm)) return pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == kConsumers) {
-    produce<HD, KT, false>(a, nullptr, nullptr, st, sm, full, empty);
+    produce<LY, HD, KT, 4, false>(a, nullptr, nullptr, st, sm, full, empty);
     return pdl_wait();
   }
   float* join = reinterpret_cast<float*>(sm + LY::off_join);
@@ -683,6 +900,16 @@ cudaError_t launch_mma(const PagedAttnArgs& a, int grid, cudaStream_t s) {
   return launch_pdl(paged_attn_mma_kernel<HD, NT>, dim3(grid), kThreads, PgLayout<HD, 64, 2, R>::bytes, s,
                     a, tk, tv);
 }
+template <int HD>
+cudaError_t launch_mma32(const PagedAttnArgs& a, int grid, cudaStream_t s) {
+  CUtensorMap tk, tv;
+  const uint64_t rows = (uint64_t)a.c.n_pages * a.c.nkv << a.c.page_shift;
+  const uint32_t box = std::min(32, 1 << a.c.page_shift);
+  if (!make_tmap_f32_2d(&tk, a.c.k_pages, rows, HD, box) ||
+      !make_tmap_f32_2d(&tv, a.c.v_pages, rows, HD, box))
+    return cudaErrorInvalidValue;
+  return launch_pdl(paged_attn_mma32_kernel<HD>, dim3(grid), kThreads, Mma32Layout<HD>::bytes, s, a, tk, tv);
+}
 template <int HD, int R>
 cudaError_t launch_fma(const PagedAttnArgs& a, int grid, cudaStream_t s) {
   return launch_pdl(paged_attn_fma_kernel<HD, R>, dim3(grid), kThreads, PgLayout<HD, 32, 4, R>::bytes, s, a);
@@ -692,6 +919,7 @@ cudaError_t launch_pass(const PagedAttnArgs& a, const PagedPlan& p, cudaStream_t
   if (p.tc) return launch_paged_tc(a, HD, p.grid, s);
   if (a.c.kv_bf16)
     return a.act_bf16 ? launch_mma<HD, 1>(a, p.grid, s) : launch_mma<HD, 3>(a, p.grid, s);
+  if (p.rows == 32) return launch_mma32<HD>(a, p.grid, s);
   if (p.rows == 2) return launch_fma<HD, 2>(a, p.grid, s);
   if (p.rows == 4) return launch_fma<HD, 4>(a, p.grid, s);
   return launch_fma<HD, 8>(a, p.grid, s);
@@ -705,6 +933,7 @@ template <int HD>
 cudaError_t set_attributes_hd() {
   cudaError_t e = allow_smem(paged_attn_mma_kernel<HD, 1>, PgLayout<HD, 64, 2, 16>::bytes);
   if (e == cudaSuccess) e = allow_smem(paged_attn_mma_kernel<HD, 3>, PgLayout<HD, 64, 2, 8>::bytes);
+  if (e == cudaSuccess) e = allow_smem(paged_attn_mma32_kernel<HD>, Mma32Layout<HD>::bytes);
   if (e == cudaSuccess) e = allow_smem(paged_attn_fma_kernel<HD, 2>, PgLayout<HD, 32, 4, 2>::bytes);
   if (e == cudaSuccess) e = allow_smem(paged_attn_fma_kernel<HD, 4>, PgLayout<HD, 32, 4, 4>::bytes);
   if (e == cudaSuccess) e = allow_smem(paged_attn_fma_kernel<HD, 8>, PgLayout<HD, 32, 4, 8>::bytes);
@@ -723,8 +952,9 @@ int slot_rows(int n_tokens) {
 struct Workspace {
   size_t counters = 0, splits[2], ml[2], o[2], whole_ml, whole_o, total;
   Workspace(int n_tokens, int nq, int hd, bool prefix) {
-    // an item of more than 16 rows belongs to one CTA per SM, smaller ones to two
-    const size_t rows = (size_t)2 * std::max(kMaxSms * slot_rows(n_tokens), 2 * kMaxSms * 16);
+    // an item of more than 32 rows belongs to one CTA per SM, smaller ones to two
+    const int most = slot_rows(n_tokens);
+    const size_t rows = (size_t)2 * std::max(kMaxSms * most, 2 * kMaxSms * std::min(32, most));
     splits[0] = align256(2 * kMaxSms * 4);
     splits[1] = splits[0] + align256(2 * kMaxSms * sizeof(PagedSplit));
     size_t at = splits[1] + align256(2 * kMaxSms * sizeof(PagedSplit));
@@ -767,7 +997,7 @@ PagedPlan plan_paged_pass(const PagedAttnArgs& a, int hd, int max_rows, int sms)
     if (p.tc) p.item_units = 3;  // 4 us against 1.5 us for a tile of 128 keys
   } else {
     p.kt = 32;
-    p.rows = max_rows <= 2 ? 2 : max_rows <= 4 ? 4 : 8;  // the smallest tile that holds them
+    p.rows = max_rows <= 2 ? 2 : max_rows <= 4 ? 4 : max_rows <= 8 ? 8 : 32;  // the smallest that holds them
     p.grid = 2 * sms;
   }
   return p;

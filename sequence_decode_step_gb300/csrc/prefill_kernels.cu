@@ -1068,20 +1068,30 @@ static EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// Row-major bf16 [rows, cols] (cols contiguous), boxes of 64 columns x box_rows rows,
-// 128-byte swizzle, zero fill outside the tensor.
-bool make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
-                       uint32_t box_rows) {
+// Row-major [rows, cols] (cols contiguous) of bf16 (es = 2) or f32 (es = 4), boxes of 128 bytes of
+// columns x box_rows rows, 128-byte swizzle, zero fill outside the tensor.
+static bool make_tmap_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
+                         uint32_t box_rows, uint32_t es) {
   EncodeTiledFn fn = encode_fn();
-  if (!fn || (cols * 2) % 16 || (reinterpret_cast<uintptr_t>(base) & 15) || box_rows > 256)
+  if (!fn || (cols * es) % 16 || (reinterpret_cast<uintptr_t>(base) & 15) || box_rows > 256)
     return false;
   const cuuint64_t dims[2] = {cols, rows};
-  const cuuint64_t strides[1] = {cols * 2};
-  const cuuint32_t box[2] = {(cuuint32_t)GBK, box_rows};
+  const cuuint64_t strides[1] = {cols * es};
+  const cuuint32_t box[2] = {128 / es, box_rows};
   const cuuint32_t estr[2] = {1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  const CUtensorMapDataType type =
+      es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+  return fn(map, type, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
+                       uint32_t box_rows) {
+  return make_tmap_2d(map, base, rows, cols, box_rows, 2);
+}
+bool make_tmap_f32_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
+                      uint32_t box_rows) {
+  return make_tmap_2d(map, base, rows, cols, box_rows, 4);
 }
 
 constexpr size_t kGemmSmemBudget = 200 * 1024;

@@ -168,6 +168,8 @@ constexpr int kResidBN = 128;
 constexpr int kResidSplit = 2;
 bool make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                        uint32_t box_rows);
+bool make_tmap_f32_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
+                      uint32_t box_rows);
 // b_lo: the weight's lo term (nullptr for exact bf16 weights); with it each product is
 // A_hi B_hi + A_lo B_hi + A_hi B_lo.
 cudaError_t launch_gemm(int bn, int epi, const CUtensorMap& a_hi, const CUtensorMap& a_lo,
