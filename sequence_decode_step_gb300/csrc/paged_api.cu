@@ -163,6 +163,8 @@ extern "C" int qw_paged_attention(const qw_paged_kv* c, const void* q, uint32_t 
     return fail(QW_ERR_ARG,
                 "qw_paged_attention: n_q_heads must be a multiple of n_kv_heads, at most 8 times it");
   if (max_new < 1) return fail(QW_ERR_ARG, "qw_paged_attention: max_new must be at least 1");
+  if ((int64_t)n_tokens * n_q_heads > INT32_MAX)
+    return fail(QW_ERR_ARG, "qw_paged_attention: n_tokens * n_q_heads must be below 2^31");
   if (n_tokens == 0) return QW_OK;
   if (!q || !out || !workspace) return fail(QW_ERR_ARG, "qw_paged_attention: null buffer");
   const int hd = c->head_dim, align = act_format == QW_ACT_BF16 ? 8 : 4;

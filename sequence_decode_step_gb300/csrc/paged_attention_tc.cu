@@ -336,48 +336,58 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
       const int lim = !live           ? 0
                       : a.prefix_pass ? c.limit
                                       : min(max(c.s.base + tok0 + token_of(r) + 1, 0), c.s.len);
-      // q into shared memory, K-major with 128-byte swizzling: the warp's 32 rows, whole rows at a
-      // time (16-byte units of 8 columns; a unit of f32 activations comes as two loads)
+      // This thread's row as others of its warp move it (whole rows at a time): token and head
+      const int rtok = token_of(r), rhead = c.kvh * a.gq + r - rtok * a.gq;
+      // q into shared memory, K-major with 128-byte swizzling, in 16-byte units of 8 columns
       {
-        constexpr int RU = HD / 8, RPI = 32 / RU, NB = 8;  // units of a row, rows per load, loads in flight
+        constexpr int RU = HD / 8, RPI = 32 / RU;  // units of a row, rows per step
         const int u = lane % RU, sub = lane / RU;
-        uint8_t* base = sm + (NT == 1 ? s * LY::kQ1 : 0);
-        const uint32_t col = (uint32_t)(u >> 3) * (128 * 128);
+        uint8_t* base = sm + (NT == 1 ? s * LY::kQ1 : 0) + (u >> 3) * (128 * 128) + (warp & 3) * 4096;
+        auto place = [&](int i) {  // of row i of the warp
+          return base + (i >> 3) * 1024 + (i & 7) * 128 + (((u & 7) ^ (i & 7)) << 4);
+        };
+        auto source = [&](int i) {
+          const int t = __shfl_sync(0xffffffffu, rtok, i), h = __shfl_sync(0xffffffffu, rhead, i);
+          return (size_t)(c.s.lo + tok0 + t) * a.ldq + (size_t)h * HD + u * 8;
+        };
+        const int live_rows = rows - (warp & 3) * 32;
+        if constexpr (NT == 1) {
+#pragma unroll 4
+          for (int i0 = 0; i0 < 32; i0 += RPI) {
+            const int i = i0 + sub;
+            const size_t at = source(i);
+            const bool in = i < live_rows;  // (a row that is not there: zeros)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(place(i))),
+                         "l"(static_cast<const uint16_t*>(a.q) + (in ? at : 0)), "r"(in ? 16 : 0)
+                         : "memory");
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+        } else {
+          constexpr int NB = 4;
 #pragma unroll 1
-        for (int i0 = 0; i0 < 32 / RPI; i0 += NB) {
-          uint4 v[NB], w[NT == 3 ? NB : 1];
+          for (int i0 = 0; i0 < 32; i0 += NB * RPI) {
+            float4 v[NB][2];
 #pragma unroll
-          for (int i = 0; i < NB; ++i) {
-            const int rr = (warp & 3) * 32 + (i0 + i) * RPI + sub, t = token_of(rr);
-            const size_t at = (size_t)(c.s.lo + tok0 + t) * a.ldq +
-                              (size_t)(c.kvh * a.gq + (rr - t * a.gq)) * HD + u * 8;
-            v[i] = make_uint4(0, 0, 0, 0);
-            if constexpr (NT == 1) {
-              if (rr < rows) v[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at));
-            } else {
-              w[i] = v[i];
-              if (rr < rows) {
-                const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(a.q) + at);
-                v[i] = __ldg(p);
-                w[i] = __ldg(p + 1);
+            for (int k = 0; k < NB; ++k) {
+              const int i = i0 + k * RPI + sub;
+              const size_t at = source(i);
+              v[k][0] = v[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (i < live_rows) {
+                const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at);
+                v[k][0] = __ldg(p);
+                v[k][1] = __ldg(p + 1);
               }
             }
-          }
 #pragma unroll
-          for (int i = 0; i < NB; ++i) {
-            const int rr = (warp & 3) * 32 + (i0 + i) * RPI + sub;
-            uint8_t* to = base + col + (rr >> 3) * 1024 + (rr & 7) * 128 + (((u & 7) ^ (rr & 7)) << 4);
-            if constexpr (NT == 1) {
-              *reinterpret_cast<uint4*>(to) = v[i];
-            } else {
-              uint32_t h[4], m[4], l[4];
-              split3(__uint_as_float(v[i].x), __uint_as_float(v[i].y), h[0], m[0], l[0]);
-              split3(__uint_as_float(v[i].z), __uint_as_float(v[i].w), h[1], m[1], l[1]);
-              split3(__uint_as_float(w[i].x), __uint_as_float(w[i].y), h[2], m[2], l[2]);
-              split3(__uint_as_float(w[i].z), __uint_as_float(w[i].w), h[3], m[3], l[3]);
-              *reinterpret_cast<uint4*>(to) = make_uint4(h[0], h[1], h[2], h[3]);
-              *reinterpret_cast<uint4*>(to + LY::kQ1) = make_uint4(m[0], m[1], m[2], m[3]);
-              *reinterpret_cast<uint4*>(to + 2 * LY::kQ1) = make_uint4(l[0], l[1], l[2], l[3]);
+            for (int k = 0; k < NB; ++k) {
+              uint4 t[3];
+              split3(v[k][0].x, v[k][0].y, t[0].x, t[1].x, t[2].x);
+              split3(v[k][0].z, v[k][0].w, t[0].y, t[1].y, t[2].y);
+              split3(v[k][1].x, v[k][1].y, t[0].z, t[1].z, t[2].z);
+              split3(v[k][1].z, v[k][1].w, t[0].w, t[1].w, t[2].w);
+              uint8_t* to = place(i0 + k * RPI + sub);
+#pragma unroll
+              for (int e = 0; e < 3; ++e) *reinterpret_cast<uint4*>(to + e * LY::kQ1) = t[e];
             }
           }
         }
@@ -506,41 +516,27 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
         tc_fence_after();
         if (whole && a.pre.o && !a.prefix_pass) pdl_wait();  // the prefix's records
         // O out through shared memory (the q tile's, which no MMA reads any more), 32 columns of the
-        // warp's 32 rows at a time, so that whole 128-byte lines leave. A row's factors and place are
-        // formed once: out = o wa + (the prefix's o) wb
+        // warp's 32 rows at a time, so that whole 128-byte lines leave. The row's own thread forms its
+        // factors and place: out = o wa + (the prefix's o) wb
         const size_t slot = (size_t)(2 * blockIdx.x + (first ? 1 : 0)) * a.slots.rows + s * half * a.gq;
         float* stage = reinterpret_cast<float*>(sm + s * LY::kQ1 + (warp & 3) * 4096);
-        const int lr = lane >> 3, lc = lane & 7;  // rows of 8 lanes
         const bool raw = !whole || a.prefix_pass, joins = whole && a.pre.o && !a.prefix_pass;
-        size_t at[8];
-        float wa[8], wb[8];
-        unsigned dead = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int rr = (warp & 3) * 32 + 4 * i + lr, t = token_of(rr);
-          const size_t row = (size_t)(c.s.lo + tok0 + t) * a.nq + c.kvh * a.gq + (rr - t * a.gq);
-          const float rm = __shfl_sync(0xffffffffu, m, 4 * i + lr);
-          const float rl = __shfl_sync(0xffffffffu, l, 4 * i + lr);
-          at[i] = (whole ? row : slot + rr) * HD + 4 * lc;
-          wa[i] = raw ? 1.f : rl > 0.f || rl != rl ? 1.f / rl : 0.f;
-          wb[i] = 0.f;
-          if (rr >= rows) {
-            dead |= 1u << i;
-            at[i] = 0;
-          } else if (joins) {
-            const float2 ml = __ldcg(a.pre.ml + row);
-            const float top = fmaxf(rm, ml.x);
-            if (top != -INFINITY) {
-              const float f = paged_exp2(rm - top), g = paged_exp2(ml.x - top);
-              const float inv = 1.f / fmaf(rl, f, ml.y * g);
-              wa[i] = f * inv;
-              wb[i] = g * inv;
-            }
-          } else if (whole && a.prefix_pass && lc == 0) {
-            a.pre.ml[row] = make_float2(rm, rl);
-          }
+        const size_t row = whole ? (size_t)(c.s.lo + tok0 + rtok) * a.nq + rhead : slot + r;
+        const int place = live ? (int)row : -1;  // (rows of a call fit: the host checks)
+        float wa = 1.f, wb = 0.f;
+        if (!raw) {
+          float2 ml = make_float2(-INFINITY, 0.f);
+          if (joins && live) ml = __ldcg(a.pre.ml + row);
+          const float top = fmaxf(m, ml.x), f = top == -INFINITY ? 0.f : paged_exp2(m - top);
+          const float g = top == -INFINITY ? 0.f : paged_exp2(ml.x - top), den = fmaf(l, f, ml.y * g);
+          const float inv = den > 0.f || den != den ? __frcp_rn(den) : 0.f;
+          wa = f * inv;
+          wb = g * inv;
+        } else if (live) {
+          __stcg((whole ? a.pre.ml : a.slots.ml) + row, make_float2(m, l));
         }
         float* const to_f = !whole ? a.slots.o : a.prefix_pass ? a.pre.o : static_cast<float*>(a.out);
+        const int lr = lane >> 3, lc = lane & 7;  // rows of 8 lanes
 #pragma unroll 1
         for (int d = 0; d < HD; d += 32) {
           uint32_t o[2][16];
@@ -555,26 +551,28 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
                 make_uint4(o[e >> 2][4 * (e & 3)], o[e >> 2][4 * (e & 3) + 1], o[e >> 2][4 * (e & 3) + 2],
                            o[e >> 2][4 * (e & 3) + 3]);
           __syncwarp();
-#pragma unroll
+#pragma unroll 2
           for (int i = 0; i < 8; ++i) {
             const int q = 4 * i + lr;
+            const int to_row = __shfl_sync(0xffffffffu, place, q);
+            const float fa = __shfl_sync(0xffffffffu, wa, q), fb = __shfl_sync(0xffffffffu, wb, q);
             float4 x = *reinterpret_cast<const float4*>(stage + q * 32 + ((lc ^ (q & 7)) << 2));
-            x.x *= wa[i], x.y *= wa[i], x.z *= wa[i], x.w *= wa[i];
-            if (dead >> i & 1) continue;
+            x.x *= fa, x.y *= fa, x.z *= fa, x.w *= fa;
+            if (to_row < 0) continue;
+            const size_t at = (size_t)to_row * HD + d + 4 * lc;
             if (joins) {
-              const float4 y = __ldcg(reinterpret_cast<const float4*>(a.pre.o + at[i] + d));
-              x.x = fmaf(wb[i], y.x, x.x), x.y = fmaf(wb[i], y.y, x.y);
-              x.z = fmaf(wb[i], y.z, x.z), x.w = fmaf(wb[i], y.w, x.w);
+              const float4 y = __ldcg(reinterpret_cast<const float4*>(a.pre.o + at));
+              x.x = fmaf(fb, y.x, x.x), x.y = fmaf(fb, y.y, x.y);
+              x.z = fmaf(fb, y.z, x.z), x.w = fmaf(fb, y.w, x.w);
             }
             if (!raw && NT == 1)
-              *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at[i] + d) =
+              *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
                   make_uint2(paged_pack(x.x, x.y), paged_pack(x.z, x.w));
             else
-              *reinterpret_cast<float4*>(to_f + at[i] + d) = x;
+              *reinterpret_cast<float4*>(to_f + at) = x;
           }
           __syncwarp();
         }
-        if (live && !whole) a.slots.ml[slot + r] = make_float2(m, l);
         tc_fence_before();
       }
       if (!whole && first && s == 0 && r == 0)  // the joining kernel's work
