@@ -241,12 +241,12 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
           issue_s(dq + s * (LY::kQ1 >> 4), dk + slot_at(2 * tiles), tm + 128 * s);
           commit(&s_full[s]);
         }
+        ok = kv_wait(2 * tiles + 1);
 #pragma unroll 1
         for (int x = 0; ok && x < n; ++x) {
           const int g = tiles + x;
           const uint64_t v = dv + slot_at(2 * g + 1), k = dk + slot_at(2 * g + 2);
           const bool last = x + 1 == n;
-          ok = kv_wait(2 * g + 1);
 #pragma unroll 1
           for (int s = 0; ok && s < streams; ++s) {
             const uint32_t p = tm + 128 * s;
@@ -272,6 +272,8 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
               issue_s(dq + s * (LY::kQ1 >> 4), k, p);  // into the columns P leaves
             }
             commit(last ? &o_full[s] : &s_full[s]);
+            // the next turn's values, while the queue still holds this turn's products
+            if (s == 0 && !last) ok = kv_wait(2 * g + 3);
           }
         }
       } else {
@@ -551,7 +553,7 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
                 make_uint4(o[e >> 2][4 * (e & 3)], o[e >> 2][4 * (e & 3) + 1], o[e >> 2][4 * (e & 3) + 2],
                            o[e >> 2][4 * (e & 3) + 3]);
           __syncwarp();
-#pragma unroll 2
+#pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int q = 4 * i + lr;
             const int to_row = __shfl_sync(0xffffffffu, place, q);
