@@ -131,6 +131,13 @@ __device__ __forceinline__ void produce(const PagedAttnArgs& a, const CUtensorMa
     mbar_wait(&full[i % NS], (uint32_t)((i / NS) & 1), kDrainNs);
 }
 
+// Place of column d of row r in a join record: 8-column groups exchanged by the row, so that the
+// eight rows of an mma fragment do not meet in the same banks.
+template <int HD>
+__device__ __forceinline__ int join_at(int r, int d) {
+  return r * HD + (d ^ ((r & 3) << 3));
+}
+
 // ------------------------------------------------------------------ end of an item's segment
 // The four warps' records are in join[0] + join[1] (o) and row_ml (m, l). A whole item is emitted;
 // a split one goes to this CTA's slot and the last CTA to arrive joins all of them in order.
@@ -152,8 +159,8 @@ __device__ __forceinline__ void finish_segment(const PagedAttnArgs& a, const Pag
       const int r = i / V4, d = (i % V4) * 4;
       PagedAcc acc;
       if (pass == 0) {
-        const float4 x = *reinterpret_cast<const float4*>(join + i * 4);
-        const float4 y = *reinterpret_cast<const float4*>(join + R * HD + i * 4);
+        const float4 x = *reinterpret_cast<const float4*>(join + join_at<HD>(r, d));
+        const float4 y = *reinterpret_cast<const float4*>(join + R * HD + join_at<HD>(r, d));
         acc.o = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
         acc.m = row_ml[r].x;
         acc.l = row_ml[r].y;
@@ -255,7 +262,7 @@ __device__ __forceinline__ void join_rows(float2* ml_s, float2* row_ml) {
 // ------------------------------------------------------------------ bf16 pages: mma.sync
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -470,10 +477,12 @@ __global__ void __launch_bounds__(kThreads, 2)
         ldsm4t(vb + (ch >> 3) * (KT * 128) + vrow * 128 + (((ch & 7) ^ (vrow & 7)) << 4), vf);
         if (left < 16) vf[0] &= vm0, vf[1] &= vm1, vf[2] &= vm0, vf[3] &= vm1;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float(&od)[4] = o[2 * d2 + h];
-          mma16816(od, pa[0], pa[1], pa[2], pa[3], vf[2 * h], vf[2 * h + 1]);
-          if constexpr (NT == 3) mma16816(od, pl[0], 0u, pl[1], 0u, vf[2 * h], vf[2 * h + 1]);
+        for (int h = 0; h < 2; ++h)
+          mma16816(o[2 * d2 + h], pa[0], pa[1], pa[2], pa[3], vf[2 * h], vf[2 * h + 1]);
+        if constexpr (NT == 3) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            mma16816(o[2 * d2 + h], pl[0], 0u, pl[1], 0u, vf[2 * h], vf[2 * h + 1]);
         }
       }
       __syncwarp();
@@ -500,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int d = 0; d < DT; ++d)
 #pragma unroll
           for (int i = 0; i < NRW; ++i) {
-            float2* at = reinterpret_cast<float2*>(join + (warp & 1) * (R * HD) + (g + 8 * i) * HD + d * 8 + q2);
+            float2* at = reinterpret_cast<float2*>(join + (warp & 1) * (R * HD) + join_at<HD>(g + 8 * i, d * 8 + q2));
             float2 b = make_float2(0.f, 0.f);
             if (step) b = *at;
             const float x = NT == 3 ? o[d][0] + o[d][2] : o[d][2 * i];
@@ -608,9 +617,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         bad = !__all_sync(0xffffffffu, mbar_wait(&full[stage], (uint32_t)((seen / NS) & 1), a.wait_ns));
       const uint8_t* kb = sm + (uint32_t)stage * 2 * LY::kTile;
       const uint8_t* vb = kb + LY::kTile;
-      float s[2][4], s2[2][4];  // first products; the small ones
+      // products of weight 1, 2^-8 and 2^-16 apart: six chains of mma with the two key groups
+      float s[2][4], s2[2][4], s3[2][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[0][i] = s[1][i] = s2[0][i] = s2[1][i] = 0.f;
+      for (int i = 0; i < 4; ++i)
+        s[0][i] = s[1][i] = s2[0][i] = s2[1][i] = s3[0][i] = s3[1][i] = 0.f;
 #pragma unroll 2
       for (int ks = 0; ks < KS; ++ks) {
         uint32_t q0[4], q1[4], q2[4];
@@ -618,21 +629,27 @@ __global__ void __launch_bounds__(kThreads, 2)
         ldsm4(qrow + ch, q0);
         ldsm4(qrow + kPlane + ch, q1);
         ldsm4(qrow + 2 * kPlane + ch, q2);
+        uint32_t b[2][3], d[2][3];
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
           const int row = 16 * kh + 8 * nt + key_n;
           const float4 k = *reinterpret_cast<const float4*>(
               kb + (ks >> 1) * (KT * 128) + row * 128 + ((((ks & 1) * 4 + q) ^ (row & 7)) << 4));
-          uint32_t b[3], d[3];
-          split3(k.x, k.y, b[0], b[1], b[2]);
-          split3(k.z, k.w, d[0], d[1], d[2]);
-          mma16816(s[nt], q0[0], q0[1], q0[2], q0[3], b[0], d[0]);
-          mma16816(s2[nt], q2[0], q2[1], q2[2], q2[3], b[0], d[0]);
-          mma16816(s2[nt], q1[0], q1[1], q1[2], q1[3], b[1], d[1]);
-          mma16816(s2[nt], q0[0], q0[1], q0[2], q0[3], b[2], d[2]);
-          mma16816(s2[nt], q1[0], q1[1], q1[2], q1[3], b[0], d[0]);
-          mma16816(s2[nt], q0[0], q0[1], q0[2], q0[3], b[1], d[1]);
+          split3(k.x, k.y, b[nt][0], b[nt][1], b[nt][2]);
+          split3(k.z, k.w, d[nt][0], d[nt][1], d[nt][2]);
         }
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) mma16816(s[nt], q0[0], q0[1], q0[2], q0[3], b[nt][0], d[nt][0]);
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) mma16816(s2[nt], q1[0], q1[1], q1[2], q1[3], b[nt][0], d[nt][0]);
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) mma16816(s3[nt], q2[0], q2[1], q2[2], q2[3], b[nt][0], d[nt][0]);
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) mma16816(s2[nt], q0[0], q0[1], q0[2], q0[3], b[nt][1], d[nt][1]);
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) mma16816(s3[nt], q1[0], q1[1], q1[2], q1[3], b[nt][1], d[nt][1]);
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) mma16816(s3[nt], q0[0], q0[1], q0[2], q0[3], b[nt][2], d[nt][2]);
       }
       const int k0 = (c.kt + x) * KT + 16 * kh;  // this warp's first key
       const bool edge = k0 + 16 > c.limit - a.tpt;
@@ -644,7 +661,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int nt = e >> 1;
-          float v = (s[nt][2 * i + (e & 1)] + s2[nt][2 * i + (e & 1)]) * a.scale_log2;
+          const int f = 2 * i + (e & 1);
+          float v = (s[nt][f] + (s2[nt][f] + s3[nt][f])) * a.scale_log2;
           if ((edge || rows < R) && k0 + nt * 8 + (e & 1 ? key_b : key_a) >= lim[i]) v = -INFINITY;
           p[i][e] = v;
           mx = fmaxf(mx, v);
@@ -686,19 +704,23 @@ __global__ void __launch_bounds__(kThreads, 2)
           const bool in = key < left;
           v[e][0] = in ? f.x : 0.f, v[e][1] = in ? f.y : 0.f, v[e][2] = in ? f.z : 0.f, v[e][3] = in ? f.w : 0.f;
         }
+        uint32_t b[4][3], d[4][3];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          uint32_t b[3], d[3];
-          split3(v[0][j], v[1][j], b[0], b[1], b[2]);
-          split3(v[2][j], v[3][j], d[0], d[1], d[2]);
-          float(&od)[4] = o[4 * blk + j];
-          mma16816(od, pt[2][0], pt[2][1], pt[2][2], pt[2][3], b[0], d[0]);
-          mma16816(od, pt[1][0], pt[1][1], pt[1][2], pt[1][3], b[1], d[1]);
-          mma16816(od, pt[0][0], pt[0][1], pt[0][2], pt[0][3], b[2], d[2]);
-          mma16816(od, pt[1][0], pt[1][1], pt[1][2], pt[1][3], b[0], d[0]);
-          mma16816(od, pt[0][0], pt[0][1], pt[0][2], pt[0][3], b[1], d[1]);
-          mma16816(od, pt[0][0], pt[0][1], pt[0][2], pt[0][3], b[0], d[0]);
+          split3(v[0][j], v[1][j], b[j][0], b[j][1], b[j][2]);
+          split3(v[2][j], v[3][j], d[j][0], d[j][1], d[j][2]);
         }
+        auto add = [&](int pe, int ve) {  // four independent outputs per product
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma16816(o[4 * blk + j], pt[pe][0], pt[pe][1], pt[pe][2], pt[pe][3], b[j][ve], d[j][ve]);
+        };
+        add(2, 0);
+        add(1, 1);
+        add(0, 2);
+        add(1, 0);
+        add(0, 1);
+        add(0, 0);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive_cta(&empty[stage]);
@@ -715,12 +737,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int i = 0; i < 2; ++i) {
       const int r = 16 * rh + g + 8 * i;
       const float w = ml_s[kh * R + r].x;
-      float* at = join + kh * (R * HD) + r * HD + 8 * q;
+      float* at = join + kh * (R * HD);
 #pragma unroll
       for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          *reinterpret_cast<float4*>(at + 32 * blk + 4 * e) =
+          *reinterpret_cast<float4*>(at + join_at<HD>(r, 32 * blk + 8 * q + 4 * e)) =
               make_float4(o[4 * blk][2 * i + e] * w, o[4 * blk + 1][2 * i + e] * w,
                           o[4 * blk + 2][2 * i + e] * w, o[4 * blk + 3][2 * i + e] * w);
     }
@@ -875,7 +897,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const float w = ml_s[warp * R + r].x;
-          float* at = join + (warp & 1) * (R * HD) + r * HD + lane * E;
+          float* at = join + (warp & 1) * (R * HD) + join_at<HD>(r, lane * E);
 #pragma unroll
           for (int e = 0; e < E; ++e) at[e] = fmaf(o[r][e], w, step ? at[e] : 0.f);
         }
