@@ -100,7 +100,6 @@ struct PagedPlan {
   bool tc;                  // paged_attention_tc.cu, else paged_attention.cu
   int kt, rows, grid, item_units;
 };
-PagedPlan plan_paged_pass(const PagedAttnArgs& a, int hd, int max_rows, int sms);
 size_t paged_attn_workspace_bytes(int n_tokens, int nq, int hd, bool prefix);
 cudaError_t launch_paged_attention(const PagedAttnArgs& base, int hd, int max_new, void* workspace,
                                    int sms, cudaStream_t s);

@@ -30,6 +30,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "paged.h"
 #include "paged_sched.cuh"
@@ -1006,21 +1007,35 @@ cudaError_t set_paged_attributes() {
 // Tiles of 32 KB that an item's q, join and output cost a CTA: 6 us against 1.3 us a tile.
 constexpr int kDecodeItemUnits = 5;
 
-// max_rows: the most query rows (tokens x heads of a KV head) that meet one key.
-PagedPlan plan_paged_pass(const PagedAttnArgs& a, int hd, int max_rows, int sms) {
+// Keys per tile, query rows per item, CTAs and an item's own cost of a launch over sequences with
+// `rows` query rows (tokens x heads of a KV head) that meet up to `keys` keys.
+//
+// bf16 pages: few rows run the mma.sync kernel; more than 16 the tensor-core tiles, unless there is so
+// little of it that their start (about 16 us with q, first product and output against 4) is most of the
+// time. Measured per tile and CTA: 1.3 us for 64 keys here, and for 128 keys there 1.5 us (bf16) or 2.9 us
+// (f32 in three terms): a 4K prefix of 128 rows takes 22 us against 43, a 2-key one 16 against 6.
+// f32 pages: the least tile of the FMA kernel that holds the rows, or tiles of 32 rows.
+PagedPlan plan_paged_pass(const PagedAttnArgs& a, long long rows, long long keys, int sms) {
   sms = std::min(sms, kMaxSms);
   PagedPlan p{};
   p.item_units = kDecodeItemUnits;
-  if (a.c.kv_bf16) {
-    p.tc = max_rows > 16;
-    p.kt = p.tc ? kPagedTcKeys : 64;
-    p.rows = p.tc ? paged_tc_rows(a.act_bf16) : a.act_bf16 ? 16 : 8;
-    p.grid = p.tc ? sms : 2 * sms;
-    if (p.tc) p.item_units = 3;  // 4 us against 1.5 us for a tile of 128 keys
-  } else {
+  p.grid = 2 * sms;
+  if (!a.c.kv_bf16) {
     p.kt = 32;
-    p.rows = max_rows <= 2 ? 2 : max_rows <= 4 ? 4 : max_rows <= 8 ? 8 : 32;  // the smallest that holds them
-    p.grid = 2 * sms;
+    p.rows = rows <= 2 ? 2 : rows <= 4 ? 4 : rows <= 8 ? 8 : 32;
+    return p;
+  }
+  p.kt = 64;
+  p.rows = a.act_bf16 ? 16 : 8;
+  if (rows > 16) {
+    auto us = [&](double start, double tile, int kt, int item_rows, int units, int grid) {
+      const double items = (double)a.c.nkv * ((rows + item_rows - 1) / item_rows);
+      return start + tile * std::ceil(items * (keys / kt + 1 + units) / grid);
+    };
+    const int tc_rows = paged_tc_rows(a.act_bf16), tc_units = 3;  // 4 us against 1.5 us a tile
+    if (us(16, a.act_bf16 ? 1.5 : 2.9, kPagedTcKeys, tc_rows, tc_units, sms) <
+        us(4, 1.3, p.kt, p.rows, p.item_units, p.grid))
+      p = PagedPlan{true, kPagedTcKeys, tc_rows, sms, tc_units};
   }
   return p;
 }
@@ -1041,20 +1056,20 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& base, int hd, int max_ne
     a.slots.rows = p.tc ? slot_rows(a.n_tokens) : p.rows;
     return hd == 64 ? launch_pass<64>(a, p, s) : launch_pass<128>(a, p, s);
   };
-  const long long cap = 1 << 20;  // row counts only choose a kernel
   // the line of a launch is counted in 32 bits
   auto too_long = [&](const PagedPlan& p, long long tiles, long long seqs) {
     const long long items = a.n_tokens / (p.rows / a.gq) + seqs;
     return tiles / p.kt + 4 > INT32_MAX / a.c.nkv / items;
   };
-  const int rows = (int)std::min(cap, (long long)std::min(max_new, a.n_tokens) * a.gq);
-  const PagedPlan own = plan_paged_pass(a, hd, rows, sms);
-  if (too_long(own, (long long)a.c.max_pages << a.c.page_shift, a.c.n_seqs)) return cudaErrorInvalidValue;
+  const long long cap = (long long)a.c.max_pages << a.c.page_shift;
+  // (the lengths are on the device: the longest that the table can hold stands for them)
+  const PagedPlan own = plan_paged_pass(a, (long long)std::min(max_new, a.n_tokens) * a.gq, cap, sms);
+  if (too_long(own, cap, a.c.n_seqs)) return cudaErrorInvalidValue;
   if (prefix) {
     a.pre.ml = reinterpret_cast<float2*>(ws + w.whole_ml);
     a.pre.o = reinterpret_cast<float*>(ws + w.whole_o);
     a.prefix_pass = 1;
-    const PagedPlan p = plan_paged_pass(a, hd, (int)std::min(cap, (long long)a.n_tokens * a.gq), sms);
+    const PagedPlan p = plan_paged_pass(a, (long long)a.n_tokens * a.gq, a.c.prefix_len, sms);
     if (too_long(p, a.c.prefix_len, 1)) return cudaErrorInvalidValue;
     cudaError_t e = run(p, 1);
     if (e == cudaSuccess) e = launch_paged_join(a, hd, p.grid, p.rows, s);

@@ -33,6 +33,24 @@ def _format(t, what: str) -> int:
     return f
 
 
+class Workspace:
+    """Scratch of PagedKV.attend, one for all caches whose calls follow one another (the layers of
+    a model): pass the first cache's ``workspace`` to the others."""
+
+    def __init__(self, device):
+        self.device, self.bytes, self.ptr = device, 0, None
+        self._kept = []
+
+    def grow(self, need: int) -> None:
+        torch = _torch()
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("the attention workspace is too small and cannot be made inside a graph "
+                               "capture: call reserve(n_tokens, n_q_heads) before it")
+        # smaller ones are kept: a captured graph may hold their address
+        self._kept.append(torch.zeros(need, dtype=torch.uint8, device=self.device))
+        self.bytes, self.ptr = need, self._kept[-1].data_ptr()
+
+
 class PagedKV:
     """One layer's pages and the batch that uses them (fields as in qw_paged_kv).
 
@@ -40,12 +58,13 @@ class PagedKV:
     page_table: int32 [n_seqs, max_pages]; kv_len: int32 [n_seqs], keys of each sequence with the
     call's new tokens; q_start: int32 [n_seqs + 1], first token row of each sequence;
     prefix_pages: int32 pages of ``prefix_len`` keys that all sequences share, or None.
+    workspace: another PagedKV's ``workspace``, to share its scratch.
     All are contiguous tensors on one CUDA device. They are borrowed, not copied: write new lengths
     or page ids into them between calls (or into a captured graph's inputs before a replay).
     """
 
     def __init__(self, k_pages, v_pages, page_table, kv_len, q_start, prefix_pages=None,
-                 prefix_len: int = 0):
+                 prefix_len: int = 0, workspace: "Workspace" = None):
         torch = _torch()
         if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
             raise ValueError("k_pages and v_pages: two [n_pages, n_kv_heads, page_size, head_dim] "
@@ -67,7 +86,9 @@ class PagedKV:
             raise ValueError("prefix_pages do not hold prefix_len keys")
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._keep = (k_pages, v_pages, page_table, kv_len, q_start, prefix_pages)
-        self._ws, self._ws_bytes, self._ws_ptr = [], 0, None
+        self.workspace = workspace if workspace is not None else Workspace(self.device)
+        if self.workspace.device != self.device:
+            raise ValueError("the workspace is on another device")
         self._lib = B.lib()
         self.head_dim = k_pages.shape[3]
         self.n_kv_heads = k_pages.shape[1]
@@ -148,8 +169,8 @@ class PagedKV:
     def attend(self, q, max_new: int = 1, out=None):
         """Attention of the tokens' rotated queries [n_tokens, n_q_heads, head_dim] over their
         sequences' keys (and the shared prefix). max_new: the most new tokens of one sequence.
-        The workspace is the cache's own: calls of one PagedKV (captured ones too) must not overlap on
-        the GPU, and it has to exist before a capture: call once before, or ``reserve``."""
+        Calls that share a workspace (those of one PagedKV, captured ones too) must not overlap on the
+        GPU, and it has to exist before a capture: call once before, or ``reserve``."""
         n = q.shape[0]
         width = q.shape[1] * q.shape[2] if q.dim() == 3 else q.shape[1]
         heads = width // self.head_dim
@@ -158,10 +179,11 @@ class PagedKV:
         out = self._out(out, q, heads)
         need = self._lib.qw_paged_attention_workspace_bytes(n, heads, self.head_dim,
                                                             self.c.prefix_len)
-        if self._ws_bytes < need:
-            self._grow(need)
+        ws = self.workspace
+        if ws.bytes < need:
+            ws.grow(need)
         rc = self._lib.qw_paged_attention(self._cref, q.data_ptr(), fmt, ld, n, heads, max_new,
-                                          out.data_ptr(), self._ws_ptr, self._ws_bytes, self._stream())
+                                          out.data_ptr(), ws.ptr, ws.bytes, self._stream())
         if rc:
             B.check("qw_paged_attention", rc)
         return out
@@ -170,17 +192,8 @@ class PagedKV:
         """Workspace for attention calls of up to n_tokens rows (as the first such call would)."""
         need = self._lib.qw_paged_attention_workspace_bytes(n_tokens, n_q_heads, self.head_dim,
                                                             self.c.prefix_len)
-        if self._ws_bytes < need:
-            self._grow(need)
-
-    def _grow(self, need: int) -> None:
-        torch = _torch()
-        if torch.cuda.is_current_stream_capturing():
-            raise RuntimeError("the attention workspace is too small and cannot be made inside a graph "
-                               "capture: call reserve(n_tokens, n_q_heads) before it")
-        # smaller ones are kept: a captured graph may hold their address
-        self._ws.append(torch.zeros(need, dtype=torch.uint8, device=self.device))
-        self._ws_bytes, self._ws_ptr = need, self._ws[-1].data_ptr()
+        if self.workspace.bytes < need:
+            self.workspace.grow(need)
 
     def check(self) -> None:
         """Raises if a call so far met a bad page id or length or gave up a wait (synchronises)."""

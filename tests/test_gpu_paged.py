@@ -336,6 +336,20 @@ def test_capture_needs_its_workspace_and_keeps_it():
     del filler
 
 
+def test_layers_share_a_workspace():
+    a = Batch([(1, 300), (1, 5)], 4, 2, 64, 16, "f32", "bf16", prefix=20, seed=79)
+    b = Batch([(1, 300), (1, 5)], 4, 2, 64, 16, "f32", "bf16", prefix=20, seed=83)
+    ca = a.cache()
+    cb = b.cache(workspace=ca.workspace)
+    ca.reserve(2, 4)
+    q = [a.q.cuda(), b.q.cuda()]
+    got = [(ca.attend(q[0]), cb.attend(q[1])) for _ in range(3)]
+    for x, y in got:
+        attend_close(a, x)
+        attend_close(b, y)
+    assert ca.workspace is cb.workspace and len(ca.workspace._kept) == 1
+
+
 def test_other_streams():
     b = Batch([(1, 500), (1, 3)], 8, 2, 128, 16, "bf16", "bf16", seed=43)
     c = b.cache()
