@@ -477,13 +477,24 @@ __global__ void __launch_bounds__(kThreads, 2)
         uint32_t vf[4];
         ldsm4t(vb + (ch >> 3) * (KT * 128) + vrow * 128 + (((ch & 7) ^ (vrow & 7)) << 4), vf);
         if (left < 16) vf[0] &= vm0, vf[1] &= vm1, vf[2] &= vm0, vf[3] &= vm1;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          mma16816(o[2 * d2 + h], pa[0], pa[1], pa[2], pa[3], vf[2 * h], vf[2 * h + 1]);
-        if constexpr (NT == 3) {
+        if constexpr (NT == 1) {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            mma16816(o[2 * d2 + h], pl[0], 0u, pl[1], 0u, vf[2 * h], vf[2 * h + 1]);
+            mma16816(o[2 * d2 + h], pa[0], pa[1], pa[2], pa[3], vf[2 * h], vf[2 * h + 1]);
+        } else {  // (mma adds with rounding towards zero: a tile's sum is formed apart)
+          float t[2][4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            t[h][0] = t[h][1] = t[h][2] = t[h][3] = 0.f;
+            mma16816(t[h], pl[0], 0u, pl[1], 0u, vf[2 * h], vf[2 * h + 1]);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            mma16816(t[h], pa[0], pa[1], pa[2], pa[3], vf[2 * h], vf[2 * h + 1]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[2 * d2 + h][e] += t[h][e];
         }
       }
       __syncwarp();
@@ -711,10 +722,13 @@ __global__ void __launch_bounds__(kThreads, 2)
           split3(v[0][j], v[1][j], b[j][0], b[j][1], b[j][2]);
           split3(v[2][j], v[3][j], d[j][0], d[j][1], d[j][2]);
         }
+        float t[4][4];  // (mma adds with rounding towards zero: a tile's sum is formed apart)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) t[j][0] = t[j][1] = t[j][2] = t[j][3] = 0.f;
         auto add = [&](int pe, int ve) {  // four independent outputs per product
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            mma16816(o[4 * blk + j], pt[pe][0], pt[pe][1], pt[pe][2], pt[pe][3], b[j][ve], d[j][ve]);
+            mma16816(t[j], pt[pe][0], pt[pe][1], pt[pe][2], pt[pe][3], b[j][ve], d[j][ve]);
         };
         add(2, 0);
         add(1, 1);
@@ -722,6 +736,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         add(1, 0);
         add(0, 1);
         add(0, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[4 * blk + j][e] += t[j][e];
       }
       __syncwarp();
       if (lane == 0) mbar_arrive_cta(&empty[stage]);
@@ -973,14 +991,16 @@ int slot_rows(int n_tokens) {
   return std::max(16, (int)std::min<long long>(kMaxRows, (8LL * n_tokens + 15) / 16 * 16));
 }
 struct Workspace {
-  size_t counters = 0, splits[2], ml[2], o[2], whole_ml, whole_o, total;
+  size_t counters = 0, splits[2], flush, ml[2], o[2], whole_ml, whole_o, total;
   Workspace(int n_tokens, int nq, int hd, bool prefix) {
     // an item of more than 32 rows belongs to one CTA per SM, smaller ones to two
     const int most = slot_rows(n_tokens);
     const size_t rows = (size_t)2 * std::max(kMaxSms * most, 2 * kMaxSms * std::min(32, most));
     splits[0] = align256(2 * kMaxSms * 4);
     splits[1] = splits[0] + align256(2 * kMaxSms * sizeof(PagedSplit));
-    size_t at = splits[1] + align256(2 * kMaxSms * sizeof(PagedSplit));
+    flush = splits[1] + align256(2 * kMaxSms * sizeof(PagedSplit));
+    // (tensor-core tiles have more than 16 rows: three tokens at least)
+    size_t at = flush + (n_tokens > 2 ? (size_t)kMaxSms * 128 * 128 * 4 : 0);
     for (int i = 0; i < (prefix ? 2 : 1); ++i) {
       ml[i] = at;
       o[i] = at + align256(rows * 8);
@@ -1047,6 +1067,7 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& base, int hd, int max_ne
   const Workspace w(a.n_tokens, a.nq, hd, prefix);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.counters = reinterpret_cast<int*>(ws);
+  a.flush = reinterpret_cast<float*>(ws + w.flush);
   auto run = [&](const PagedPlan& p, int i) {
     a.item_units = p.item_units;
     a.tpt = p.rows > 128 ? 2 * (128 / a.gq) : p.rows / a.gq;

@@ -14,7 +14,11 @@
 // products take 2 x 128^3 MACs = 1024 cycles at the dense bf16 rate and the 128 x 128 exponentials
 // and packing about as long, so two streams keep the tensor core busy.
 // f32 activations (NT = 3): q and P as three bf16 terms each (24 bits, f32 results), six products
-// per tile, one stream with two S buffers; the tensor core is the bound by itself.
+// per tile, one stream with two S buffers; the tensor core is the bound by itself. Its accumulators
+// round every addition towards zero, about 1.2e-8 of the value per product: 1.8e-5 over 64 tiles when
+// they ran into one O. So the small terms go first into S, and every kFlush tiles O moves into a record
+// in L2 that is added to in f32 (round to nearest): below 1e-6 at any length, at 414 TFLOP/s of the formula's
+// products (32K keys, 4096 rows); every 4 tiles it would be 1.8e-6 at 494.
 //
 // Warps: 0 page look-up and TMA, 1 MMA issue, 2-5 (and 6-9) softmax; TMEM is S/P and O:
 //   NT = 1: S_A, S_B (128 columns each), O_A, O_B
@@ -36,6 +40,8 @@ namespace qw {
 namespace {
 
 constexpr int KT = kPagedTcKeys;
+constexpr uint32_t kTmemX = 384;  // TMEM column of X_0 (NT = 3)
+constexpr int kFlush = 2;  // tiles of one O (NT = 3)
 
 // mbar_wait inlined: a call in the softmax loop would have to save the row of scores around it.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, int phase, uint64_t limit_ns) {
@@ -80,7 +86,7 @@ struct TcLayout {
   static constexpr int kBars = 2 * kSlots + 10;
   static constexpr uint32_t off_tmem = off_bar + kBars * 8;
   static constexpr uint32_t bytes = off_tmem + 16;
-  static constexpr uint32_t t_o = 256, t_x = 384;          // TMEM columns (t_x: NT = 3)
+  static constexpr uint32_t t_o = 256;                     // TMEM column of O
   static_assert(sizeof(PagedStart) <= 96, "start words");
   static_assert(bytes <= 227 * 1024, "tiles fit one CTA's shared memory");
 };
@@ -90,6 +96,29 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t&
   const float ra = a - __uint_as_float(hi << 16), rb = b - __uint_as_float(hi & 0xffff0000u);
   mid = paged_pack(ra, rb);
   lo = paged_pack(ra - __uint_as_float(mid << 16), rb - __uint_as_float(mid & 0xffff0000u));
+}
+
+// O of this thread's row into its column of the CTA's record [HD][128 rows], whose earlier
+// contents are scaled by f (nothing before the first time).
+template <int HD>
+__device__ __forceinline__ void add_record_hd(float* rec, uint32_t to, bool first, float f) {
+#pragma unroll 1
+  for (int d = 0; d < HD; d += 64) {
+    uint32_t o[4][16];
+    float old[64];
+#pragma unroll
+    for (int e = 0; e < 64; ++e) old[e] = first ? 0.f : __ldcg(rec + (d + e) * 128);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tmem_ld16(to + d + 16 * i, o[i]);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      tmem_regs_ready(o[i]);
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        __stcg(rec + (d + 16 * i + e) * 128, fmaf(old[16 * i + e], f, __uint_as_float(o[i][e])));
+    }
+  }
 }
 
 template <int HD, int NT>
@@ -204,14 +233,21 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
     const uint64_t dk = sw128_kmajor_desc(smem_addr(sm + LY::off_ring));
     const uint64_t dv = sw128_mnmajor_desc(smem_addr(sm + LY::off_ring), KT * 128);
     auto slot_at = [&](int use) { return (uint64_t)((uint32_t)(use % NS) * (LY::kTile >> 4)); };
-    auto issue_s = [&](uint64_t q, uint64_t k, uint32_t d) {  // d = q . k^T (all terms of q)
+    auto issue_s = [&](uint64_t q, uint64_t k, uint32_t d) {  // d = q . k^T, the smallest term of q first
       if (lead) {
 #pragma unroll
         for (int i = 0; i < HD / 16; ++i) {
           const int at = (i >> 2) * (128 * 128) + (i & 3) * 32;  // k-step i of q and of k alike
+          tc_mma_bf16(d, q + (((NT - 1) * LY::kQ1 + at) >> 4), k + (at >> 4), id_s, i != 0);
+        }
+        if constexpr (NT == 3) {
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
-            tc_mma_bf16(d, q + ((t * LY::kQ1 + at) >> 4), k + (at >> 4), id_s, (i | t) != 0);
+          for (int t = 1; t >= 0; --t)
+#pragma unroll
+            for (int i = 0; i < HD / 16; ++i) {
+              const int at = (i >> 2) * (128 * 128) + (i & 3) * 32;
+              tc_mma_bf16(d, q + ((t * LY::kQ1 + at) >> 4), k + (at >> 4), id_s, 1);
+            }
         }
       }
       __syncwarp();
@@ -294,14 +330,15 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
           if (!ok) break;
           tc_fence_after();
           const uint64_t v = dv + slot_at(2 * g + 1);
-          const uint32_t p = tm + 128 * (g & 1), px = tm + LY::t_x + 64 * (g & 1);
+          const uint32_t p = tm + 128 * (g & 1), px = tm + kTmemX + 64 * (g & 1);
+          const bool fresh = x % kFlush == 0;  // (O has been taken away before p_full)
           if (lead) {
 #pragma unroll
-            for (int i = 0; i < KT / 16; ++i) {
-              tc_mma_bf16_ta(tm + LY::t_o, p + 8 * i, v + (i * 2048 >> 4), id_o, (x | i) != 0);
-              tc_mma_bf16_ta(tm + LY::t_o, p + 64 + 8 * i, v + (i * 2048 >> 4), id_o, 1);
-              tc_mma_bf16_ta(tm + LY::t_o, px + 8 * i, v + (i * 2048 >> 4), id_o, 1);
-            }
+            for (int t = 2; t >= 0; --t)
+#pragma unroll
+              for (int i = 0; i < KT / 16; ++i)
+                tc_mma_bf16_ta(tm + LY::t_o, (t == 2 ? px : p + 64 * t) + 8 * i, v + (i * 2048 >> 4), id_o,
+                               !fresh || t != 2 || i != 0);
           }
           __syncwarp();
           commit(&o_full[0]);
@@ -320,6 +357,8 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
     const int s = (warp - 2) >> 2, r = (warp & 3) * 32 + lane;  // a warp reaches 32 lanes of TMEM
     const uint32_t lrow = (uint32_t)((warp & 3) * 32) << 16;
     // row / gq for rows below 256 and gq <= 8
+    float* const rec = a.flush + (size_t)blockIdx.x * (128 * 128) + r;  // NT = 3: [HD][128 rows]
+    auto add_record = [](float* p, uint32_t to, bool first, float f) { add_record_hd<HD>(p, to, first, f); };
     const uint32_t gmul = 65536u / a.gq + 1;
     auto token_of = [&](int row) { return (int)((uint32_t)row * gmul >> 16); };
     PagedCursor c = paged_cursor<KT>(a, st);
@@ -398,7 +437,7 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_cta(q_full);
       }
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY, l = 0.f, rec_m = -INFINITY;
       const uint32_t to = tb + LY::t_o + 128 * s + lrow;
       for (int x = 0; x < (rows > 0 ? n : 0); ++x, ++mine) {
         const int g = tiles + x, buf = NT == 1 ? s : g & 1;
@@ -443,7 +482,9 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
         const float mn = mx > m + 8.f ? mx : m;  // a row without a key yet keeps -inf
         const float mu = mn == -INFINITY ? 0.f : mn;
         const float alpha = paged_exp2(m - mu);
-        if (x > 0 && __any_sync(0xffffffffu, mn != m)) {  // O moves to the new reference
+        const bool take = NT == 3 && x > 0 && x % kFlush == 0;  // O goes into the record below
+        const float m_old = m;
+        if (x > 0 && !take && __any_sync(0xffffffffu, mn != m)) {  // O moves to the new reference
           if (NT == 3) {  // (NT = 1: P V of the last tile was done before s_full of this one)
             wait(&o_full[0], g - 1);
             tc_fence_after();
@@ -490,13 +531,20 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
             for (int e = 0; e < 16; ++e) split3(p[e].x, p[e].y, ph[e], pm[e], pl[e]);
             tmem_st16(ts + 16 * i, ph);
             tmem_st16(ts + 64 + 16 * i, pm);
-            tmem_st16(tb + LY::t_x + 64 * buf + lrow + 16 * i, pl);
+            tmem_st16(tb + kTmemX + 64 * buf + lrow + 16 * i, pl);
           }
         }
         l = l * alpha + ((ps[0].x + ps[0].y) + (ps[1].x + ps[1].y));
         // every phase of o_full is waited for before the next can end: a parity skipped could be
         // taken for the one before it
-        if (NT == 3 && x > 0) wait(&o_full[0], g - 1);
+        if (NT == 3 && x > 0) {
+          wait(&o_full[0], g - 1);
+          if (take) {
+            tc_fence_after();
+            add_record(rec, to, x == kFlush, paged_exp2(rec_m - (m_old == -INFINITY ? 0.f : m_old)));
+            rec_m = m_old;
+          }
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -537,6 +585,7 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
         } else if (live) {
           __stcg((whole ? a.pre.ml : a.slots.ml) + row, make_float2(m, l));
         }
+        const float rec_f = paged_exp2(rec_m - (m == -INFINITY ? 0.f : m));
         float* const to_f = !whole ? a.slots.o : a.prefix_pass ? a.pre.o : static_cast<float*>(a.out);
         const int lr = lane >> 3, lc = lane & 7;  // rows of 8 lanes
 #pragma unroll 1
@@ -547,6 +596,13 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
           tmem_ld_wait();
           tmem_regs_ready(o[0]);
           tmem_regs_ready(o[1]);
+          if (NT == 3 && n > kFlush) {  // and the record of the tiles before
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              uint32_t& x = o[e >> 4][e & 15];
+              x = __float_as_uint(fmaf(__ldcg(rec + (d + e) * 128), rec_f, __uint_as_float(x)));
+            }
+          }
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             *reinterpret_cast<uint4*>(stage + lane * 32 + ((e ^ (lane & 7)) << 2)) =

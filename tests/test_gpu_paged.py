@@ -156,6 +156,28 @@ def test_chunk_of_one_long_sequence():
         c.check()
 
 
+@pytest.mark.parametrize("kv,prefix,tokens", [("bf16", 8192, 512), ("bf16", 3000, 40), ("f32", 8192, 64)])
+def test_f32_results_at_long_prefixes(kv, prefix, tokens):
+    """The tensor cores add with rounding towards zero, up to 2^-23 of the sum per product: 48 of
+    them at most run into one accumulator (5.7e-6), whatever the length."""
+    nq, nkv, hd, page = 64, 8, 128, 64
+    from sequence_decode_step_gb300 import PagedKV
+    g = torch.Generator(device="cuda").manual_seed(5)
+    n = -(-prefix // page)
+    k = torch.randn(n + 1, nkv, page, hd, generator=g, device="cuda").to(DT[kv])
+    v = torch.randn(n + 1, nkv, page, hd, generator=g, device="cuda").to(DT[kv])
+    q = torch.randn(tokens, nq, hd, generator=g, device="cuda") * 1.5
+    i32 = {"device": "cuda", "dtype": torch.int32}
+    c = PagedKV(k, v, torch.full((tokens, 1), n, **i32), torch.zeros(tokens, **i32),
+                torch.arange(tokens + 1, **i32), prefix_pages=torch.arange(n, **i32), prefix_len=prefix)
+    got = c.attend(q)[-2:].double()
+    kk, vv = (t[:n].permute(1, 0, 2, 3).reshape(nkv, -1, hd)[:, :prefix].double() for t in (k, v))
+    s = torch.einsum("thgd,hkd->thgk", q[-2:].double().view(2, nkv, -1, hd), kk) / math.sqrt(hd)
+    want = torch.einsum("thgk,hkd->thgd", torch.softmax(s, -1), vv).reshape(2, nq, hd)
+    assert float((got - want).norm() / want.norm()) <= 6e-6
+    c.check()
+
+
 def test_padding_rows_are_left_and_strides():
     for act, kv in TYPES:
         b = Batch([(2, 9), (1, 40)], 4, 2, 64, 16, act, kv, pad=3, seed=13)
