@@ -66,12 +66,15 @@ struct PagedSlots {
   float2* ml;
   int rows;
 };
-// The prefix's record of every (token, query head): written by the prefix launch for items that one
-// CTA did whole and by the kernel that joins the records of split ones, read by the launch over the
-// sequences' own keys.
+// The prefix's record of every (token, query head): in (o, ml) for items that one CTA of the prefix
+// launch did whole. Split items: behind tensor-core tiles over the sequences' own keys a kernel joins
+// them into (o, ml) first; the decode kernels find the CTAs that share an item from the launch's shape
+// and join their slots themselves, so that they can start under the prefix launch.
 struct PagedPrefix {
   float* o;      // [n_tokens][nq][hd], nullptr without a prefix
   float2* ml;    // [n_tokens][nq]
+  PagedSlots slots;
+  int tpt, kt, grid, item_units;  // of the prefix launch
 };
 struct PagedSplit {    // a split item of a CTA, for the kernel that joins its records
   int c1;              // last CTA, -1: this CTA begins no split item

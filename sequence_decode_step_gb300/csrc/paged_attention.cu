@@ -170,23 +170,42 @@ __device__ __forceinline__ void finish_segment(const PagedAttnArgs& a, const Pag
           if (d == 0) __stcg(a.slots.ml + slot + r, make_float2(acc.m, acc.l));
           continue;
         }
-      } else {
+      }
+      const int t = paged_token(r, gmul), token = c.s.lo + tok0 + t, hg = r - t * a.gq;
+      // records to join: this item's, if it was split, then the prefix's
+#pragma unroll 1
+      for (int src = pass == 1 ? 0 : 1; src < 2; ++src) {
+        const float* so = a.slots.o;
+        const float2* sml = a.slots.ml;
+        size_t row = r, rows_of = R;  // record of CTA z: row (2 z + (z == first)) rows_of + row
+        int z0 = c0, z1 = c1;
+        if (src == 1) {
+          if (!a.pre.o || a.prefix_pass) break;
+          const PagedShare p = paged_prefix_share(a, token, c.kvh, hg);
+          z0 = p.c0, z1 = p.c1;
+          row = p.row, rows_of = a.pre.slots.rows;
+          so = a.pre.slots.o, sml = a.pre.slots.ml;
+          if (z0 == z1) {  // done whole by one CTA
+            row = (size_t)token * a.nq + c.kvh * a.gq + hg, rows_of = 0;
+            so = a.pre.o, sml = a.pre.ml;
+          }
+        }
         constexpr int NB = 8;  // records per round of loads
 #pragma unroll 1
-        for (int x = c0; x <= c1; x += NB) {
+        for (int x = z0; x <= z1; x += NB) {
           float2 ml[NB];
           float4 o[NB];
           float top = acc.m;
 #pragma unroll
           for (int y = 0; y < NB; ++y) {
-            const int z = min(x + y, c1);
-            const size_t row = (size_t)(2 * z + (z == c0)) * R + r;
-            ml[y] = __ldcg(a.slots.ml + row);
-            o[y] = __ldcg(reinterpret_cast<const float4*>(a.slots.o + row * HD + d));
+            const int z = min(x + y, z1);
+            const size_t at = (size_t)(2 * z + (z == z0)) * rows_of + row;
+            ml[y] = __ldcg(sml + at);
+            o[y] = __ldcg(reinterpret_cast<const float4*>(so + at * HD + d));
           }
 #pragma unroll
           for (int y = 0; y < NB; ++y) {
-            if (x + y > c1) ml[y].x = -INFINITY;
+            if (x + y > z1) ml[y].x = -INFINITY;
             top = fmaxf(top, ml[y].x);
           }
           const float mu = top == -INFINITY ? 0.f : top;
@@ -197,8 +216,7 @@ __device__ __forceinline__ void finish_segment(const PagedAttnArgs& a, const Pag
           for (int y = 0; y < NB; ++y) acc.add(paged_exp2(ml[y].x - mu), ml[y].y, o[y]);
         }
       }
-      const int t = paged_token(r, gmul);
-      paged_emit(a, HD, c.s.lo + tok0 + t, c.kvh * a.gq + r - t * a.gq, d, acc);
+      paged_emit<false>(a, HD, token, c.kvh * a.gq + hg, d, acc);
     }
     if (whole || pass == 1) break;
     if (a.prefix_pass) {  // joined by the next launch
@@ -1093,9 +1111,14 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& base, int hd, int max_ne
     const PagedPlan p = plan_paged_pass(a, (long long)a.n_tokens * a.gq, a.c.prefix_len, sms);
     if (too_long(p, a.c.prefix_len, 1)) return cudaErrorInvalidValue;
     cudaError_t e = run(p, 1);
-    if (e == cudaSuccess) e = launch_paged_join(a, hd, p.grid, p.rows, s);
+    if (e == cudaSuccess && own.tc) e = launch_paged_join(a, hd, p.grid, p.rows, s);
     if (e != cudaSuccess) return e;
     a.prefix_pass = 0;
+    a.pre.slots = a.slots;
+    a.pre.tpt = a.tpt;
+    a.pre.kt = p.kt;
+    a.pre.grid = p.grid;
+    a.pre.item_units = p.item_units;
   }
   return run(own, 0);
 }

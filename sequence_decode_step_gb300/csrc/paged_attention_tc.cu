@@ -661,7 +661,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   if (sp.c1 < 0 || r >= sp.rows) return;
   PagedAcc acc;
   paged_join_slots<HD>(a.slots, blockIdx.x, sp.c1, r, d, acc);
-  paged_emit(a, HD, sp.token + r / a.gq, sp.head + r % a.gq, d, acc);
+  paged_emit<true>(a, HD, sp.token + r / a.gq, sp.head + r % a.gq, d, acc);
 }
 
 template <int HD, int NT>

@@ -297,13 +297,31 @@ __device__ __forceinline__ void paged_join_slots(const PagedSlots& sl, int c0, i
   }
 }
 
+// The CTAs c0 .. c1 of the prefix launch that share the item of (token, KV head), and the query
+// head's row in it.
+struct PagedShare {
+  int c0, c1, row;
+};
+__device__ __forceinline__ PagedShare paged_prefix_share(const PagedAttnArgs& a, int token, int kvh,
+                                                         int head_in_group) {
+  const PagedPrefix& p = a.pre;
+  const int end = min(max(__ldg(a.c.q_start + a.c.n_seqs), 0), a.n_tokens);
+  const int lo = min(max(__ldg(a.c.q_start), 0), end);
+  const int nrt = (end - lo + p.tpt - 1) / p.tpt, nkt = (a.c.prefix_len + p.kt - 1) / p.kt;
+  const int rt = (token - lo) / p.tpt, units = p.item_units + nkt;
+  const int per = max((a.c.nkv * nrt * units + p.grid - 1) / p.grid, kPagedLeastUnits);
+  const int first = (kvh * nrt + rt) * units + p.item_units;
+  return PagedShare{first / per, (first + nkt - 1) / per, (token - lo - rt * p.tpt) * a.gq + head_in_group};
+}
+
 // row / gq for rows below 256 and gq <= 8, with gmul = 65536 / gq + 1.
 __device__ __forceinline__ int paged_token(int row, uint32_t gmul) {
   return (int)((uint32_t)row * gmul >> 16);
 }
 
 // Writes one float4 (columns d..d+3) of query row (token, head): the prefix's record in its
-// launches, else the output after that record is joined; a row without a key is 0.
+// launches, else the output (JOIN: after the prefix's record is joined); a row without a key is 0.
+template <bool JOIN>
 __device__ __forceinline__ void paged_emit(const PagedAttnArgs& a, int hd, int token, int head, int d,
                                            PagedAcc acc) {
   const size_t row = (size_t)token * a.nq + head, at = row * hd + d;
@@ -312,7 +330,7 @@ __device__ __forceinline__ void paged_emit(const PagedAttnArgs& a, int hd, int t
     to = a.pre.o;
     if (d == 0) a.pre.ml[row] = make_float2(acc.m, acc.l);
   } else {
-    if (a.pre.o) {
+    if (JOIN && a.pre.o) {
       const float2 ml = __ldcg(a.pre.ml + row);
       acc.join(ml.x, ml.y, __ldcg(reinterpret_cast<const float4*>(a.pre.o + at)));
     }

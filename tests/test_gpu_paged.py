@@ -168,10 +168,12 @@ def test_f32_results_at_long_prefixes(kv, prefix, tokens):
     v = torch.randn(n + 1, nkv, page, hd, generator=g, device="cuda").to(DT[kv])
     q = torch.randn(tokens, nq, hd, generator=g, device="cuda") * 1.5
     i32 = {"device": "cuda", "dtype": torch.int32}
-    c = PagedKV(k, v, torch.full((tokens, 1), n, **i32), torch.zeros(tokens, **i32),
+    c = PagedKV(k, v, torch.full((tokens, 1), n, **i32), torch.ones(tokens, **i32),
                 torch.arange(tokens + 1, **i32), prefix_pages=torch.arange(n, **i32), prefix_len=prefix)
     got = c.attend(q)[-2:].double()
-    kk, vv = (t[:n].permute(1, 0, 2, 3).reshape(nkv, -1, hd)[:, :prefix].double() for t in (k, v))
+    # the prefix, then the one key of their own: the first of the last page, for all of them
+    kk, vv = (torch.cat([t[:n].permute(1, 0, 2, 3).reshape(nkv, -1, hd)[:, :prefix], t[n, :, :1]], 1).double()
+              for t in (k, v))
     s = torch.einsum("thgd,hkd->thgk", q[-2:].double().view(2, nkv, -1, hd), kk) / math.sqrt(hd)
     want = torch.einsum("thgk,hkd->thgd", torch.softmax(s, -1), vv).reshape(2, nq, hd)
     assert float((got - want).norm() / want.norm()) <= 6e-6
