@@ -105,27 +105,24 @@ class PagedKV:
         self._current = torch.cuda.current_device
         self._int32 = torch.int32
 
-    def _rows(self, t, what: str, width: int, rows: int):
+    def _rows(self, t, what: str, width: int, rows: int) -> int:
         """Row stride of an activation matrix [rows, width] or [rows, heads, head_dim] whose rows
         are adjacent elements."""
         shape, inner = t.shape, t.stride()
         if len(shape) == 3:  # heads back to back
-            ok = shape[1] * shape[2] == width and inner[2] == 1 and (inner[1] == shape[2] or shape[1] == 1)
+            ok = inner[2] == 1 and shape[1] * shape[2] == width and (inner[1] == shape[2] or shape[1] == 1)
         else:
-            ok = len(shape) == 2 and shape[1] == width and inner[1] == 1
-        if not ok or shape[0] != rows:
-            raise ValueError(f"{what}: {rows} rows of {width} adjacent elements wanted, got {tuple(shape)} "
-                             f"with strides {inner}")
-        if t.device != self.device:
-            raise ValueError(f"{what} is not on the cache's device")
+            ok = len(shape) == 2 and inner[1] == 1 and shape[1] == width
+        if not ok or shape[0] != rows or t.get_device() != self._index:
+            raise ValueError(f"{what}: {rows} rows of {width} adjacent elements on {self.device} wanted, got "
+                             f"{tuple(shape)} with strides {inner} on {t.device}")
         return inner[0] if rows > 1 else width
 
-    def _out(self, out, like, n_q_heads: int):
+    def _out(self, out, like, n_q_heads: int, rows: int):
         if out is None:
-            return _torch().zeros(like.shape[0], n_q_heads, self.head_dim, dtype=like.dtype,
-                                  device=self.device)
+            return _torch().zeros(rows, n_q_heads, self.head_dim, dtype=like.dtype, device=self.device)
         width = n_q_heads * self.head_dim
-        if out.dtype != like.dtype or self._rows(out, "out", width, like.shape[0]) != width:
+        if out.dtype is not like.dtype or self._rows(out, "out", width, rows) != width:
             raise ValueError("out: contiguous rows of the input's type wanted")
         return out
 
@@ -145,15 +142,15 @@ class PagedKV:
         n = qkv.shape[0]
         fmt = _format(qkv, "qkv")
         ld = self._rows(qkv, "qkv", (n_q_heads + 2 * self.n_kv_heads) * self.head_dim, n)
-        out = self._out(out, qkv, n_q_heads)
+        out = self._out(out, qkv, n_q_heads, n)
         for t in (q_norm, k_norm):
-            if t is not None and (t.element_size() != 2 or t.shape != (self.head_dim,) or
-                                  t.stride(0) != 1 or t.device != self.device):
+            if t is not None and (t.element_size() != 2 or t.dim() != 1 or t.numel() != self.head_dim or
+                                  t.stride(0) != 1 or t.get_device() != self._index):
                 raise ValueError("q_norm and k_norm: bfloat16 [head_dim] on the cache's device")
         if positions is not None:
             want = (n, 3) if sections is not None else (n,)
-            if positions.dtype != self._int32 or positions.shape != want or \
-                    not positions.is_contiguous() or positions.device != self.device:
+            if positions.dtype is not self._int32 or positions.shape != want or \
+                    not positions.is_contiguous() or positions.get_device() != self._index:
                 raise ValueError(f"positions: contiguous int32 {want} wanted")
         sec = (C.c_int32 * 3)(*sections) if sections is not None else None
         rc = self._lib.qw_paged_append(
@@ -176,7 +173,7 @@ class PagedKV:
         heads = width // self.head_dim
         fmt = _format(q, "q")
         ld = self._rows(q, "q", heads * self.head_dim, n)
-        out = self._out(out, q, heads)
+        out = self._out(out, q, heads, n)
         need = self._lib.qw_paged_attention_workspace_bytes(n, heads, self.head_dim,
                                                             self.c.prefix_len)
         ws = self.workspace
