@@ -1070,7 +1070,7 @@ PagedPlan plan_paged_pass(const PagedAttnArgs& a, long long rows, long long keys
       const double items = (double)a.c.nkv * ((rows + item_rows - 1) / item_rows);
       return start + tile * std::ceil(items * (keys / kt + 1 + units) / grid);
     };
-    const int tc_rows = paged_tc_rows(a.act_bf16), tc_units = 3;  // 4 us against 1.5 us a tile
+    const int tc_rows = paged_tc_rows(a.act_bf16), tc_units = 5;  // 7 us (with the last tile's drain) against 1.5 us a tile
     if (us(16, a.act_bf16 ? 1.5 : 2.9, kPagedTcKeys, tc_rows, tc_units, sms) <
         us(4, 1.3, p.kt, p.rows, p.item_units, p.grid))
       p = PagedPlan{true, kPagedTcKeys, tc_rows, sms, tc_units};
