@@ -494,7 +494,8 @@ int qw_paged_append(const qw_paged_kv* c, const void* qkv, uint32_t act_format, 
  *              multiple of 16 bytes; 16-byte aligned (q_out of qw_paged_append, ldq = n_q_heads * head_dim)
  *   max_new:   the most new tokens of one sequence, which chooses the kernel; a wrong value
  *              costs speed only
- *   out:       act_format [n_tokens, n_q_heads * head_dim] DEVICE, 16-byte aligned
+ *   out:       act_format [n_tokens, n_q_heads * head_dim] DEVICE, 16-byte aligned; must not
+ *              overlap q
  *   workspace: DEVICE scratch of qw_paged_attention_workspace_bytes(n_tokens, n_q_heads,
  *              head_dim, prefix_len) bytes, 16-byte aligned, zero-filled before its first use and
  *              left ready for the next call; calls that overlap on the GPU need one each */

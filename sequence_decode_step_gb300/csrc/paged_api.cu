@@ -194,7 +194,7 @@ extern "C" int qw_paged_attention(const qw_paged_kv* c, const void* q, uint32_t 
   if (e == cudaErrorInvalidValue)
     return fail(QW_ERR_ARG,
                 "qw_paged_attention: tokens x keys beyond what one call counts (n_kv_heads x row tiles x "
-                "key tiles of the longest possible sequences must stay below 2^31), or an unaligned pool");
+                "key tiles of the longest possible sequences must stay below 2^30), or an unaligned pool");
   if (e != cudaSuccess) return fail(QW_ERR_CUDA, cudaGetErrorString(e));
   return QW_OK;
 }

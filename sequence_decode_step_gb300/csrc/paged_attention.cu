@@ -1098,7 +1098,7 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& base, int hd, int max_ne
   // the line of a launch is counted in 32 bits
   auto too_long = [&](const PagedPlan& p, long long tiles, long long seqs) {
     const long long items = a.n_tokens / (p.rows / a.gq) + seqs;
-    return tiles / p.kt + 4 > INT32_MAX / a.c.nkv / items;
+    return tiles / p.kt + 8 > INT32_MAX / 2 / a.c.nkv / items;
   };
   const long long cap = (long long)a.c.max_pages << a.c.page_shift;
   // (the lengths are on the device: the longest that the table can hold stands for them)

@@ -46,9 +46,12 @@ class Workspace:
         if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("the attention workspace is too small and cannot be made inside a graph "
                                "capture: call reserve(n_tokens, n_q_heads) before it")
-        # smaller ones are kept: a captured graph may hold their address
-        self._kept.append(torch.zeros(need, dtype=torch.uint8, device=self.device))
-        self.bytes, self.ptr = need, self._kept[-1].data_ptr()
+        # smaller ones are kept, as a captured graph may hold their address; each is at least twice
+        # the one before, so that they stay below the largest together
+        size = max(need, 2 * self.bytes)
+        self._kept.append(torch.zeros(size, dtype=torch.uint8, device=self.device))
+        torch.cuda.current_stream(self.device).synchronize()  # zero for calls on any stream
+        self.bytes, self.ptr = size, self._kept[-1].data_ptr()
 
 
 class PagedKV:
@@ -85,6 +88,7 @@ class PagedKV:
                                                   prefix_pages.numel() * page < prefix_len)):
             raise ValueError("prefix_pages do not hold prefix_len keys")
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        torch.cuda.current_stream(self.device).synchronize()  # zero for calls on any stream
         self._keep = (k_pages, v_pages, page_table, kv_len, q_start, prefix_pages)
         self.workspace = workspace if workspace is not None else Workspace(self.device)
         if self.workspace.device != self.device:
@@ -103,7 +107,7 @@ class PagedKV:
         self._cref = C.byref(self.c)
         self._index = self.device.index
         self._current = torch.cuda.current_device
-        self._int32 = torch.int32
+        self._int32, self._gains = torch.int32, (torch.bfloat16, torch.int16)
 
     def _rows(self, t, what: str, width: int, rows: int) -> int:
         """Row stride of an activation matrix [rows, width] or [rows, heads, head_dim] whose rows
@@ -144,9 +148,10 @@ class PagedKV:
         ld = self._rows(qkv, "qkv", (n_q_heads + 2 * self.n_kv_heads) * self.head_dim, n)
         out = self._out(out, qkv, n_q_heads, n)
         for t in (q_norm, k_norm):
-            if t is not None and (t.element_size() != 2 or t.dim() != 1 or t.numel() != self.head_dim or
+            if t is not None and (t.dtype not in self._gains or t.dim() != 1 or t.numel() != self.head_dim or
                                   t.stride(0) != 1 or t.get_device() != self._index):
-                raise ValueError("q_norm and k_norm: bfloat16 [head_dim] on the cache's device")
+                raise ValueError("q_norm and k_norm: bfloat16 (or its int16 bits) [head_dim] on the cache's "
+                                 "device")
         if positions is not None:
             want = (n, 3) if sections is not None else (n,)
             if positions.dtype is not self._int32 or positions.shape != want or \

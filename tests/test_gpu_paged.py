@@ -97,6 +97,31 @@ def test_rows_without_a_key_are_zero():
 
 
 @pytest.mark.parametrize("act,kv", TYPES)
+def test_chunks_whose_first_tokens_see_nothing(act, kv):
+    # kv_len below the new tokens: reported, the tokens before the first key get zeros (or the
+    # prefix alone), the others what they see; with many rows per key and with few
+    for prefix, new, length in [(0, 150, 40), (0, 9, 2), (33, 150, 0)]:
+        b = Batch([(new, 0), (1, 70)], 8, 2, 64, 16, act, kv, prefix=prefix, seed=89)
+        b.len[0] = length
+        c = b.cache()
+        got = c.attend(b.q.cuda(), max_new=new).double().cpu()
+        assert torch.isfinite(got).all()
+        if prefix == 0:
+            assert (got[:new - length] == 0).all()
+        k, v = b.keys(b.k, 0), b.keys(b.v, 0)
+        for i in (0, new // 2, new - 1):
+            n = prefix + max(0, length - new + i + 1)
+            for h in (0, 5):
+                p = torch.softmax(k[h // 4, :n] @ b.q[i, h].double() / 8.0, 0)
+                want = p @ v[h // 4, :n]
+                # up to 73 keys: f32 sums (1e-5 of values below 5), or bf16 weights and output
+                tol = 1e-4 if act == "f32" else 2 * HALF["bf16"] * float(v.abs().max())
+                assert n == 0 or (got[i, h] - want).abs().max() <= tol
+        with pytest.raises(RuntimeError, match="BAD_LENGTH"):
+            c.check()
+
+
+@pytest.mark.parametrize("act,kv", TYPES)
 def test_large_scores_and_ties(act, kv):
     # one key far above the rest, equal keys, and large values: the softmax's reference moves
     b = Batch([(1, 300), (1, 90)], 4, 2, 64, 16, act, kv, seed=9)
@@ -372,6 +397,9 @@ def test_layers_share_a_workspace():
         attend_close(a, x)
         attend_close(b, y)
     assert ca.workspace is cb.workspace and len(ca.workspace._kept) == 1
+    for n in range(3, 400):                       # growing batches do not pile up workspaces
+        ca.reserve(n, 4)
+    assert len(ca.workspace._kept) <= 4
 
 
 def test_other_streams():
@@ -431,6 +459,9 @@ def test_tensors_that_do_not_fit_are_refused():
         c.append(b.qkv.cuda()[:, ::2], 4)
     with pytest.raises(ValueError):
         c.append(b.qkv.cuda(), 4, positions=torch.zeros(1, dtype=torch.int64, device="cuda"))
+    with pytest.raises(ValueError):
+        g = torch.ones(64, dtype=torch.float16, device="cuda")
+        c.append(b.qkv.cuda(), 4, q_norm=g, k_norm=g)
     with pytest.raises(ValueError):
         PagedKV(b.kd, b.vd, b.table_d.long(), b.len_d, b.start_d)
     with pytest.raises(ValueError):
