@@ -649,11 +649,12 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
   pdl_wait();
 }
 
-// Joins the records of the items that a launch split: CTA (x, y) takes the 4 rows from 4 y on (8
+// Joins the records of the items that a launch split: CTA (x, y) takes the 8 rows from 8 y on (16
 // with head_dim 64) of the item that begins in CTA x, a row by hd/4 lanes.
+constexpr int kJoinThreads = 256;
 template <int HD>
-__global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedAttnArgs a) {
-  constexpr int V4 = HD / 4, RB = 128 / V4;
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedAttnArgs a) {
+  constexpr int V4 = HD / 4, RB = kJoinThreads / V4;
   pdl_launch_dependents();
   pdl_wait();
   const PagedSplit sp = a.splits[blockIdx.x];
@@ -698,10 +699,10 @@ cudaError_t launch_paged_tc(const PagedAttnArgs& a, int hd, int grid, cudaStream
 }
 
 cudaError_t launch_paged_join(const PagedAttnArgs& a, int hd, int grid, int item_rows, cudaStream_t s) {
-  const int rb = 512 / hd;  // rows of a CTA
+  const int rb = kJoinThreads * 4 / hd;  // rows of a CTA
   const dim3 g(grid, (std::min(item_rows, a.slots.rows) + rb - 1) / rb);
-  return hd == 64 ? launch_pdl(paged_join_kernel<64>, g, 128, 0, s, a)
-                  : launch_pdl(paged_join_kernel<128>, g, 128, 0, s, a);
+  return hd == 64 ? launch_pdl(paged_join_kernel<64>, g, kJoinThreads, 0, s, a)
+                  : launch_pdl(paged_join_kernel<128>, g, kJoinThreads, 0, s, a);
 }
 
 cudaError_t set_paged_tc_attributes() {
