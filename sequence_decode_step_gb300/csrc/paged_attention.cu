@@ -133,10 +133,10 @@ __device__ __forceinline__ void produce(const PagedAttnArgs& a, const CUtensorMa
 }
 
 // Place of column d of row r in a join record: 8-column groups exchanged by the row, so that the
-// eight rows of an mma fragment do not meet in the same banks.
+// rows of an mma fragment do not meet in the same banks.
 template <int HD>
 __device__ __forceinline__ int join_at(int r, int d) {
-  return r * HD + (d ^ ((r & 3) << 3));
+  return r * HD + (d ^ ((r >> 1 & 3) << 3));
 }
 
 // ------------------------------------------------------------------ end of an item's segment
@@ -307,14 +307,25 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t&
   lo = paged_pack(ra - __uint_as_float(mid << 16), rb - __uint_as_float(mid & 0xffff0000u));
 }
 
-// NT = 1: R = 16 rows, bf16 q and P. NT = 3: R = 8 rows, q and P in three bf16 terms.
+// 8x8 matrix of 16-bit elements across the warp, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// R = 8 query rows as the n side of the products, keys (16 per warp and tile) and head columns as
+// the m side:  S^T = K q^T,  O^T += V^T P^T.  NT = 1: bf16 q and P; NT = 3: three bf16 terms of each, added
+// into the same accumulators. P^T comes from S^T's fragment by one 8x8 transpose per 8 keys.
+template <int HD>
+using MmaLayout = PgLayout<HD, 64, 2, 8, 64 * 1024>;
 template <int HD, int NT>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 3)
     paged_attn_mma_kernel(const __grid_constant__ PagedAttnArgs a,
                           const __grid_constant__ CUtensorMap tk,
                           const __grid_constant__ CUtensorMap tv) {
-  constexpr int KT = 64, R = NT == 1 ? 16 : 8, NRW = R / 8, KS = HD / 16, DT = HD / 8;
-  using LY = PgLayout<HD, KT, 2, R>;
+  constexpr int KT = 64, R = 8, KS = HD / 16, HT = HD / 16;
+  using LY = MmaLayout<HD>;
   constexpr int NS = LY::kStages;
   extern __shared__ __align__(1024) uint8_t sm[];
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + LY::off_bar);
@@ -331,12 +342,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   float2* row_ml = reinterpret_cast<float2*>(sm + LY::off_row);
   int* flag = reinterpret_cast<int*>(sm + LY::off_start + 96 + 40);
 
-  const int g = lane >> 2, q2 = (lane & 3) * 2;
-  // ldmatrix rows of this lane. K (plain): keys 16 warp + (matrix / 2) * 8 + row, chunk matrix % 2.
-  // V (transposed): keys 16 warp + (matrix % 2) * 8 + row, chunk matrix / 2.
+  const int g = lane >> 2, q2 = (lane & 3) * 2;  // this thread's keys g, g + 8 and rows q2, q2 + 1
+  // ldmatrix rows of this lane: matrices of keys 0-7 / 8-15 and 16-byte chunks of the row.
+  // K (plain): keys 8 (matrix % 2), chunk matrix / 2; V (transposed): keys 8 (matrix / 2), chunk matrix % 2
   const int mat = lane >> 3, mr = lane & 7;
-  const int krow = 16 * warp + (mat >> 1) * 8 + mr, kch = mat & 1;
-  const int vrow = 16 * warp + (mat & 1) * 8 + mr, vch = mat >> 1;
+  const int krow = 16 * warp + (mat & 1) * 8 + mr, kch = mat >> 1;
+  const int vrow = 16 * warp + (mat >> 1) * 8 + mr, vch = mat & 1;
   const uint32_t ring = smem_addr(sm);
 
   const uint32_t gmul = 65536u / a.gq + 1;
@@ -346,8 +357,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   do {
     const int n = c.kend - c.kt;
     const int tok0 = c.rt * a.tpt, rows = min(a.tpt, c.s.nb - tok0) * a.gq;
-    // q through shared memory (where the join works at the item's end) as A fragments: rows g and
-    // g + 8 of a 16-row tile; with NT = 3 "row" g + 8 is row g's second term, the third is in ql
+    // q through shared memory (where the join works at the item's end) as B fragments, a plane of
+    // [8 rows][HD] per term
     constexpr uint32_t kPlane = 8 * HD * 2;
     {
       uint8_t* to = reinterpret_cast<uint8_t*>(join);
@@ -379,108 +390,86 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     consumer_sync();
-    uint32_t qa[KS][4], ql[NT == 3 ? KS : 1][2];
+    uint32_t qb[NT][KS][2];
     {
       const uint32_t from = smem_addr(join) + mr * (HD * 2);
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-        ldsm4(from + (mat & 1) * kPlane + (((ks * 2 + (mat >> 1)) ^ mr) << 4), qa[ks]);
-      if constexpr (NT == 3) {
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int ks = 0; ks < KS; ks += 2) {
           uint32_t x[4];
-          ldsm4(from + 2 * kPlane + (((ks * 2 + mat) ^ mr) << 4), x);
-          ql[ks][0] = x[0], ql[ks][1] = x[1], ql[ks + 1][0] = x[2], ql[ks + 1][1] = x[3];
+          ldsm4(from + t * kPlane + (((ks * 2 + mat) ^ mr) << 4), x);
+          qb[t][ks][0] = x[0], qb[t][ks][1] = x[1], qb[t][ks + 1][0] = x[2], qb[t][ks + 1][1] = x[3];
         }
-      }
     }
-    int lim[NRW];
+    int lim[2];
 #pragma unroll
-    for (int i = 0; i < NRW; ++i) {
-      const int r = g + 8 * i, t = tok0 + paged_token(r, gmul);
+    for (int i = 0; i < 2; ++i) {
+      const int r = q2 + i, t = tok0 + paged_token(r, gmul);
       lim[i] = r >= rows ? 0 : a.prefix_pass ? c.limit : min(max(c.s.base + t + 1, 0), c.s.len);
     }
-    float o[DT][4], m[NRW], l[NRW];
+    float o[HT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
-    for (int d = 0; d < DT; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
-#pragma unroll
-    for (int i = 0; i < NRW; ++i) m[i] = -INFINITY, l[i] = 0.f;
+    for (int d = 0; d < HT; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
 
     for (int x = 0; x < n; ++x, ++seen) {
       const int stage = seen % NS;
       if (!bad)
         bad = !__all_sync(0xffffffffu, mbar_wait(&full[stage], (uint32_t)((seen / NS) & 1), a.wait_ns));
       const uint32_t kb = ring + (uint32_t)stage * 2 * LY::kTile, vb = kb + LY::kTile;
-      float s[2][4], s2[2][4];  // even and odd k-steps: two chains of mma
+      float s[4], s2[4];  // even and odd k-steps; with NT = 3 the first terms' and the others' products
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[0][i] = s[1][i] = s2[0][i] = s2[1][i] = 0.f;
+      for (int i = 0; i < 4; ++i) s[i] = s2[i] = 0.f;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         const int ch = ks * 2 + kch;  // 16-byte chunk of the row; 8 of them per column block
         uint32_t kf[4];
         ldsm4(kb + (ch >> 3) * (KT * 128) + krow * 128 + (((ch & 7) ^ (krow & 7)) << 4), kf);
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          float(&d)[4] = ks & 1 ? s2[nt] : s[nt];
-          mma16816(d, qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], kf[2 * nt], kf[2 * nt + 1]);
-        }
-        if constexpr (NT == 3) {
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
-            mma16816(ks & 1 ? s[nt] : s2[nt], ql[ks][0], 0u, ql[ks][1], 0u, kf[2 * nt], kf[2 * nt + 1]);
+        if constexpr (NT == 1) {
+          mma16816(ks & 1 ? s2 : s, kf[0], kf[1], kf[2], kf[3], qb[0][ks][0], qb[0][ks][1]);
+        } else {
+          mma16816(s, kf[0], kf[1], kf[2], kf[3], qb[0][ks][0], qb[0][ks][1]);
+          mma16816(s2, kf[0], kf[1], kf[2], kf[3], qb[2][ks][0], qb[2][ks][1]);
+          mma16816(s2, kf[0], kf[1], kf[2], kf[3], qb[1][ks][0], qb[1][ks][1]);
         }
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[0][i] += s2[0][i], s[1][i] += s2[1][i];
       const int k0 = (c.kt + x) * KT + 16 * warp;  // this warp's first key
       const bool edge = k0 + 16 > c.limit - a.tpt;  // keys some row does not see
-      float p[NRW][4];
+      float p[4], alpha[2];  // p[0], p[1]: key g, rows q2 and q2 + 1; p[2], p[3]: key g + 8
       bool moved = false;
-      float alpha[NRW];
 #pragma unroll
-      for (int i = 0; i < NRW; ++i) {
-        float mx = -INFINITY;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int nt = e >> 1, j = e & 1;
-          float v = NT == 3 ? s[nt][j] + s[nt][2 + j] : s[nt][2 * i + j];
-          v *= a.scale_log2;
-          if ((edge || rows < R) && k0 + nt * 8 + q2 + j >= lim[i]) v = -INFINITY;
-          p[i][e] = v;
-          mx = fmaxf(mx, v);
+      for (int i = 0; i < 2; ++i) {
+        float u = (s[i] + s2[i]) * a.scale_log2, v = (s[2 + i] + s2[2 + i]) * a.scale_log2;
+        if (edge || rows < R) {
+          if (k0 + g >= lim[i]) u = -INFINITY;
+          if (k0 + 8 + g >= lim[i]) v = -INFINITY;
         }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        float mx = fmaxf(u, v);
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
         const float mn = fmaxf(m[i], mx);
         const float mu = mn == -INFINITY ? 0.f : mn;
         alpha[i] = paged_exp2(m[i] - mu);
         moved = moved || mn != m[i];
         m[i] = mn;
-        float sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          p[i][e] = paged_exp2(p[i][e] - mu);
-          sum += p[i][e];
-        }
-        l[i] = l[i] * alpha[i] + sum;  // this thread's keys; the four lanes are added at the end
+        p[i] = paged_exp2(u - mu);
+        p[2 + i] = paged_exp2(v - mu);
+        l[i] = l[i] * alpha[i] + (p[i] + p[2 + i]);  // this thread's keys; the lanes are added at the end
       }
       if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          o[d][0] *= alpha[0], o[d][1] *= alpha[0];
-          o[d][2] *= alpha[NRW - 1], o[d][3] *= alpha[NRW - 1];
-        }
+        for (int d = 0; d < HT; ++d)
+          o[d][0] *= alpha[0], o[d][1] *= alpha[1], o[d][2] *= alpha[0], o[d][3] *= alpha[1];
       }
-      // P as A fragments over this warp's 16 keys
-      uint32_t pa[4], pl[2];
+      uint32_t pb[NT][2];  // P^T as B fragments
       if constexpr (NT == 1) {
-        pa[0] = paged_pack(p[0][0], p[0][1]);
-        pa[2] = paged_pack(p[0][2], p[0][3]);
-        pa[1] = paged_pack(p[NRW - 1][0], p[NRW - 1][1]);
-        pa[3] = paged_pack(p[NRW - 1][2], p[NRW - 1][3]);
+        pb[0][0] = transpose8(paged_pack(p[0], p[1]));
+        pb[0][1] = transpose8(paged_pack(p[2], p[3]));
       } else {
-        split3(p[0][0], p[0][1], pa[0], pa[1], pl[0]);
-        split3(p[0][2], p[0][3], pa[2], pa[3], pl[1]);
+        split3(p[0], p[1], pb[0][0], pb[1][0], pb[2][0]);
+        split3(p[2], p[3], pb[0][1], pb[1][1], pb[2][1]);
+#pragma unroll
+        for (int t = 0; t < 3; ++t) pb[t][0] = transpose8(pb[t][0]), pb[t][1] = transpose8(pb[t][1]);
       }
       // values behind the last key are whatever the page held: cleared, since 0 * NaN is NaN
       const int left = c.limit - k0;  // keys of this warp's 16 that exist
@@ -490,29 +479,20 @@ __global__ void __launch_bounds__(kThreads, 2)
         vm1 = (q2 + 8 < left ? 0xffffu : 0u) | (q2 + 9 < left ? 0xffff0000u : 0u);
       }
 #pragma unroll
-      for (int d2 = 0; d2 < DT / 2; ++d2) {
-        const int ch = d2 * 2 + vch;
-        uint32_t vf[4];
+      for (int d = 0; d < HT; ++d) {
+        const int ch = d * 2 + vch;
+        uint32_t vf[4];  // head columns 16 d + g (+ 8), keys q2, q2 + 1 (+ 8)
         ldsm4t(vb + (ch >> 3) * (KT * 128) + vrow * 128 + (((ch & 7) ^ (vrow & 7)) << 4), vf);
-        if (left < 16) vf[0] &= vm0, vf[1] &= vm1, vf[2] &= vm0, vf[3] &= vm1;
+        if (left < 16) vf[0] &= vm0, vf[1] &= vm0, vf[2] &= vm1, vf[3] &= vm1;
         if constexpr (NT == 1) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            mma16816(o[2 * d2 + h], pa[0], pa[1], pa[2], pa[3], vf[2 * h], vf[2 * h + 1]);
+          mma16816(o[d], vf[0], vf[1], vf[2], vf[3], pb[0][0], pb[0][1]);
         } else {  // (mma adds with rounding towards zero: a tile's sum is formed apart)
-          float t[2][4];
+          float t[4] = {0.f, 0.f, 0.f, 0.f};
+          mma16816(t, vf[0], vf[1], vf[2], vf[3], pb[2][0], pb[2][1]);
+          mma16816(t, vf[0], vf[1], vf[2], vf[3], pb[1][0], pb[1][1]);
+          mma16816(t, vf[0], vf[1], vf[2], vf[3], pb[0][0], pb[0][1]);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            t[h][0] = t[h][1] = t[h][2] = t[h][3] = 0.f;
-            mma16816(t[h], pl[0], 0u, pl[1], 0u, vf[2 * h], vf[2 * h + 1]);
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            mma16816(t[h], pa[0], pa[1], pa[2], pa[3], vf[2 * h], vf[2 * h + 1]);
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[2 * d2 + h][e] += t[h][e];
+          for (int e = 0; e < 4; ++e) o[d][e] += t[e];
         }
       }
       __syncwarp();
@@ -520,31 +500,24 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     // join the warps
 #pragma unroll
-    for (int i = 0; i < NRW; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
+      if (g == 0) ml_s[warp * R + q2 + i] = make_float2(m[i], l[i]);
     }
-    if ((lane & 3) == 0)
-#pragma unroll
-      for (int i = 0; i < NRW; ++i) ml_s[warp * R + g + 8 * i] = make_float2(m[i], l[i]);
     join_rows<R>(ml_s, row_ml);
-    float w[NRW];
-#pragma unroll
-    for (int i = 0; i < NRW; ++i) w[i] = ml_s[warp * R + g + 8 * i].x;
+    const float w0 = ml_s[warp * R + q2].x, w1 = ml_s[warp * R + q2 + 1].x;
     // warps 2 and 3 put their o down, warps 0 and 1 add theirs
 #pragma unroll 1
     for (int step = 0; step < 2; ++step) {
       if ((warp < 2) == (step == 1)) {
+        float* at = join + (warp & 1) * (R * HD);
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
+        for (int d = 0; d < HT; ++d)
 #pragma unroll
-          for (int i = 0; i < NRW; ++i) {
-            float2* at = reinterpret_cast<float2*>(join + (warp & 1) * (R * HD) + join_at<HD>(g + 8 * i, d * 8 + q2));
-            float2 b = make_float2(0.f, 0.f);
-            if (step) b = *at;
-            const float x = NT == 3 ? o[d][0] + o[d][2] : o[d][2 * i];
-            const float y = NT == 3 ? o[d][1] + o[d][3] : o[d][2 * i + 1];
-            *at = make_float2(fmaf(x, w[i], b.x), fmaf(y, w[i], b.y));
+          for (int e = 0; e < 4; ++e) {
+            float& to = at[join_at<HD>(q2 + (e & 1), 16 * d + g + 8 * (e >> 1))];
+            to = fmaf(o[d][e], e & 1 ? w1 : w0, step ? to : 0.f);
           }
       }
       consumer_sync();
@@ -949,15 +922,14 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 template <int HD, int NT>
 cudaError_t launch_mma(const PagedAttnArgs& a, int grid, cudaStream_t s) {
-  constexpr int R = NT == 1 ? 16 : 8;
   CUtensorMap tk, tv;
   const uint64_t rows = (uint64_t)a.c.n_pages * a.c.nkv << a.c.page_shift;
   const uint32_t box = std::min(64, 1 << a.c.page_shift);
   if (!make_tmap_bf16_2d(&tk, a.c.k_pages, rows, HD, box) ||
       !make_tmap_bf16_2d(&tv, a.c.v_pages, rows, HD, box))
     return cudaErrorInvalidValue;
-  return launch_pdl(paged_attn_mma_kernel<HD, NT>, dim3(grid), kThreads, PgLayout<HD, 64, 2, R>::bytes, s,
-                    a, tk, tv);
+  return launch_pdl(paged_attn_mma_kernel<HD, NT>, dim3(grid), kThreads, MmaLayout<HD>::bytes, s, a,
+                    tk, tv);
 }
 template <int HD>
 cudaError_t launch_mma32(const PagedAttnArgs& a, int grid, cudaStream_t s) {
@@ -990,8 +962,8 @@ cudaError_t allow_smem(K kernel, uint32_t bytes) {
 }
 template <int HD>
 cudaError_t set_attributes_hd() {
-  cudaError_t e = allow_smem(paged_attn_mma_kernel<HD, 1>, PgLayout<HD, 64, 2, 16>::bytes);
-  if (e == cudaSuccess) e = allow_smem(paged_attn_mma_kernel<HD, 3>, PgLayout<HD, 64, 2, 8>::bytes);
+  cudaError_t e = allow_smem(paged_attn_mma_kernel<HD, 1>, MmaLayout<HD>::bytes);
+  if (e == cudaSuccess) e = allow_smem(paged_attn_mma_kernel<HD, 3>, MmaLayout<HD>::bytes);
   if (e == cudaSuccess) e = allow_smem(paged_attn_mma32_kernel<HD>, Mma32Layout<HD>::bytes);
   if (e == cudaSuccess) e = allow_smem(paged_attn_fma_kernel<HD, 2>, PgLayout<HD, 32, 4, 2>::bytes);
   if (e == cudaSuccess) e = allow_smem(paged_attn_fma_kernel<HD, 4>, PgLayout<HD, 32, 4, 4>::bytes);
@@ -1002,7 +974,8 @@ cudaError_t set_attributes_hd() {
 // Workspace of a call: counters and split descriptors, the slots of the two launches, the
 // prefix's whole records. A slot holds as many rows as an item can have: at most kMaxRows and at
 // most 8 query heads of every token.
-constexpr int kMaxSms = 192;         // CTAs per launch: at most two per SM
+constexpr int kMaxSms = 192;
+constexpr int kMaxCtas = 3 * kMaxSms;  // of a launch
 constexpr int kMaxRows = 256;
 constexpr size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 int slot_rows(int n_tokens) {
@@ -1011,12 +984,13 @@ int slot_rows(int n_tokens) {
 struct Workspace {
   size_t counters = 0, splits[2], flush, ml[2], o[2], whole_ml, whole_o, total;
   Workspace(int n_tokens, int nq, int hd, bool prefix) {
-    // an item of more than 32 rows belongs to one CTA per SM, smaller ones to two
+    // an item of more than 32 rows belongs to one CTA per SM, of more than 8 to two, smaller ones to three
     const int most = slot_rows(n_tokens);
-    const size_t rows = (size_t)2 * std::max(kMaxSms * most, 2 * kMaxSms * std::min(32, most));
-    splits[0] = align256(2 * kMaxSms * 4);
-    splits[1] = splits[0] + align256(2 * kMaxSms * sizeof(PagedSplit));
-    flush = splits[1] + align256(2 * kMaxSms * sizeof(PagedSplit));
+    const size_t rows =
+        (size_t)2 * std::max({kMaxSms * most, 2 * kMaxSms * std::min(32, most), 3 * kMaxSms * 8});
+    splits[0] = align256(kMaxCtas * 4);
+    splits[1] = splits[0] + align256(kMaxCtas * sizeof(PagedSplit));
+    flush = splits[1] + align256(kMaxCtas * sizeof(PagedSplit));
     // (tensor-core tiles have more than 16 rows: three tokens at least)
     size_t at = flush + (n_tokens > 2 ? (size_t)kMaxSms * 128 * 128 * 4 : 0);
     for (int i = 0; i < (prefix ? 2 : 1); ++i) {
@@ -1064,7 +1038,8 @@ PagedPlan plan_paged_pass(const PagedAttnArgs& a, long long rows, long long keys
     return p;
   }
   p.kt = 64;
-  p.rows = a.act_bf16 ? 16 : 8;
+  p.rows = 8;
+  p.grid = 3 * sms;
   if (rows > 16) {
     auto us = [&](double start, double tile, int kt, int item_rows, int units, int grid) {
       const double items = (double)a.c.nkv * ((rows + item_rows - 1) / item_rows);
