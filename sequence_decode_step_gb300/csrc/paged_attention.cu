@@ -7,23 +7,24 @@
 // row join as m' = max, weights 2^(m - m').
 //
 // One producer warp walks the CTA's units (paged_sched.cuh), looks the pages up one unit ahead and
-// streams key and value tiles into a ring of 96 KB with TMA, across item boundaries, so that short
-// sequences do not drain the stream; two CTAs per SM keep 192 KB in flight. Four consumer warps
-// share every tile by keys, each with its own (m, l, o) in registers: no barrier per tile, one
-// join in shared memory per item.
+// streams key and value tiles of 32 KB into a ring with TMA, across item boundaries, so that short
+// sequences do not drain the stream; three CTAs per SM (rings of 64 KB) keep 192 KB in flight and fill
+// each other's gaps between items. Four consumer warps share every tile by keys, each with its own
+// (m, l, o) in registers: no barrier per tile, one join in shared memory per item.
 //
-// bf16 pages (kernel _mma): 64-key tiles, products on the tensor cores with mma.sync. At most 16
-// query rows meet a key here, so a tcgen05 tile of 128 rows would be empty and HBM is the bound:
-// 128 (NT = 1) or 256 (NT = 3) mma of 64 keys take ~250-500 cycles of an SM whose HBM share
-// delivers the tile's 32 KB in ~1400. f32 activations keep f32 results: q and P enter as three
-// bf16 terms (24 bits), rows 0-7 of a fragment carrying the first and rows 8-15 the second term,
-// the third in a second mma, so R = 8 rows cost two mma instead of three.
+// bf16 pages, up to 8 query rows (kernel _mma): 64-key tiles, products on the tensor cores with mma.sync,
+// keys and head columns as the 16-row side and the query rows as the 8-column side. So few rows meet a
+// key that a tcgen05 tile of 128 rows would be empty and HBM is the bound: the 64 (NT = 1) or 192 (NT = 3)
+// mma of a tile take about 200-600 cycles of an SM whose HBM share delivers its 32 KB in ~1400. f32
+// activations keep f32 results: q and P enter as three bf16 terms (24 bits). Measured: 256 sequences of
+// up to 8K keys 654 us bf16, 651 f32 (6.8 TB/s, the copy's rate); 256 x 128 keys 35 and 40 us (20 of HBM).
 // f32 pages, up to 8 query rows (kernel _fma): 32-key tiles and f32 FMAs, lanes splitting the head
-// dimension (512 contiguous bytes of a row per load), scores summed by a transposing butterfly.
+// dimension (512 contiguous bytes of a row per load), scores summed by a transposing butterfly. 256
+// sequences of up to 8K keys: 1 256 us (6.9 TB/s).
 // f32 pages, more rows (kernel _mma32): tiles of 32 query rows x 32 keys on mma.sync with q, K, P and V
 // in three bf16 terms each and the six products above 2^-24. A warp takes 16 rows x 16 keys and splits
 // the keys and values in its registers: ~1000 instructions for 256 (row, key) pairs, where the FMA
-// kernel needs ~950 for 64.
+// kernel needs ~950 for 64. The bound is mma.sync itself, at 3.1 cycles per instruction and SM.
 
 #include <cuda_runtime.h>
 #include <math.h>
@@ -781,12 +782,16 @@ struct Lane<2> {
   }
 };
 
-// R query rows (2, 4 or 8, the least power of two that holds a tile), q and o in registers.
+// R query rows (2, 4 or 8, the least power of two that holds a tile), q and o in registers, which
+// leave room for three CTAs per SM up to four rows.
+constexpr int fma_ctas(int r) { return r <= 4 ? 3 : 2; }
 template <int HD, int R>
-__global__ void __launch_bounds__(kThreads, 2)
+using FmaLayout = PgLayout<HD, 32, 4, R, fma_ctas(R) == 3 ? 64 * 1024 : 96 * 1024>;
+template <int HD, int R>
+__global__ void __launch_bounds__(kThreads, fma_ctas(R))
     paged_attn_fma_kernel(const __grid_constant__ PagedAttnArgs a) {
   constexpr int KT = 32, E = HD / 32, KW = KT / kConsumers;  // 8 keys of a tile per warp
-  using LY = PgLayout<HD, KT, 4, R>;
+  using LY = FmaLayout<HD, R>;
   constexpr int NS = LY::kStages;
   extern __shared__ __align__(1024) uint8_t sm[];
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + LY::off_bar);
@@ -943,7 +948,7 @@ cudaError_t launch_mma32(const PagedAttnArgs& a, int grid, cudaStream_t s) {
 }
 template <int HD, int R>
 cudaError_t launch_fma(const PagedAttnArgs& a, int grid, cudaStream_t s) {
-  return launch_pdl(paged_attn_fma_kernel<HD, R>, dim3(grid), kThreads, PgLayout<HD, 32, 4, R>::bytes, s, a);
+  return launch_pdl(paged_attn_fma_kernel<HD, R>, dim3(grid), kThreads, FmaLayout<HD, R>::bytes, s, a);
 }
 template <int HD>
 cudaError_t launch_pass(const PagedAttnArgs& a, const PagedPlan& p, cudaStream_t s) {
@@ -965,9 +970,9 @@ cudaError_t set_attributes_hd() {
   cudaError_t e = allow_smem(paged_attn_mma_kernel<HD, 1>, MmaLayout<HD>::bytes);
   if (e == cudaSuccess) e = allow_smem(paged_attn_mma_kernel<HD, 3>, MmaLayout<HD>::bytes);
   if (e == cudaSuccess) e = allow_smem(paged_attn_mma32_kernel<HD>, Mma32Layout<HD>::bytes);
-  if (e == cudaSuccess) e = allow_smem(paged_attn_fma_kernel<HD, 2>, PgLayout<HD, 32, 4, 2>::bytes);
-  if (e == cudaSuccess) e = allow_smem(paged_attn_fma_kernel<HD, 4>, PgLayout<HD, 32, 4, 4>::bytes);
-  if (e == cudaSuccess) e = allow_smem(paged_attn_fma_kernel<HD, 8>, PgLayout<HD, 32, 4, 8>::bytes);
+  if (e == cudaSuccess) e = allow_smem(paged_attn_fma_kernel<HD, 2>, FmaLayout<HD, 2>::bytes);
+  if (e == cudaSuccess) e = allow_smem(paged_attn_fma_kernel<HD, 4>, FmaLayout<HD, 4>::bytes);
+  if (e == cudaSuccess) e = allow_smem(paged_attn_fma_kernel<HD, 8>, FmaLayout<HD, 8>::bytes);
   return e;
 }
 
@@ -1016,7 +1021,8 @@ cudaError_t set_paged_attributes() {
   return e == cudaSuccess ? set_paged_tc_attributes() : e;
 }
 
-// Tiles of 32 KB that an item's q, join and output cost a CTA: 6 us against 1.3 us a tile.
+// Tiles of 32 KB that an item's q, join and output cost a CTA: 6 us against 1.3 us a tile (3 to 5 give
+// the same within 2 % on the ragged cases).
 constexpr int kDecodeItemUnits = 5;
 
 // Keys per tile, query rows per item, CTAs and an item's own cost of a launch over sequences with
@@ -1024,8 +1030,8 @@ constexpr int kDecodeItemUnits = 5;
 //
 // bf16 pages: few rows run the mma.sync kernel; more than 16 the tensor-core tiles, unless there is so
 // little of it that their start (about 16 us with q, first product and output against 4) is most of the
-// time. Measured per tile and CTA: 1.3 us for 64 keys here, and for 128 keys there 1.5 us (bf16) or 2.9 us
-// (f32 in three terms): a 4K prefix of 128 rows takes 22 us against 43, a 2-key one 16 against 6.
+// time. Measured per tile and CTA: 1.5 us for 64 keys here, and for 128 keys there 1.5 us (bf16) or 2.9 us
+// (f32 in three terms): a 4K prefix of 128 rows takes 22 us against 34, a 2-key one 16 against 6.
 // f32 pages: the least tile of the FMA kernel that holds the rows, or tiles of 32 rows.
 PagedPlan plan_paged_pass(const PagedAttnArgs& a, long long rows, long long keys, int sms) {
   sms = std::min(sms, kMaxSms);
@@ -1035,6 +1041,7 @@ PagedPlan plan_paged_pass(const PagedAttnArgs& a, long long rows, long long keys
   if (!a.c.kv_bf16) {
     p.kt = 32;
     p.rows = rows <= 2 ? 2 : rows <= 4 ? 4 : rows <= 8 ? 8 : 32;
+    if (p.rows <= 8) p.grid = fma_ctas(p.rows) * sms;
     return p;
   }
   p.kt = 64;
@@ -1047,7 +1054,7 @@ PagedPlan plan_paged_pass(const PagedAttnArgs& a, long long rows, long long keys
     };
     const int tc_rows = paged_tc_rows(a.act_bf16), tc_units = 5;  // 7 us (with the last tile's drain) against 1.5 us a tile
     if (us(16, a.act_bf16 ? 1.5 : 2.9, kPagedTcKeys, tc_rows, tc_units, sms) <
-        us(4, 1.3, p.kt, p.rows, p.item_units, p.grid))
+        us(4, 1.5, p.kt, p.rows, p.item_units, p.grid))
       p = PagedPlan{true, kPagedTcKeys, tc_rows, sms, tc_units};
   }
   return p;
