@@ -18,9 +18,11 @@
 // mma of a tile take about 200-600 cycles of an SM whose HBM share delivers its 32 KB in ~1400. f32
 // activations keep f32 results: q and P enter as three bf16 terms (24 bits). Measured: 256 sequences of
 // up to 8K keys 654 us bf16, 651 f32 (6.8 TB/s, the copy's rate); 256 x 128 keys 35 and 40 us (20 of HBM).
-// f32 pages, up to 8 query rows (kernel _fma): 32-key tiles and f32 FMAs, lanes splitting the head
+// f32 pages, up to 4 query rows (kernel _fma): 32-key tiles and f32 FMAs, lanes splitting the head
 // dimension (512 contiguous bytes of a row per load), scores summed by a transposing butterfly. 256
 // sequences of up to 8K keys: 1 256 us (6.9 TB/s).
+// f32 pages, up to 8 rows (kernel _mma8): as _mma, with all four operands in three bf16 terms. FMAs for 8
+// rows take 1.2 times the HBM time; these products about half of it.
 // f32 pages, more rows (kernel _mma32): tiles of 32 query rows x 32 keys on mma.sync with q, K, P and V
 // in three bf16 terms each and the six products above 2^-24. A warp takes 16 rows x 16 keys and splits
 // the keys and values in its registers: ~1000 instructions for 256 (row, key) pairs, where the FMA
@@ -530,6 +532,42 @@ __global__ void __launch_bounds__(kThreads, 3)
 }
 
 // ------------------------------------------------------------------ f32 pages, many rows: mma.sync
+// The item's q rows as three bf16 planes [R][HD] in shared memory (where the join works at its end):
+// 16-byte units of a row exchanged by the row, columns 4q + e (4q + 2 + e) of a 16-column k-step at its
+// positions 2q + e (8 + 2q + e).
+template <int HD, int R>
+__device__ __forceinline__ void stage_q_terms(const PagedAttnArgs& a, const PagedCursor& c, uint32_t gmul,
+                                              int tok0, int rows, uint8_t* to) {
+  constexpr uint32_t kPlane = R * HD * 2;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < R * HD / 8; i += kConsumers * 32) {
+    const int r = i / (HD / 8), u = i % (HD / 8), t = paged_token(r, gmul);
+    const size_t at = (size_t)(c.s.lo + tok0 + t) * a.ldq + (size_t)(c.kvh * a.gq + r - t * a.gq) * HD + u * 8;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+    if (r < rows) {
+      if (a.act_bf16) {
+        x = KvElem<true>::load4(static_cast<const uint16_t*>(a.q) + at);
+        y = KvElem<true>::load4(static_cast<const uint16_t*>(a.q) + at + 4);
+      } else {
+        x = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at));
+        y = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at + 4));
+      }
+    }
+    uint32_t t0[3], t1[3], t2[3], t3[3];  // terms of columns (0, 1), (2, 3), (4, 5), (6, 7)
+    split3(x.x, x.y, t0[0], t0[1], t0[2]);
+    split3(x.z, x.w, t1[0], t1[1], t1[2]);
+    split3(y.x, y.y, t2[0], t2[1], t2[2]);
+    split3(y.z, y.w, t3[0], t3[1], t3[2]);
+    uint8_t* row = to + r * (HD * 2) + (u & 1) * 8;
+    const int ch = u & ~1;
+#pragma unroll
+    for (int e = 0; e < 3; ++e) {
+      *reinterpret_cast<uint2*>(row + e * kPlane + ((ch ^ (r & 7)) << 4)) = make_uint2(t0[e], t2[e]);
+      *reinterpret_cast<uint2*>(row + e * kPlane + (((ch + 1) ^ (r & 7)) << 4)) = make_uint2(t1[e], t3[e]);
+    }
+  }
+}
+
 // Warp (kh, rh) = (warp & 1, warp >> 1) takes keys 16 kh .. and rows 16 rh .. of every 32 x 32 tile.
 // Which of a fragment's k and n positions a column or a key takes is free as long as both operands
 // agree; the places below let every thread read 16 bytes at once without bank conflicts:
@@ -573,36 +611,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   do {
     const int n = c.kend - c.kt;
     const int tok0 = c.rt * a.tpt, rows = min(a.tpt, c.s.nb - tok0) * a.gq;
-    {  // q's terms in shared memory (where the join works at the item's end)
-      uint8_t* to = reinterpret_cast<uint8_t*>(join);
-#pragma unroll 1
-      for (int i = threadIdx.x; i < R * HD / 8; i += kConsumers * 32) {
-        const int r = i / (HD / 8), u = i % (HD / 8), t = paged_token(r, gmul);
-        const size_t at = (size_t)(c.s.lo + tok0 + t) * a.ldq + (size_t)(c.kvh * a.gq + r - t * a.gq) * HD + u * 8;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-        if (r < rows) {
-          if (a.act_bf16) {
-            x = KvElem<true>::load4(static_cast<const uint16_t*>(a.q) + at);
-            y = KvElem<true>::load4(static_cast<const uint16_t*>(a.q) + at + 4);
-          } else {
-            x = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at));
-            y = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at + 4));
-          }
-        }
-        uint32_t t0[3], t1[3], t2[3], t3[3];  // terms of columns (0, 1), (2, 3), (4, 5), (6, 7)
-        split3(x.x, x.y, t0[0], t0[1], t0[2]);
-        split3(x.z, x.w, t1[0], t1[1], t1[2]);
-        split3(y.x, y.y, t2[0], t2[1], t2[2]);
-        split3(y.z, y.w, t3[0], t3[1], t3[2]);
-        uint8_t* row = to + r * (HD * 2) + (u & 1) * 8;
-        const int ch = u & ~1;
-#pragma unroll
-        for (int e = 0; e < 3; ++e) {
-          *reinterpret_cast<uint2*>(row + e * kPlane + ((ch ^ (r & 7)) << 4)) = make_uint2(t0[e], t2[e]);
-          *reinterpret_cast<uint2*>(row + e * kPlane + (((ch + 1) ^ (r & 7)) << 4)) = make_uint2(t1[e], t3[e]);
-        }
-      }
-    }
+    stage_q_terms<HD, R>(a, c, gmul, tok0, rows, reinterpret_cast<uint8_t*>(join));
     consumer_sync();
     const uint32_t qrow = smem_addr(join) + (16 * rh + (mat & 1) * 8 + mr) * (HD * 2);
     int lim[2];
@@ -764,6 +773,211 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (bad && lane == 0 && a.c.status) atomicOr(a.c.status, PG_TIMEOUT);
 }
 
+// ------------------------------------------------------------------ f32 pages, 5 to 8 rows: mma.sync
+// As paged_attn_mma_kernel, with keys and values split into three bf16 terms in registers and six
+// products. Two warps take a 32-key tile by halves, the other two the next one. Fragment places as in
+// paged_attn_mma32_kernel: a thread reads 16 bytes at once without bank conflicts; output rows g and
+// g + 8 of m-tile (blk, t) are columns 32 blk + 4 g + 2 t and the one after it.
+// 256 sequences up to 4K keys, 16 heads over 2: 68 us, with FMAs 88; 64 up to 4K, 40 over 8: 83 and 108;
+// one of 8K, 16 over 2: 26.8 and 28.7. Two CTAs per SM: the fragments take 168 registers.
+template <int HD>
+using Mma8Layout = PgLayout<HD, 32, 4, 8, 96 * 1024>;
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 2)
+    paged_attn_mma8_kernel(const __grid_constant__ PagedAttnArgs a,
+                           const __grid_constant__ CUtensorMap tk,
+                           const __grid_constant__ CUtensorMap tv) {
+  constexpr int KT = 32, R = 8, KS = HD / 16, NB = HD / 32;
+  using LY = Mma8Layout<HD>;
+  constexpr int NS = LY::kStages;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + LY::off_bar);
+  uint64_t* empty = full + NS;
+  PagedStart* st = reinterpret_cast<PagedStart*>(sm + LY::off_start);
+  if (!open_cta<KT, LY>(a, sm)) return pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == kConsumers) {
+    produce<LY, HD, KT, 4, true>(a, &tk, &tv, st, sm, full, empty);
+    return pdl_wait();
+  }
+  float* join = reinterpret_cast<float*>(sm + LY::off_join);
+  float2* ml_s = reinterpret_cast<float2*>(sm + LY::off_ml);
+  float2* row_ml = reinterpret_cast<float2*>(sm + LY::off_row);
+  int* flag = reinterpret_cast<int*>(sm + LY::off_start + 96 + 40);
+
+  const int g = lane >> 2, q = lane & 3, mat = lane >> 3, mr = lane & 7;
+  const int kh = warp & 1, pair = warp >> 1;
+  const int key_m = g & 1 ? ((g - 1) ^ 4) + 1 : g;     // key of m position g
+  const int key_a = 2 * q, key_b = ((2 * q) ^ 4) + 1;  // of k positions 2q, 2q + 1 of the outputs
+  constexpr uint32_t kPlane = R * HD * 2;
+  const uint32_t gmul = 65536u / a.gq + 1;
+  PagedCursor c = paged_cursor<KT>(a, st);
+  int seen = 0;
+  bool bad = false;
+  do {
+    const int n = c.kend - c.kt;
+    const int tok0 = c.rt * a.tpt, rows = min(a.tpt, c.s.nb - tok0) * a.gq;
+    stage_q_terms<HD, R>(a, c, gmul, tok0, rows, reinterpret_cast<uint8_t*>(join));
+    consumer_sync();
+    uint32_t qb[3][KS][2];
+    {
+      const uint32_t from = smem_addr(join) + mr * (HD * 2);
+#pragma unroll
+      for (int t = 0; t < 3; ++t)
+#pragma unroll
+        for (int ks = 0; ks < KS; ks += 2) {
+          uint32_t x[4];
+          ldsm4(from + t * kPlane + (((ks * 2 + mat) ^ mr) << 4), x);
+          qb[t][ks][0] = x[0], qb[t][ks][1] = x[1], qb[t][ks + 1][0] = x[2], qb[t][ks + 1][1] = x[3];
+        }
+    }
+    int lim[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = 2 * q + i, t = tok0 + paged_token(r, gmul);
+      lim[i] = r >= rows ? 0 : a.prefix_pass ? c.limit : min(max(c.s.base + t + 1, 0), c.s.len);
+    }
+    float o[2 * NB][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int d = 0; d < 2 * NB; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
+
+    for (int x = 0; x < n; ++x, ++seen) {
+      const int stage = seen % NS;
+      if (!bad)
+        bad = !__all_sync(0xffffffffu, mbar_wait(&full[stage], (uint32_t)((seen / NS) & 1), a.wait_ns));
+      if ((seen & 1) != pair) {  // the other pair's; a warp that left its phase out would mistake the next
+        if (lane == 0) mbar_arrive_cta(&empty[stage]);
+        continue;
+      }
+      const uint8_t* kb = sm + (uint32_t)stage * 2 * LY::kTile;
+      const uint8_t* vb = kb + LY::kTile;
+      float s[4], s2[4], s3[4];  // products of weight 1, 2^-8 and 2^-16 apart
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] = s2[i] = s3[i] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        uint32_t k[3][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int row = 16 * kh + 8 * h + key_m;
+          const float4 f = *reinterpret_cast<const float4*>(
+              kb + (ks >> 1) * (KT * 128) + row * 128 + ((((ks & 1) * 4 + q) ^ (row & 7)) << 4));
+          split3(f.x, f.y, k[0][h], k[1][h], k[2][h]);
+          split3(f.z, f.w, k[0][2 + h], k[1][2 + h], k[2][2 + h]);
+        }
+        auto add = [&](float (&d)[4], int ke, int qe) {
+          mma16816(d, k[ke][0], k[ke][1], k[ke][2], k[ke][3], qb[qe][ks][0], qb[qe][ks][1]);
+        };
+        add(s, 0, 0);
+        add(s2, 0, 1);
+        add(s3, 0, 2);
+        add(s2, 1, 0);
+        add(s3, 1, 1);
+        add(s3, 2, 0);
+      }
+      const int k0 = (c.kt + x) * KT + 16 * kh;  // this warp's first key
+      const bool edge = k0 + 16 > c.limit - a.tpt;
+      float p[4], alpha[2];
+      bool moved = false;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float u = (s[i] + (s2[i] + s3[i])) * a.scale_log2;
+        float v = (s[2 + i] + (s2[2 + i] + s3[2 + i])) * a.scale_log2;
+        if (edge || rows < R) {
+          if (k0 + key_m >= lim[i]) u = -INFINITY;
+          if (k0 + 8 + key_m >= lim[i]) v = -INFINITY;
+        }
+        float mx = fmaxf(u, v);
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        const float mn = fmaxf(m[i], mx);
+        const float mu = mn == -INFINITY ? 0.f : mn;
+        alpha[i] = paged_exp2(m[i] - mu);
+        moved = moved || mn != m[i];
+        m[i] = mn;
+        p[i] = paged_exp2(u - mu);
+        p[2 + i] = paged_exp2(v - mu);
+        l[i] = l[i] * alpha[i] + (p[i] + p[2 + i]);
+      }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int d = 0; d < 2 * NB; ++d)
+          o[d][0] *= alpha[0], o[d][1] *= alpha[1], o[d][2] *= alpha[0], o[d][3] *= alpha[1];
+      }
+      uint32_t pb[3][2];
+      split3(p[0], p[1], pb[0][0], pb[1][0], pb[2][0]);
+      split3(p[2], p[3], pb[0][1], pb[1][1], pb[2][1]);
+#pragma unroll
+      for (int t = 0; t < 3; ++t) pb[t][0] = transpose8(pb[t][0]), pb[t][1] = transpose8(pb[t][1]);
+      const int left = c.limit - k0;  // behind the last key lies whatever the page held
+#pragma unroll
+      for (int blk = 0; blk < NB; ++blk) {
+        float v[4][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = (e & 1 ? key_b : key_a) + (e & 2 ? 8 : 0), row = 16 * kh + key;
+          const float4 f = *reinterpret_cast<const float4*>(vb + blk * (KT * 128) + row * 128 +
+                                                            ((g ^ (row & 7)) << 4));
+          const bool in = key < left;
+          v[e][0] = in ? f.x : 0.f, v[e][1] = in ? f.y : 0.f, v[e][2] = in ? f.z : 0.f, v[e][3] = in ? f.w : 0.f;
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          uint32_t w[3][4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            split3(v[0][2 * t + h], v[1][2 * t + h], w[0][h], w[1][h], w[2][h]);
+            split3(v[2][2 * t + h], v[3][2 * t + h], w[0][2 + h], w[1][2 + h], w[2][2 + h]);
+          }
+          // (mma adds with rounding towards zero: a tile's sum is formed apart)
+          float d[4] = {0.f, 0.f, 0.f, 0.f}, d2[4] = {0.f, 0.f, 0.f, 0.f};
+          auto add = [&](float (&x2)[4], int ve, int pe) {
+            mma16816(x2, w[ve][0], w[ve][1], w[ve][2], w[ve][3], pb[pe][0], pb[pe][1]);
+          };
+          add(d2, 0, 2);
+          add(d, 0, 0);
+          add(d2, 1, 1);
+          add(d2, 2, 0);
+          add(d2, 0, 1);
+          add(d2, 1, 0);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[2 * blk + t][e] += d[e] + d2[e];
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cta(&empty[stage]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
+      if (g == 0) ml_s[warp * R + 2 * q + i] = make_float2(m[i], l[i]);
+    }
+    join_rows<R>(ml_s, row_ml);
+#pragma unroll 1
+    for (int step = 0; step < 2; ++step) {
+      if ((warp < 2) == (step == 1)) {
+        float* at = join + (warp & 1) * (R * HD);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float w = ml_s[warp * R + 2 * q + e].x;
+#pragma unroll
+          for (int blk = 0; blk < NB; ++blk) {
+            float4& to = *reinterpret_cast<float4*>(at + join_at<HD>(2 * q + e, 32 * blk + 4 * g));
+            const float4 old = step ? to : make_float4(0.f, 0.f, 0.f, 0.f);
+            to = make_float4(fmaf(o[2 * blk][e], w, old.x), fmaf(o[2 * blk][2 + e], w, old.y),
+                             fmaf(o[2 * blk + 1][e], w, old.z), fmaf(o[2 * blk + 1][2 + e], w, old.w));
+          }
+        }
+      }
+      consumer_sync();
+    }
+    finish_segment<HD, R>(a, c, gmul, join, row_ml, flag);
+    consumer_sync();
+  } while (c.next<KT>(a));
+  if (bad && lane == 0 && a.c.status) atomicOr(a.c.status, PG_TIMEOUT);
+}
+
 // ------------------------------------------------------------------ f32 pages: FMAs
 template <int E>
 struct Lane;  // E consecutive floats of a lane
@@ -782,13 +996,11 @@ struct Lane<2> {
   }
 };
 
-// R query rows (2, 4 or 8, the least power of two that holds a tile), q and o in registers, which
-// leave room for three CTAs per SM up to four rows.
-constexpr int fma_ctas(int r) { return r <= 4 ? 3 : 2; }
+// R query rows (2 or 4), q and o in registers.
 template <int HD, int R>
-using FmaLayout = PgLayout<HD, 32, 4, R, fma_ctas(R) == 3 ? 64 * 1024 : 96 * 1024>;
+using FmaLayout = PgLayout<HD, 32, 4, R, 64 * 1024>;
 template <int HD, int R>
-__global__ void __launch_bounds__(kThreads, fma_ctas(R))
+__global__ void __launch_bounds__(kThreads, 3)
     paged_attn_fma_kernel(const __grid_constant__ PagedAttnArgs a) {
   constexpr int KT = 32, E = HD / 32, KW = KT / kConsumers;  // 8 keys of a tile per warp
   using LY = FmaLayout<HD, R>;
@@ -936,15 +1148,18 @@ cudaError_t launch_mma(const PagedAttnArgs& a, int grid, cudaStream_t s) {
   return launch_pdl(paged_attn_mma_kernel<HD, NT>, dim3(grid), kThreads, MmaLayout<HD>::bytes, s, a,
                     tk, tv);
 }
-template <int HD>
-cudaError_t launch_mma32(const PagedAttnArgs& a, int grid, cudaStream_t s) {
+template <int HD, int R>
+cudaError_t launch_mma_f32(const PagedAttnArgs& a, int grid, cudaStream_t s) {
   CUtensorMap tk, tv;
   const uint64_t rows = (uint64_t)a.c.n_pages * a.c.nkv << a.c.page_shift;
   const uint32_t box = std::min(32, 1 << a.c.page_shift);
   if (!make_tmap_f32_2d(&tk, a.c.k_pages, rows, HD, box) ||
       !make_tmap_f32_2d(&tv, a.c.v_pages, rows, HD, box))
     return cudaErrorInvalidValue;
-  return launch_pdl(paged_attn_mma32_kernel<HD>, dim3(grid), kThreads, Mma32Layout<HD>::bytes, s, a, tk, tv);
+  if constexpr (R == 8)
+    return launch_pdl(paged_attn_mma8_kernel<HD>, dim3(grid), kThreads, Mma8Layout<HD>::bytes, s, a, tk, tv);
+  else
+    return launch_pdl(paged_attn_mma32_kernel<HD>, dim3(grid), kThreads, Mma32Layout<HD>::bytes, s, a, tk, tv);
 }
 template <int HD, int R>
 cudaError_t launch_fma(const PagedAttnArgs& a, int grid, cudaStream_t s) {
@@ -955,10 +1170,10 @@ cudaError_t launch_pass(const PagedAttnArgs& a, const PagedPlan& p, cudaStream_t
   if (p.tc) return launch_paged_tc(a, HD, p.grid, s);
   if (a.c.kv_bf16)
     return a.act_bf16 ? launch_mma<HD, 1>(a, p.grid, s) : launch_mma<HD, 3>(a, p.grid, s);
-  if (p.rows == 32) return launch_mma32<HD>(a, p.grid, s);
+  if (p.rows == 32) return launch_mma_f32<HD, 32>(a, p.grid, s);
+  if (p.rows == 8) return launch_mma_f32<HD, 8>(a, p.grid, s);
   if (p.rows == 2) return launch_fma<HD, 2>(a, p.grid, s);
-  if (p.rows == 4) return launch_fma<HD, 4>(a, p.grid, s);
-  return launch_fma<HD, 8>(a, p.grid, s);
+  return launch_fma<HD, 4>(a, p.grid, s);
 }
 
 template <class K>
@@ -970,9 +1185,9 @@ cudaError_t set_attributes_hd() {
   cudaError_t e = allow_smem(paged_attn_mma_kernel<HD, 1>, MmaLayout<HD>::bytes);
   if (e == cudaSuccess) e = allow_smem(paged_attn_mma_kernel<HD, 3>, MmaLayout<HD>::bytes);
   if (e == cudaSuccess) e = allow_smem(paged_attn_mma32_kernel<HD>, Mma32Layout<HD>::bytes);
+  if (e == cudaSuccess) e = allow_smem(paged_attn_mma8_kernel<HD>, Mma8Layout<HD>::bytes);
   if (e == cudaSuccess) e = allow_smem(paged_attn_fma_kernel<HD, 2>, FmaLayout<HD, 2>::bytes);
   if (e == cudaSuccess) e = allow_smem(paged_attn_fma_kernel<HD, 4>, FmaLayout<HD, 4>::bytes);
-  if (e == cudaSuccess) e = allow_smem(paged_attn_fma_kernel<HD, 8>, FmaLayout<HD, 8>::bytes);
   return e;
 }
 
@@ -1032,7 +1247,7 @@ constexpr int kDecodeItemUnits = 5;
 // little of it that their start (about 16 us with q, first product and output against 4) is most of the
 // time. Measured per tile and CTA: 1.5 us for 64 keys here, and for 128 keys there 1.5 us (bf16) or 2.9 us
 // (f32 in three terms): a 4K prefix of 128 rows takes 22 us against 34, a 2-key one 16 against 6.
-// f32 pages: the least tile of the FMA kernel that holds the rows, or tiles of 32 rows.
+// f32 pages: the least tile that holds the rows: 2 or 4 with FMAs, 8 or 32 with mma.sync.
 PagedPlan plan_paged_pass(const PagedAttnArgs& a, long long rows, long long keys, int sms) {
   sms = std::min(sms, kMaxSms);
   PagedPlan p{};
@@ -1041,7 +1256,7 @@ PagedPlan plan_paged_pass(const PagedAttnArgs& a, long long rows, long long keys
   if (!a.c.kv_bf16) {
     p.kt = 32;
     p.rows = rows <= 2 ? 2 : rows <= 4 ? 4 : rows <= 8 ? 8 : 32;
-    if (p.rows <= 8) p.grid = fma_ctas(p.rows) * sms;
+    if (p.rows <= 4) p.grid = 3 * sms;
     return p;
   }
   p.kt = 64;
