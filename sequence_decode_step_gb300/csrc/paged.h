@@ -110,8 +110,10 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& base, int hd, int max_ne
 cudaError_t set_paged_attributes();
 
 // ---- tensor-core tiles (paged_attention_tc.cu) ----
-constexpr int kPagedTcKeys = 128;  // keys per tile
-int paged_tc_rows(bool act_bf16);  // query rows per item
+constexpr __host__ __device__ int paged_tc_keys(bool kv_bf16) { return kv_bf16 ? 128 : 64; }  // per tile
+constexpr int paged_tc_rows(bool act_bf16, bool kv_bf16) {  // query rows per item
+  return act_bf16 && kv_bf16 ? 256 : 128;
+}
 cudaError_t launch_paged_tc(const PagedAttnArgs& a, int hd, int grid, cudaStream_t s);
 // Joins the records of the items that the launch before it (`grid` CTAs) has split.
 cudaError_t launch_paged_join(const PagedAttnArgs& a, int hd, int grid, int item_rows, cudaStream_t s);

@@ -23,7 +23,7 @@
 // sequences of up to 8K keys: 1 256 us (6.9 TB/s).
 // f32 pages, up to 8 rows (kernel _mma8): as _mma, with all four operands in three bf16 terms. FMAs for 8
 // rows take 1.2 times the HBM time; these products about half of it.
-// f32 pages, more rows (kernel _mma32): tiles of 32 query rows x 32 keys on mma.sync with q, K, P and V
+// f32 pages, more rows and few keys (kernel _mma32): tiles of 32 query rows x 32 keys on mma.sync with q, K, P and V
 // in three bf16 terms each and the six products above 2^-24. A warp takes 16 rows x 16 keys and splits
 // the keys and values in its registers: ~1000 instructions for 256 (row, key) pairs, where the FMA
 // kernel needs ~950 for 64. The bound is mma.sync itself, at 3.1 cycles per instruction and SM.
@@ -1247,30 +1247,27 @@ constexpr int kDecodeItemUnits = 5;
 // little of it that their start (about 16 us with q, first product and output against 4) is most of the
 // time. Measured per tile and CTA: 1.5 us for 64 keys here, and for 128 keys there 1.5 us (bf16) or 2.9 us
 // (f32 in three terms): a 4K prefix of 128 rows takes 22 us against 34, a 2-key one 16 against 6.
-// f32 pages: the least tile that holds the rows: 2 or 4 with FMAs, 8 or 32 with mma.sync.
+// f32 pages: the least tile that holds the rows: 2 or 4 with FMAs, 8 or 32 with mma.sync. More than 16
+// rows by the same estimate: 3.3 us for 32 rows x 32 keys on mma.sync, 2.5 us for 128 rows x 64 keys on the
+// tensor-core tiles, whose start takes 2 us more. Measured, with a key of each sequence's own: a prefix of
+// 1K keys and 32 rows 23 us against 27, 256 rows 49 against 37; of 16K keys 66 against 56 and 381 against 103.
 PagedPlan plan_paged_pass(const PagedAttnArgs& a, long long rows, long long keys, int sms) {
   sms = std::min(sms, kMaxSms);
-  PagedPlan p{};
-  p.item_units = kDecodeItemUnits;
-  p.grid = 2 * sms;
-  if (!a.c.kv_bf16) {
-    p.kt = 32;
+  const bool f32 = !a.c.kv_bf16;
+  PagedPlan p{false, f32 ? 32 : 64, 8, 3 * sms, kDecodeItemUnits};
+  if (f32) {
     p.rows = rows <= 2 ? 2 : rows <= 4 ? 4 : rows <= 8 ? 8 : 32;
-    if (p.rows <= 4) p.grid = 3 * sms;
-    return p;
+    if (p.rows > 4) p.grid = 2 * sms;
   }
-  p.kt = 64;
-  p.rows = 8;
-  p.grid = 3 * sms;
   if (rows > 16) {
     auto us = [&](double start, double tile, int kt, int item_rows, int units, int grid) {
       const double items = (double)a.c.nkv * ((rows + item_rows - 1) / item_rows);
       return start + tile * std::ceil(items * (keys / kt + 1 + units) / grid);
     };
-    const int tc_rows = paged_tc_rows(a.act_bf16), tc_units = 5;  // 7 us (with the last tile's drain) against 1.5 us a tile
-    if (us(16, a.act_bf16 ? 1.5 : 2.9, kPagedTcKeys, tc_rows, tc_units, sms) <
-        us(4, 1.5, p.kt, p.rows, p.item_units, p.grid))
-      p = PagedPlan{true, kPagedTcKeys, tc_rows, sms, tc_units};
+    const PagedPlan t{true, paged_tc_keys(!f32), paged_tc_rows(a.act_bf16, !f32), sms, 5};
+    if (us(f32 ? 6 : 16, f32 ? 2.5 : a.act_bf16 ? 1.5 : 2.9, t.kt, t.rows, t.item_units, t.grid) <
+        us(4, f32 ? 3.3 : 1.5, p.kt, p.rows, p.item_units, p.grid))
+      p = t;
   }
   return p;
 }

@@ -1,5 +1,5 @@
 // qw_paged_attention for many query rows per key: a prefix that a batch shares, and chunks of
-// prompts. bf16 pages, tcgen05 tiles of 128 query rows x 128 keys.
+// prompts. tcgen05 tiles of 128 query rows x 128 keys (bf16 pages) or 64 keys (f32 pages).
 //
 //   S = Q K^T (TMEM, f32),  P = 2^(s scale - m) as bf16 back into TMEM,  O += P V (TMEM, f32)
 //
@@ -20,9 +20,20 @@
 // in L2 that is added to in f32 (round to nearest): below 1e-6 at any length, at 414 TFLOP/s of the formula's
 // products (32K keys, 4096 rows); every 4 tiles it would be 1.8e-6 at 494.
 //
-// Warps: 0 page look-up and TMA, 1 MMA issue, 2-5 (and 6-9) softmax; TMEM is S/P and O:
+// f32 pages (F; NT = 3): keys and values as three bf16 terms as well, six products each for S and O. Eight
+// warps of their own load the pages into registers, a tile ahead, and write the terms as three swizzled
+// planes (four warps with 16 keys each were the bound at 3.4 us a tile, eight take 2.5). Three q and six
+// key and value planes leave room for one tile of 64 keys: its keys are split while P V of the tile before
+// runs, its values during the next tile's scores. A product q . k reads 4 KB of q and 2 KB of k from shared
+// memory, 48 cycles where the tensor core needs 32, so q's first term, half of the products, lies in TMEM.
+// The small products of P V have an accumulator of their own, so that O takes 4 additions a tile at full
+// size and moves to the record every 8 tiles. 238 TFLOP/s (32K keys, 4096 rows); mma.sync tiles: 61.
+//
+// Warps: 0 page look-up and TMA, 1 MMA issue, 2-5 softmax, 6-9 softmax (NT = 1), 6-13 the planes (f32
+// pages); TMEM is S/P and O:
 //   NT = 1: S_A, S_B (128 columns each), O_A, O_B
 //   NT = 3: S_0, S_1, O, X_0, X_1 (64 each); P's first two terms overwrite S_i, the third is in X_i
+//   f32 pages: S_0, S_1 (64 each), X_0, X_1 (32 each), q's first term (64), O, O's small products
 // Work is shared as in paged_sched.cuh with one CTA per SM (its tiles fill the shared memory).
 
 #include <cuda_runtime.h>
@@ -39,9 +50,6 @@
 namespace qw {
 namespace {
 
-constexpr int KT = kPagedTcKeys;
-constexpr uint32_t kTmemX = 384;  // TMEM column of X_0 (NT = 3)
-constexpr int kFlush = 2;  // tiles of one O (NT = 3)
 
 // mbar_wait inlined: a call in the softmax loop would have to save the row of scores around it.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, int phase, uint64_t limit_ns) {
@@ -72,21 +80,39 @@ __device__ __forceinline__ float2 add2(const float2& a, const float2& b) {
   return *reinterpret_cast<float2*>(&r);
 }
 
-template <int HD, int NT>
+// TMEM columns of O, of X_i (NT = 3), of O's small products and q's first term (f32 pages)
+constexpr uint32_t kO = 256, kO2 = 384, kQ0 = 192;
+template <bool F>
+constexpr uint32_t kX = F ? 128 : 384;
+
+// F: f32 pages (NT = 3).
+template <int HD, int NT, bool F>
 struct TcLayout {
+  static constexpr int KT = paged_tc_keys(!F);
   static constexpr int kStreams = NT == 1 ? 2 : 1;
-  static constexpr int kThreads = 64 + 128 * kStreams;
+  static constexpr int kThreads = 64 + 128 * kStreams + (F ? 256 : 0);
   static constexpr uint32_t kQ1 = 128 * HD * 2;            // one term of a stream's q tile
   static constexpr uint32_t kQ = kQ1 * (NT == 1 ? 2 : 3);
-  static constexpr uint32_t kTile = KT * HD * 2;           // a K or V tile
-  static constexpr int kSlots = (224 * 1024 - kQ) / kTile > 10 ? 10 : (224 * 1024 - kQ) / kTile;
+  static constexpr uint32_t kPlane = KT * HD * 2;
+  static constexpr uint32_t kTile = kPlane * (F ? 3 : 1);  // a K or V tile
+  static constexpr int kFit = (224 * 1024 - kQ) / kTile;
+  static constexpr int kSlots = F ? kFit / 2 * 2 : kFit > 10 ? 10 : kFit;
+  // Tile g's keys are use 2g of the ring, its values use 2g + 1. With f32 pages the two take turns out of
+  // this order and have a ring each.
+  static __device__ __forceinline__ int slot(int use) {
+    return F ? (use & 1) * (kSlots / 2) + (use >> 1) % (kSlots / 2) : use % kSlots;
+  }
+  static __device__ __forceinline__ int phase(int use) {
+    return F ? (use >> 1) / (kSlots / 2) : use / kSlots;
+  }
   static constexpr uint32_t off_ring = kQ;
   static constexpr uint32_t off_start = off_ring + kSlots * kTile;
   static constexpr uint32_t off_bar = off_start + 96 + 128;
   static constexpr int kBars = 2 * kSlots + 10;
   static constexpr uint32_t off_tmem = off_bar + kBars * 8;
   static constexpr uint32_t bytes = off_tmem + 16;
-  static constexpr uint32_t t_o = 256;                     // TMEM column of O
+  static constexpr uint32_t t_s = F ? 64 : 128;            // TMEM columns between S buffers or streams
+  static constexpr int kFlush = F ? 8 : 2;                 // tiles of one O (NT = 3)
   static_assert(sizeof(PagedStart) <= 96, "start words");
   static_assert(bytes <= 227 * 1024, "tiles fit one CTA's shared memory");
 };
@@ -99,34 +125,84 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t&
 }
 
 // O of this thread's row into its column of the CTA's record [HD][128 rows], whose earlier
-// contents are scaled by f (nothing before the first time).
-template <int HD>
-__device__ __forceinline__ void add_record_hd(float* rec, uint32_t to, bool first, float f) {
+// contents are scaled by f (nothing before the first time). ready() waits for O, under the first loads.
+template <int HD, bool F, class Ready>
+__device__ __forceinline__ void add_record(float* rec, uint32_t to, bool first, float f, Ready ready) {
+  if (!F) ready();
 #pragma unroll 1
   for (int d = 0; d < HD; d += 64) {
-    uint32_t o[4][16];
     float old[64];
 #pragma unroll
     for (int e = 0; e < 64; ++e) old[e] = first ? 0.f : __ldcg(rec + (d + e) * 128);
+    if (F && d == 0) ready();
+    constexpr int C = F ? 1 : 4;  // 16 columns each
 #pragma unroll
-    for (int i = 0; i < 4; ++i) tmem_ld16(to + d + 16 * i, o[i]);
-    tmem_ld_wait();
+    for (int i0 = 0; i0 < 4; i0 += C) {
+      uint32_t o[C][16], o2[16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      tmem_regs_ready(o[i]);
+      for (int i = 0; i < C; ++i) tmem_ld16(to + d + 16 * (i0 + i), o[i]);
+      if constexpr (F) tmem_ld16(to + (kO2 - kO) + d + 16 * i0, o2);
+      tmem_ld_wait();
+      if constexpr (F) tmem_regs_ready(o2);
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
-        __stcg(rec + (d + 16 * i + e) * 128, fmaf(old[16 * i + e], f, __uint_as_float(o[i][e])));
+      for (int i = 0; i < C; ++i) {
+        tmem_regs_ready(o[i]);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float x = __uint_as_float(o[i][e]) + (F ? __uint_as_float(o2[e]) : 0.f);
+          __stcg(rec + (d + 16 * (i0 + i) + e) * 128, fmaf(old[16 * (i0 + i) + e], f, x));
+        }
+      }
     }
   }
 }
 
-template <int HD, int NT>
-__global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
+__device__ __forceinline__ float4 load_once(const float* p) {  // 16 bytes that this SM does not read again
+  float4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// f32 pages: one of eight warps' 8 keys of a tile, split into the three bf16 planes [KT][HD] of a K or V
+// tile (rows of 128 bytes with 128-byte swizzling, as TMA writes them for bf16 pages). A load takes 512
+// bytes of a page; keys behind the last one are zeros.
+template <int HD>
+struct TcRows {
+  static constexpr int kKeys = 8, RPI = 128 / HD, N = kKeys / RPI;  // rows per load, loads
+  float4 v[N];
+  __device__ __forceinline__ void load(const float* pages, long long row, int keys, int lane) {
+    const int sub = lane / (HD / 4), col = lane % (HD / 4) * 4;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i * RPI + sub < keys) v[i] = load_once(pages + (row + i * RPI + sub) * HD + col);
+    }
+  }
+  template <uint32_t PLANE>
+  __device__ __forceinline__ void store(uint8_t* tile, int w, int lane) const {
+    const int sub = lane / (HD / 4), u = lane % (HD / 4);
+    uint8_t* to = tile + (u >> 4) * (64 * 128) + (u & 1) * 8;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int row = kKeys * w + i * RPI + sub;
+      uint2 t[3];
+      split3(v[i].x, v[i].y, t[0].x, t[1].x, t[2].x);
+      split3(v[i].z, v[i].w, t[0].y, t[1].y, t[2].y);
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+        *reinterpret_cast<uint2*>(to + e * PLANE + row * 128 + ((((u >> 1) & 7) ^ (row & 7)) << 4)) = t[e];
+    }
+  }
+};
+
+template <int HD, int NT, bool F>
+__global__ void __launch_bounds__(TcLayout<HD, NT, F>::kThreads, 1)
     paged_attn_tc_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ CUtensorMap tk,
                          const __grid_constant__ CUtensorMap tv) {
-  using LY = TcLayout<HD, NT>;
-  constexpr int NS = LY::kSlots, ST = LY::kStreams, QA = HD / 64;
+  using LY = TcLayout<HD, NT, F>;
+  constexpr int KT = LY::KT, NS = LY::kSlots, ST = LY::kStreams, QA = HD / 64, kFlush = LY::kFlush;
   extern __shared__ __align__(1024) uint8_t sm[];
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(sm + LY::off_bar);
   uint64_t* kv_empty = kv_full + NS;
@@ -142,7 +218,7 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_full[i], F ? 8 : 1);          // the converting warps, or the tensor copies
       mbar_init(&kv_empty[i], NT == 1 ? 2 : 1);  // the streams' softmax warps, or a commit
     }
     mbar_init(q_full, 4 * ST);  // one arrival per softmax warp
@@ -169,6 +245,68 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
   const bool idle = !st->any;
 
   if (idle) {
+  } else if (F && warp == 0) {
+  } else if (F && warp >= 6) {
+    // ---- f32 pages into the planes. The tensor core's order is S_0, then S_(g+1), P V_g: the keys of tile
+    // g + 1 are split during P V_(g-1), the values of tile g during S_(g+1). A thread's next rows of
+    // both are in flight meanwhile.
+    const int w = warp - 6;
+    PagedCursor c = paged_cursor<KT>(a, st);
+    TcRows<HD> k, v;
+    struct Place {
+      long long row;
+      int keys;
+    };
+    bool ok = true, more = true;
+    int page = 0;  // of the cursor's tile, not yet checked, so that nothing waits for it before it is used
+    auto find = [&] {
+      const int key = c.kt * KT + TcRows<HD>::kKeys * w;
+      if (key < c.limit) page = paged_page_entry(a, c.b, key);
+    };
+    auto take = [&] {  // the cursor's place; on to the next tile
+      const int key = c.kt * KT + TcRows<HD>::kKeys * w, keys = c.limit - key;
+      const Place x{keys > 0 ? paged_row(a, paged_page_checked(a, page), c.kvh, key) : 0, keys};
+      if (++c.kt == c.kend) more = c.next<KT>(a);
+      if (more) find();
+      return x;
+    };
+    auto load = [&](TcRows<HD>& x, const void* pages, const Place& at) {
+      x.load(static_cast<const float*>(pages), at.row, at.keys, lane);
+    };
+    auto put = [&](const TcRows<HD>& x, int use) {
+      const int slot = LY::slot(use), n = LY::phase(use);
+      if (ok && n > 0) ok = __all_sync(0xffffffffu, wait_for(&kv_empty[slot], n - 1, a.wait_ns));
+      if (!ok) return;
+      x.template store<LY::kPlane>(sm + LY::off_ring + slot * LY::kTile, w, lane);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cta(&kv_full[slot]);
+    };
+    find();
+    Place at = take();
+    load(k, a.c.k_pages, at);
+    load(v, a.c.v_pages, at);
+    put(k, 0);
+    bool ahead = more;  // k holds tile g + 1, v tile g
+    if (more) {
+      at = take();
+      load(k, a.c.k_pages, at);
+    }
+#pragma unroll 1
+    for (int g = 0; ok; ++g) {
+      const Place now = at;
+      const bool was = ahead;
+      if (was) put(k, 2 * g + 2);
+      ahead = more;
+      if (more) {
+        at = take();
+        load(k, a.c.k_pages, at);
+      }
+      put(v, 2 * g + 1);
+      if (!was) break;
+      load(v, a.c.v_pages, now);
+    }
+    if (!ok && lane == 0 && a.c.status) atomicOr(a.c.status, PG_TIMEOUT);
   } else if (warp == 0) {
     // ---- producer: lane = (K or V) x column block x piece of a page's rows
     const int prow = min(KT, 1 << a.c.page_shift), np = KT / prow;
@@ -232,22 +370,30 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
     const uint64_t dq = sw128_kmajor_desc(smem_addr(sm));
     const uint64_t dk = sw128_kmajor_desc(smem_addr(sm + LY::off_ring));
     const uint64_t dv = sw128_mnmajor_desc(smem_addr(sm + LY::off_ring), KT * 128);
-    auto slot_at = [&](int use) { return (uint64_t)((uint32_t)(use % NS) * (LY::kTile >> 4)); };
+    auto slot_at = [&](int use) { return (uint64_t)((uint32_t)LY::slot(use) * (LY::kTile >> 4)); };
     auto issue_s = [&](uint64_t q, uint64_t k, uint32_t d) {  // d = q . k^T, the smallest term of q first
       if (lead) {
+        auto product = [&](int tq, int tkey, bool zero) {
 #pragma unroll
-        for (int i = 0; i < HD / 16; ++i) {
-          const int at = (i >> 2) * (128 * 128) + (i & 3) * 32;  // k-step i of q and of k alike
-          tc_mma_bf16(d, q + (((NT - 1) * LY::kQ1 + at) >> 4), k + (at >> 4), id_s, i != 0);
-        }
-        if constexpr (NT == 3) {
+          for (int i = 0; i < HD / 16; ++i) {
+            const int in = (i & 3) * 32, cb = i >> 2;  // k-step i: place in the column block
+            const uint64_t kd = k + ((tkey * LY::kPlane + cb * (KT * 128) + in) >> 4);
+            if (F && tq == 0)
+              tc_mma_bf16_ta(d, tm + kQ0 + 8 * i, kd, id_s, !zero || i != 0);
+            else
+              tc_mma_bf16(d, q + ((tq * LY::kQ1 + cb * (128 * 128) + in) >> 4), kd, id_s, !zero || i != 0);
+          }
+        };
+        if constexpr (F) {
+          product(2, 0, true);
+          product(1, 1, false);
+          product(0, 2, false);
+          product(1, 0, false);
+          product(0, 1, false);
+          product(0, 0, false);
+        } else {
 #pragma unroll
-          for (int t = 1; t >= 0; --t)
-#pragma unroll
-            for (int i = 0; i < HD / 16; ++i) {
-              const int at = (i >> 2) * (128 * 128) + (i & 3) * 32;
-              tc_mma_bf16(d, q + ((t * LY::kQ1 + at) >> 4), k + (at >> 4), id_s, 1);
-            }
+          for (int t = NT - 1; t >= 0; --t) product(t, 0, t == NT - 1);
         }
       }
       __syncwarp();
@@ -262,7 +408,7 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
     auto wait = [&](uint64_t* bar, int n) {
       return __all_sync(0xffffffffu, wait_for(bar, n, a.wait_ns)) != 0;
     };
-    auto kv_wait = [&](int use) { return wait(&kv_full[use % NS], use / NS); };
+    auto kv_wait = [&](int use) { return wait(&kv_full[LY::slot(use)], LY::phase(use)); };
     bool ok = true;
     do {
       const int n = __shfl_sync(0xffffffffu, c.kend - c.kt, 0);
@@ -291,7 +437,7 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
               if (lead) {
 #pragma unroll
                 for (int i = 0; i < KT / 32; ++i)
-                  tc_mma_bf16_ta(p + LY::t_o, p + 8 * (i0 + i), v + ((i0 + i) * 2048 >> 4), id_o,
+                  tc_mma_bf16_ta(p + kO, p + 8 * (i0 + i), v + ((i0 + i) * 2048 >> 4), id_o,
                                  (x | i0 | i) != 0);
               }
               __syncwarp();
@@ -313,36 +459,47 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
           }
         }
       } else {
-        issue_s(dq, dk + slot_at(2 * tiles), tm + 128 * (tiles & 1));
+        issue_s(dq, dk + slot_at(2 * tiles), tm + LY::t_s * (tiles & 1));
         commit(&s_full[tiles & 1]);
-        commit(&kv_empty[(2 * tiles) % NS]);
+        commit(&kv_empty[LY::slot(2 * tiles)]);
         for (int x = 0; x < n; ++x) {
           const int g = tiles + x;
           if (x + 1 < n) {  // the next tile's scores while this one's weights are formed
             ok = kv_wait(2 * g + 2);
             if (!ok) break;
             tc_fence_after();
-            issue_s(dq, dk + slot_at(2 * g + 2), tm + 128 * ((g + 1) & 1));
+            issue_s(dq, dk + slot_at(2 * g + 2), tm + LY::t_s * ((g + 1) & 1));
             commit(&s_full[(g + 1) & 1]);
-            commit(&kv_empty[(2 * g + 2) % NS]);
+            commit(&kv_empty[LY::slot(2 * g + 2)]);
           }
           ok = kv_wait(2 * g + 1) && wait(&p_full[0], g);
           if (!ok) break;
           tc_fence_after();
           const uint64_t v = dv + slot_at(2 * g + 1);
-          const uint32_t p = tm + 128 * (g & 1), px = tm + kTmemX + 64 * (g & 1);
+          const uint32_t p = tm + LY::t_s * (g & 1), px = tm + kX<F> + KT / 2 * (g & 1);
           const bool fresh = x % kFlush == 0;  // (O has been taken away before p_full)
           if (lead) {
-#pragma unroll
-            for (int t = 2; t >= 0; --t)
+            auto product = [&](uint32_t d, int tp, int tval, bool zero) {
 #pragma unroll
               for (int i = 0; i < KT / 16; ++i)
-                tc_mma_bf16_ta(tm + LY::t_o, (t == 2 ? px : p + 64 * t) + 8 * i, v + (i * 2048 >> 4), id_o,
-                               !fresh || t != 2 || i != 0);
+                tc_mma_bf16_ta(d, (tp == 2 ? px : p + KT / 2 * tp) + 8 * i,
+                               v + ((tval * LY::kPlane + i * 2048) >> 4), id_o, !zero || i != 0);
+            };
+            if constexpr (F) {
+              product(tm + kO2, 2, 0, fresh);
+              product(tm + kO2, 1, 1, false);
+              product(tm + kO2, 0, 2, false);
+              product(tm + kO2, 1, 0, false);
+              product(tm + kO2, 0, 1, false);
+              product(tm + kO, 0, 0, fresh);
+            } else {
+#pragma unroll
+              for (int t = 2; t >= 0; --t) product(tm + kO, t, 0, fresh && t == 2);
+            }
           }
           __syncwarp();
           commit(&o_full[0]);
-          commit(&kv_empty[(2 * g + 1) % NS]);
+          commit(&kv_empty[LY::slot(2 * g + 1)]);
         }
       }
       tiles += n;
@@ -358,7 +515,6 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
     const uint32_t lrow = (uint32_t)((warp & 3) * 32) << 16;
     // row / gq for rows below 256 and gq <= 8
     float* const rec = a.flush + (size_t)blockIdx.x * (128 * 128) + r;  // NT = 3: [HD][128 rows]
-    auto add_record = [](float* p, uint32_t to, bool first, float f) { add_record_hd<HD>(p, to, first, f); };
     const uint32_t gmul = 65536u / a.gq + 1;
     auto token_of = [&](int row) { return (int)((uint32_t)row * gmul >> 16); };
     PagedCursor c = paged_cursor<KT>(a, st);
@@ -413,7 +569,14 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
               const int i = i0 + k * RPI + sub;
               const size_t at = source(i);
               v[k][0] = v[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (i < live_rows) {
+              if (F && a.act_bf16) {
+                if (i >= live_rows) continue;
+                const uint4 x = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at));
+                v[k][0] = make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u),
+                                      __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u));
+                v[k][1] = make_float4(__uint_as_float(x.z << 16), __uint_as_float(x.z & 0xffff0000u),
+                                      __uint_as_float(x.w << 16), __uint_as_float(x.w & 0xffff0000u));
+              } else if (i < live_rows) {
                 const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at);
                 v[k][0] = __ldg(p);
                 v[k][1] = __ldg(p + 1);
@@ -432,16 +595,30 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
             }
           }
         }
+        if constexpr (F) {  // q's first term into TMEM too
+          __syncwarp();
+          const uint8_t* from = sm + (warp & 3) * 4096 + (lane >> 3) * 1024 + (lane & 7) * 128;
+#pragma unroll
+          for (int i = 0; i < HD / 32; ++i) {
+            uint32_t x[16];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              *reinterpret_cast<uint4*>(x + 4 * e) = *reinterpret_cast<const uint4*>(
+                  from + (i >> 1) * (128 * 128) + ((((i & 1) * 4 + e) ^ (lane & 7)) << 4));
+            tmem_st16(tb + kQ0 + lrow + 16 * i, x);
+          }
+          tmem_st_wait();
+        }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cta(q_full);
       }
       float m = -INFINITY, l = 0.f, rec_m = -INFINITY;
-      const uint32_t to = tb + LY::t_o + 128 * s + lrow;
+      const uint32_t to = tb + kO + 128 * s + lrow;
       for (int x = 0; x < (rows > 0 ? n : 0); ++x, ++mine) {
         const int g = tiles + x, buf = NT == 1 ? s : g & 1;
-        const uint32_t ts = tb + 128 * buf + lrow;
+        const uint32_t ts = tb + LY::t_s * buf + lrow;
         wait(&s_full[buf], NT == 1 ? mine : g >> 1);
         tc_fence_after();
         if (NT == 1 && (warp & 3) == 0 && lane == 0) {  // S_g and P V of tile g - 1 have finished
@@ -449,7 +626,7 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
           if (x > 0) mbar_arrive_cta(&kv_empty[(2 * g - 1) % NS]);
         }
         const int k0 = (c.kt + x) * KT;
-        if (k0 + KT > c.limit) {
+        if (!F && k0 + KT > c.limit) {
           // values behind the last key are whatever the page held: cleared (0 * NaN is NaN), by both
           // streams alike, each before its own products
           wait(&kv_full[(2 * g + 1) % NS], (2 * g + 1) / NS);
@@ -498,6 +675,14 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
             tmem_st16(to + d, o);
+            if constexpr (F) {
+              tmem_ld16(to + (kO2 - kO) + d, o);
+              tmem_ld_wait();
+              tmem_regs_ready(o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st16(to + (kO2 - kO) + d, o);
+            }
           }
         }
         m = mn;
@@ -530,19 +715,23 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 16; ++e) split3(p[e].x, p[e].y, ph[e], pm[e], pl[e]);
             tmem_st16(ts + 16 * i, ph);
-            tmem_st16(ts + 64 + 16 * i, pm);
-            tmem_st16(tb + kTmemX + 64 * buf + lrow + 16 * i, pl);
+            tmem_st16(ts + KT / 2 + 16 * i, pm);
+            tmem_st16(tb + kX<F> + KT / 2 * buf + lrow + 16 * i, pl);
           }
         }
         l = l * alpha + ((ps[0].x + ps[0].y) + (ps[1].x + ps[1].y));
         // every phase of o_full is waited for before the next can end: a parity skipped could be
         // taken for the one before it
         if (NT == 3 && x > 0) {
-          wait(&o_full[0], g - 1);
-          if (take) {
+          auto ready = [&] {
+            wait(&o_full[0], g - 1);
             tc_fence_after();
-            add_record(rec, to, x == kFlush, paged_exp2(rec_m - (m_old == -INFINITY ? 0.f : m_old)));
+          };
+          if (take) {
+            add_record<HD, F>(rec, to, x == kFlush, paged_exp2(rec_m - (m_old == -INFINITY ? 0.f : m_old)), ready);
             rec_m = m_old;
+          } else {
+            ready();
           }
         }
         tmem_st_wait();
@@ -596,6 +785,17 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
           tmem_ld_wait();
           tmem_regs_ready(o[0]);
           tmem_regs_ready(o[1]);
+          if constexpr (F) {
+            uint32_t o2[2][16];
+            tmem_ld16(to + (kO2 - kO) + d, o2[0]);
+            tmem_ld16(to + (kO2 - kO) + d + 16, o2[1]);
+            tmem_ld_wait();
+            tmem_regs_ready(o2[0]);
+            tmem_regs_ready(o2[1]);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              o[e >> 4][e & 15] = __float_as_uint(__uint_as_float(o[e >> 4][e & 15]) + __uint_as_float(o2[e >> 4][e & 15]));
+          }
           if (NT == 3 && n > kFlush) {  // and the record of the tiles before
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
@@ -623,7 +823,7 @@ __global__ void __launch_bounds__(TcLayout<HD, NT>::kThreads, 1)
               x.x = fmaf(fb, y.x, x.x), x.y = fmaf(fb, y.y, x.y);
               x.z = fmaf(fb, y.z, x.z), x.w = fmaf(fb, y.w, x.w);
             }
-            if (!raw && NT == 1)
+            if (!raw && (NT == 1 || (F && a.act_bf16)))
               *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
                   make_uint2(paged_pack(x.x, x.y), paged_pack(x.z, x.w));
             else
@@ -665,37 +865,40 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
   paged_emit<true>(a, HD, sp.token + r / a.gq, sp.head + r % a.gq, d, acc);
 }
 
-template <int HD, int NT>
+template <int HD, int NT, bool F>
 cudaError_t launch_tc(const PagedAttnArgs& a, int grid, cudaStream_t s) {
-  CUtensorMap tk, tv;
+  using LY = TcLayout<HD, NT, F>;
+  CUtensorMap tk{}, tv{};
   const uint64_t rows = (uint64_t)a.c.n_pages * a.c.nkv << a.c.page_shift;
-  const uint32_t box = std::min(KT, 1 << a.c.page_shift);
-  if (!make_tmap_bf16_2d(&tk, a.c.k_pages, rows, HD, box) ||
-      !make_tmap_bf16_2d(&tv, a.c.v_pages, rows, HD, box))
+  const uint32_t box = std::min(LY::KT, 1 << a.c.page_shift);
+  if (!F && (!make_tmap_bf16_2d(&tk, a.c.k_pages, rows, HD, box) ||
+             !make_tmap_bf16_2d(&tv, a.c.v_pages, rows, HD, box)))
     return cudaErrorInvalidValue;
-  cudaError_t e = launch_pdl(paged_attn_tc_kernel<HD, NT>, dim3(grid), TcLayout<HD, NT>::kThreads,
-                             TcLayout<HD, NT>::bytes, s, a, tk, tv);
-  if (e == cudaSuccess && !a.prefix_pass) e = launch_paged_join(a, HD, grid, paged_tc_rows(NT == 1), s);
+  cudaError_t e = launch_pdl(paged_attn_tc_kernel<HD, NT, F>, dim3(grid), LY::kThreads, LY::bytes, s, a, tk, tv);
+  if (e == cudaSuccess && !a.prefix_pass) e = launch_paged_join(a, HD, grid, 128 * LY::kStreams, s);
   return e;
 }
 template <int HD>
+cudaError_t launch_hd(const PagedAttnArgs& a, int grid, cudaStream_t s) {
+  if (!a.c.kv_bf16) return launch_tc<HD, 3, true>(a, grid, s);
+  return a.act_bf16 ? launch_tc<HD, 1, false>(a, grid, s) : launch_tc<HD, 3, false>(a, grid, s);
+}
+template <int HD, int NT, bool F>
+cudaError_t allow_smem() {
+  return cudaFuncSetAttribute(paged_attn_tc_kernel<HD, NT, F>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)TcLayout<HD, NT, F>::bytes);
+}
+template <int HD>
 cudaError_t set_attributes_hd() {
-  cudaError_t e = cudaFuncSetAttribute(paged_attn_tc_kernel<HD, 1>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)TcLayout<HD, 1>::bytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(paged_attn_tc_kernel<HD, 3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)TcLayout<HD, 3>::bytes);
-  return e;
+  cudaError_t e = allow_smem<HD, 1, false>();
+  if (e == cudaSuccess) e = allow_smem<HD, 3, false>();
+  return e == cudaSuccess ? allow_smem<HD, 3, true>() : e;
 }
 
 }  // namespace
 
-int paged_tc_rows(bool act_bf16) { return act_bf16 ? 256 : 128; }
-
 cudaError_t launch_paged_tc(const PagedAttnArgs& a, int hd, int grid, cudaStream_t s) {
-  if (hd == 64) return a.act_bf16 ? launch_tc<64, 1>(a, grid, s) : launch_tc<64, 3>(a, grid, s);
-  return a.act_bf16 ? launch_tc<128, 1>(a, grid, s) : launch_tc<128, 3>(a, grid, s);
+  return hd == 64 ? launch_hd<64>(a, grid, s) : launch_hd<128>(a, grid, s);
 }
 
 cudaError_t launch_paged_join(const PagedAttnArgs& a, int hd, int grid, int item_rows, cudaStream_t s) {

@@ -216,15 +216,20 @@ __device__ __forceinline__ PagedCursor paged_cursor(const PagedAttnArgs& a, cons
 
 // Page of key tile row `key` of the cursor's item; a page id outside the pool is reported and read
 // as page 0, so that no read leaves the pool.
-__device__ __forceinline__ int paged_page(const PagedAttnArgs& a, int b, int key) {
+__device__ __forceinline__ int paged_page_entry(const PagedAttnArgs& a, int b, int key) {
   const int at = key >> a.c.page_shift;
-  int pg = a.prefix_pass ? __ldg(a.c.prefix_pages + at)
-                         : __ldg(a.c.page_table + (size_t)b * a.c.max_pages + at);
+  return a.prefix_pass ? __ldg(a.c.prefix_pages + at)
+                       : __ldg(a.c.page_table + (size_t)b * a.c.max_pages + at);
+}
+__device__ __forceinline__ int paged_page_checked(const PagedAttnArgs& a, int pg) {
   if ((unsigned)pg >= (unsigned)a.c.n_pages) {
     if (a.c.status) atomicOr(a.c.status, PG_BAD_PAGE);
     pg = 0;
   }
   return pg;
+}
+__device__ __forceinline__ int paged_page(const PagedAttnArgs& a, int b, int key) {
+  return paged_page_checked(a, paged_page_entry(a, b, key));
 }
 // First row (of hd elements) in the pool of key `key` under KV head kvh.
 __device__ __forceinline__ long long paged_row(const PagedAttnArgs& a, int page, int kvh, int key) {

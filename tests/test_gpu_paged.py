@@ -205,6 +205,38 @@ def test_f32_results_at_long_prefixes(kv, prefix, tokens):
     c.check()
 
 
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("nq,nkv,hd,page,prefix", [
+    (8, 2, 64, 16, 0), (16, 2, 128, 64, 130), (5, 1, 128, 32, 0), (7, 1, 64, 256, 65), (3, 3, 128, 128, 1100)])
+def test_f32_pages_of_wide_tables(act, nq, nkv, hd, page, prefix):
+    # the longest sequence that the table could hold decides the kernel: tiles of 128 rows here, with
+    # ends inside tiles, diagonals, a sequence without tokens and items split over several CTAs
+    b = Batch([(150, 10), (129, 0), (1, 700), (64, 200), (0, 30), (2, 127), (40, 1100)], nq, nkv, hd, page,
+              act, "f32", prefix=prefix, pad=2, seed=97, extra_cols=32768 // page)
+    c = b.cache()
+    out = torch.full((b.rows, nq, hd), 7.0, dtype=DT[act], device="cuda")
+    got = c.attend(b.q.cuda(), max_new=150, out=out)
+    attend_close(b, got)
+    assert (got[b.tokens:] == 7.0).all()
+    for _ in range(2):
+        assert torch.equal(c.attend(b.q.cuda(), max_new=150)[:b.tokens], got[:b.tokens])
+    c.check()
+
+
+def test_f32_pages_of_wide_tables_bad_entries():
+    # a page outside the pool is read as page 0, tokens before the first key get zeros, both reported
+    b = Batch([(150, 300), (100, 0)], 8, 2, 64, 16, "f32", "f32", seed=101, extra_cols=2048)
+    b.table[0, 3] = b.n_pages
+    b.table[0, 5] = -1
+    b.k[0] = b.v[0] = 0.5
+    b.len[1] = 30
+    c = b.cache()
+    got = c.attend(b.q.cuda(), max_new=150)[:b.tokens]
+    assert torch.isfinite(got).all() and (got[150:220] == 0).all() and (got[220:] != 0).any(-1).all()
+    with pytest.raises(RuntimeError, match="BAD_PAGE.*BAD_LENGTH|BAD_LENGTH.*BAD_PAGE"):
+        c.check()
+
+
 def test_padding_rows_are_left_and_strides():
     for act, kv in TYPES:
         b = Batch([(2, 9), (1, 40)], 4, 2, 64, 16, act, kv, pad=3, seed=13)
