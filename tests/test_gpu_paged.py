@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 import torch
 
-from paged_ref import DT, HALF, Batch
+from paged_ref import DT, HALF, U, Batch
 
 pytestmark = pytest.mark.gpu
 
@@ -220,6 +220,44 @@ def test_f32_pages_of_wide_tables(act, nq, nkv, hd, page, prefix):
     assert (got[b.tokens:] == 7.0).all()
     for _ in range(2):
         assert torch.equal(c.attend(b.q.cuda(), max_new=150)[:b.tokens], got[:b.tokens])
+    c.check()
+
+
+@pytest.mark.parametrize("act,kv,nq", [("bf16", "bf16", 32), ("f32", "bf16", 32), ("f32", "f32", 16), ("f32", "f32", 64),
+                                       ("bf16", "f32", 32)])
+@pytest.mark.parametrize("prefix", [0, 1386])
+def test_every_tile_is_read_before_its_stage_is_filled_again(act, kv, nq, prefix):
+    """Keys of zero weigh all rows alike, and a value row is the unit vector of its 32-key block (mod
+    128): column d of the output counts the keys of such blocks, exactly in f32. Over and over, since a
+    copy that overtakes a read is rare."""
+    from sequence_decode_step_gb300 import PagedKV
+    nkv, hd, page, n = 8, 128, 64, 161
+    r = np.random.RandomState(3)
+    lens = r.randint(1, 4096, size=n)
+    pages = -(-lens // page)
+    total, npre = int(pages.sum()), -(-prefix // page)
+    perm, table, at = r.permutation(total), np.zeros((n, int(pages.max())), np.int32), 0
+    block = np.zeros((total, page), np.int64)
+    for b in range(n):
+        ids = perm[at:at + pages[b]]
+        table[b, :pages[b]] = ids
+        at += pages[b]
+        block[ids] = np.arange(pages[b] * page).reshape(-1, page) // 32
+    k = torch.zeros(total + npre + 1, nkv, page, hd, device="cuda", dtype=DT[kv])
+    v = torch.zeros_like(k)
+    v[:total] = torch.nn.functional.one_hot(torch.from_numpy(block).cuda() % 128, 128).to(DT[kv])[:, None]
+    i32 = {"device": "cuda", "dtype": torch.int32}
+    c = PagedKV(k, v, torch.from_numpy(table).cuda(), torch.from_numpy(lens.astype(np.int32)).cuda(),
+                torch.arange(n + 1, **i32), prefix_len=prefix,
+                prefix_pages=torch.arange(total, total + npre, **i32) if prefix else None)
+    q = torch.randn(n, nq, hd, device="cuda").to(DT[act])
+    length = torch.from_numpy(lens).cuda()
+    count = (length[:, None] - 32 * torch.arange(128, device="cuda")[None]).clamp(0, 32).double()
+    want = (count / (length[:, None] + prefix))[:, None]
+    for _ in range(25):
+        # products of 0 and 1 and their sums are exact; a reciprocal, a product and the output's rounding
+        # follow, and one key more or less changes a count by 1/32 of it at least
+        assert ((c.attend(q).double() - want).abs() <= want * (HALF[act] + 4 * U)).all()
     c.check()
 
 
