@@ -108,7 +108,7 @@ struct TcLayout {
   static constexpr uint32_t off_ring = kQ;
   static constexpr uint32_t off_start = off_ring + kSlots * kTile;
   static constexpr uint32_t off_bar = off_start + 96 + 128;
-  static constexpr int kBars = 2 * kSlots + 10;
+  static constexpr int kBars = 2 * kSlots + 11;
   static constexpr uint32_t off_tmem = off_bar + kBars * 8;
   static constexpr uint32_t bytes = off_tmem + 16;
   static constexpr uint32_t t_s = F ? 64 : 128;            // TMEM columns between S buffers or streams
@@ -202,12 +202,12 @@ __global__ void __launch_bounds__(TcLayout<HD, NT, F>::kThreads, 1)
     paged_attn_tc_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ CUtensorMap tk,
                          const __grid_constant__ CUtensorMap tv) {
   using LY = TcLayout<HD, NT, F>;
-  constexpr int KT = LY::KT, NS = LY::kSlots, ST = LY::kStreams, QA = HD / 64, kFlush = LY::kFlush;
+  constexpr int KT = LY::KT, NS = LY::kSlots, QA = HD / 64, kFlush = LY::kFlush;
   extern __shared__ __align__(1024) uint8_t sm[];
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(sm + LY::off_bar);
   uint64_t* kv_empty = kv_full + NS;
   uint64_t* q_full = kv_empty + NS;
-  uint64_t* s_full = q_full + 1;   // NT = 1: of each stream; NT = 3: of each S buffer
+  uint64_t* s_full = q_full + 2;   // NT = 1: of each stream; NT = 3: of each S buffer
   uint64_t* p_full = s_full + 2;   // NT = 1: of each stream; NT = 3: p_full[0]
   uint64_t* p_half = p_full + 2;   // NT = 1: the first 64 keys' weights of each stream
   uint64_t* o_full = p_half + 2;   // NT = 1: the end of an item, of each stream; NT = 3: every tile
@@ -221,8 +221,8 @@ __global__ void __launch_bounds__(TcLayout<HD, NT, F>::kThreads, 1)
       mbar_init(&kv_full[i], F ? 8 : 1);          // the converting warps, or the tensor copies
       mbar_init(&kv_empty[i], NT == 1 ? 2 : 1);  // the streams' softmax warps, or a commit
     }
-    mbar_init(q_full, 4 * ST);  // one arrival per softmax warp
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 4);  // one arrival per softmax warp
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
       mbar_init(&p_half[i], 4);
@@ -405,6 +405,7 @@ __global__ void __launch_bounds__(TcLayout<HD, NT, F>::kThreads, 1)
     PagedCursor c = paged_cursor<KT>(a, st);
     int items = 0, tiles = 0;  // of this CTA so far; tile g uses slots 2g (K), 2g + 1 (V)
     int turns[2] = {0, 0};     // tiles of each stream (NT = 1)
+    int pairs = 0;             // items with two streams
     auto wait = [&](uint64_t* bar, int n) {
       return __all_sync(0xffffffffu, wait_for(bar, n, a.wait_ns)) != 0;
     };
@@ -414,7 +415,7 @@ __global__ void __launch_bounds__(TcLayout<HD, NT, F>::kThreads, 1)
       const int n = __shfl_sync(0xffffffffu, c.kend - c.kt, 0);
       const int streams =  // the second stream may have no rows in this item
           __shfl_sync(0xffffffffu, NT == 1 && c.s.nb - c.rt * a.tpt > half ? 2 : 1, 0);
-      ok = wait(q_full, items) && kv_wait(2 * tiles);
+      ok = wait(&q_full[0], items) && (streams == 1 || wait(&q_full[1], pairs++)) && kv_wait(2 * tiles);
       if (!ok) break;
       tc_fence_after();
       if constexpr (NT == 1) {
@@ -612,7 +613,7 @@ __global__ void __launch_bounds__(TcLayout<HD, NT, F>::kThreads, 1)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cta(q_full);
+        if (lane == 0 && rows > 0) mbar_arrive_cta(&q_full[s]);  // (without rows it may run items ahead)
       }
       float m = -INFINITY, l = 0.f, rec_m = -INFINITY;
       const uint32_t to = tb + kO + 128 * s + lrow;

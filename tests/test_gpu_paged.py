@@ -223,6 +223,20 @@ def test_f32_pages_of_wide_tables(act, nq, nkv, hd, page, prefix):
     c.check()
 
 
+@pytest.mark.parametrize("act,kv", TYPES)
+def test_many_short_chunks_in_wide_tables(act, kv):
+    # several items per CTA, most of which fill one row tile of two: the other one's warps run ahead
+    b = Batch([(1 + 13 * i % 41, 0) for i in range(60)] + [(150, 3)], 16, 8, 64, 64, act, kv, seed=103,
+              extra_cols=512)
+    c = b.cache()
+    q = b.q.cuda()
+    got = c.attend(q, max_new=150)
+    attend_close(b, got)
+    for _ in range(20):
+        assert torch.equal(c.attend(q, max_new=150), got)
+    c.check()
+
+
 @pytest.mark.parametrize("act,kv,nq", [("bf16", "bf16", 32), ("f32", "bf16", 32), ("f32", "f32", 16), ("f32", "f32", 64),
                                        ("bf16", "f32", 32)])
 @pytest.mark.parametrize("prefix", [0, 1386])
