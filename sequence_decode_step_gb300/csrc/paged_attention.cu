@@ -1207,11 +1207,11 @@ int slot_rows(int n_tokens) {
 }
 struct Workspace {
   size_t counters = 0, splits[2], flush, ml[2], o[2], whole_ml, whole_o, total;
+  size_t rows;  // of a launch's slots
   Workspace(int n_tokens, int nq, int hd, bool prefix) {
-    // an item of more than 32 rows belongs to one CTA per SM, of more than 8 to two, smaller ones to three
-    const int most = slot_rows(n_tokens);
-    const size_t rows =
-        (size_t)2 * std::max({kMaxSms * most, 2 * kMaxSms * std::min(32, most), 3 * kMaxSms * 8});
+    // tensor-core tiles have one CTA per SM, tiles of 32 rows (from 9 rows on: two tokens) two, smaller three
+    rows = (size_t)2 * std::max({kMaxSms * slot_rows(n_tokens),
+                                 2 * kMaxSms * (n_tokens > 1 ? 32 : 8), 3 * kMaxSms * 8});
     splits[0] = align256(kMaxCtas * 4);
     splits[1] = splits[0] + align256(kMaxCtas * sizeof(PagedSplit));
     flush = splits[1] + align256(kMaxCtas * sizeof(PagedSplit));
@@ -1291,6 +1291,7 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& base, int hd, int max_ne
     a.slots.ml = reinterpret_cast<float2*>(ws + w.ml[i]);
     a.slots.o = reinterpret_cast<float*>(ws + w.o[i]);
     a.slots.rows = p.tc ? slot_rows(a.n_tokens) : p.rows;
+    if ((size_t)2 * p.grid * a.slots.rows > w.rows || p.grid > kMaxCtas) return cudaErrorInvalidValue;
     return hd == 64 ? launch_pass<64>(a, p, s) : launch_pass<128>(a, p, s);
   };
   // the line of a launch is counted in 32 bits

@@ -224,6 +224,17 @@ def test_f32_pages_of_wide_tables(act, nq, nkv, hd, page, prefix):
 
 
 @pytest.mark.parametrize("act,kv", TYPES)
+@pytest.mark.parametrize("nq,nkv,hd", [(14, 2, 64), (16, 2, 128)])
+def test_two_tokens_over_many_keys(act, kv, nq, nkv, hd):
+    # 14 and 16 rows per key, split over all CTAs: the most records that the smallest workspace holds
+    for seqs, prefix in (([(1, 20), (1, 300)], 9001), ([(2, 9000)], 0)):
+        b = Batch(seqs, nq, nkv, hd, 64, act, kv, prefix=prefix, seed=107)
+        c = b.cache()
+        attend_close(b, c.attend(b.q.cuda(), max_new=2))
+        c.check()
+
+
+@pytest.mark.parametrize("act,kv", TYPES)
 def test_many_short_chunks_in_wide_tables(act, kv):
     # several items per CTA, most of which fill one row tile of two: the other one's warps run ahead
     b = Batch([(1 + 13 * i % 41, 0) for i in range(60)] + [(150, 3)], 16, 8, 64, 64, act, kv, seed=103,
