@@ -447,7 +447,8 @@ typedef struct qw_paged_kv {
   int32_t n_kv_heads;
   int32_t head_dim;            /* 64 or 128 */
   int32_t n_seqs;
-  int32_t max_pages;           /* columns of page_table */
+  int32_t max_pages;           /* columns of page_table; prefix_len + max_pages * page_size
+                                  < 2^31 - 512 */
   int32_t prefix_len;          /* keys of the shared prefix, 0 for none */
   uint32_t reserved0;
   void* k_pages;               /* [n_pages, n_kv_heads, page_size, head_dim], 16-byte aligned */

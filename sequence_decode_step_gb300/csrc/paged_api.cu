@@ -29,6 +29,9 @@ const char* check_cache(const qw_paged_kv* c, int* shift) {
   if (((int64_t)c->n_pages * c->n_kv_heads << sh) > INT32_MAX)
     return "n_pages * n_kv_heads * page_size must be below 2^31";
   if (c->prefix_len < 0) return "prefix_len must not be negative";
+  // (places of keys, rounded up to a tile, are counted in 32 bits)
+  if (c->prefix_len + ((int64_t)c->max_pages << sh) > INT32_MAX - 512)
+    return "prefix_len + max_pages * page_size must be below 2^31 - 512";
   if (!c->k_pages || !c->v_pages || !c->page_table || !c->kv_len || !c->q_start)
     return "null buffer";
   if (c->prefix_len > 0 && !c->prefix_pages) return "prefix_len without prefix_pages";

@@ -54,6 +54,13 @@ def test_bad_caches(L, bad):
     assert B.last_error()
 
 
+@pytest.mark.parametrize("bad", [dict(max_pages=1 << 27), dict(max_pages=(1 << 27) - 31),
+                                 dict(max_pages=1 << 26, prefix_len=(1 << 30) - 511, prefix_pages=16)])
+def test_places_beyond_32_bits(L, bad):
+    assert append(L, cache(**bad)) == B.QW_ERR_ARG and "2^31" in B.last_error()
+    assert attend(L, cache(**bad)) == B.QW_ERR_ARG and "2^31" in B.last_error()
+
+
 def test_short_struct(L):
     c = cache(struct_size=C.sizeof(B.qw_paged_kv) - 8)
     assert append(L, c) == B.QW_ERR_ABI and attend(L, c) == B.QW_ERR_ABI
