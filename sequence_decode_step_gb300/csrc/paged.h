@@ -74,7 +74,7 @@ struct PagedPrefix {
   float* o;      // [n_tokens][nq][hd], nullptr without a prefix
   float2* ml;    // [n_tokens][nq]
   PagedSlots slots;
-  int tpt, kt, grid, item_units;  // of the prefix launch
+  int tpt, kt, grid, item_units, least_units;  // of the prefix launch
 };
 struct PagedSplit {    // a split item of a CTA, for the kernel that joins its records
   int c1;              // last CTA, -1: this CTA begins no split item
@@ -89,6 +89,7 @@ struct PagedAttnArgs {
   int act_bf16;
   int tpt;                  // tokens per row tile
   int item_units;           // tiles that an item costs beside its keys
+  int least_units;          // least share of a CTA: fewer records of a short line to join
   float scale_log2;         // log2(e) / sqrt(hd)
   PagedSlots slots;         // of this launch
   int* counters;            // [grid] arrivals of split items, 0 between launches
@@ -102,7 +103,7 @@ struct PagedAttnArgs {
 // row counts.
 struct PagedPlan {
   bool tc;                  // paged_attention_tc.cu, else paged_attention.cu
-  int kt, rows, grid, item_units;
+  int kt, rows, grid, item_units, least_units;
 };
 size_t paged_attn_workspace_bytes(int n_tokens, int nq, int hd, bool prefix);
 cudaError_t launch_paged_attention(const PagedAttnArgs& base, int hd, int max_new, void* workspace,

@@ -1248,29 +1248,34 @@ constexpr int kDecodeItemUnits = 5;
 // `rows` query rows (tokens x heads of a KV head) that meet up to `keys` keys.
 //
 // bf16 pages: few rows run the mma.sync kernel; more than 16 the tensor-core tiles, unless there is so
-// little of it that their start (about 16 us with q, first product and output against 4) is most of the
-// time. Measured per tile and CTA: 1.5 us for 64 keys here, and for 128 keys there 1.5 us (bf16) or 2.9 us
-// (f32 in three terms): a 4K prefix of 128 rows takes 22 us against 34, a 2-key one 16 against 6.
+// little of it that their start (3 to 5.5 us more, with q, first product and output) is most of the time.
+// Measured per tile and CTA: 1.3 us for 64 keys here, and for 128 keys there 1.5 us (bf16) or 2.9 us (f32 in
+// three terms). Calls with 4K prefix keys: 32 rows 20.6 us against 22.5 there, 64 rows 27.4 against 22.9 (f32
+// 30.8 and 27.6), 128 rows 44 against 28.7; one chunk of 64 tokens behind 2K keys 26.7 against 21, 512 keys 16.8
+// against 20.5. An item of tensor-core tiles costs about 7 us beside them; a share of 2 instead of 4 tiles at
+// least lets a 4K prefix of 128 rows use all SMs (36.8 us instead of 40.8 with f32 q).
 // f32 pages: the least tile that holds the rows: 2 or 4 with FMAs, 8 or 32 with mma.sync. More than 16
 // rows by the same estimate: 3.3 us for 32 rows x 32 keys on mma.sync, 2.5 us for 128 rows x 64 keys on the
 // tensor-core tiles, whose start takes 2 us more. Measured, with a key of each sequence's own: a prefix of
-// 1K keys and 32 rows 23 us against 27, 256 rows 49 against 37; of 16K keys 66 against 56 and 381 against 103.
+// 1K keys and 32 rows 20 us against 27, 256 rows 49 against 37; of 16K keys 66 against 56 and 381 against 103.
 PagedPlan plan_paged_pass(const PagedAttnArgs& a, long long rows, long long keys, int sms) {
   sms = std::min(sms, kMaxSms);
   const bool f32 = !a.c.kv_bf16;
-  PagedPlan p{false, f32 ? 32 : 64, 8, 3 * sms, kDecodeItemUnits};
+  PagedPlan p{false, f32 ? 32 : 64, 8, 3 * sms, kDecodeItemUnits, 4};
   if (f32) {
     p.rows = rows <= 2 ? 2 : rows <= 4 ? 4 : rows <= 8 ? 8 : 32;
     if (p.rows > 4) p.grid = 2 * sms;
+    if (p.rows > 8) p.least_units = 2;  // (a tile takes 3.3 us: 32 rows x 1K keys 22.5 -> 19.7 us)
   }
   if (rows > 16) {
     auto us = [&](double start, double tile, int kt, int item_rows, int units, int grid) {
       const double items = (double)a.c.nkv * ((rows + item_rows - 1) / item_rows);
       return start + tile * std::ceil(items * (keys / kt + 1 + units) / grid);
     };
-    const PagedPlan t{true, paged_tc_keys(!f32), paged_tc_rows(a.act_bf16, !f32), sms, 5};
-    if (us(f32 ? 6 : 16, f32 ? 2.5 : a.act_bf16 ? 1.5 : 2.9, t.kt, t.rows, t.item_units, t.grid) <
-        us(4, f32 ? 3.3 : 1.5, p.kt, p.rows, p.item_units, p.grid))
+    const PagedPlan t{true, paged_tc_keys(!f32), paged_tc_rows(a.act_bf16, !f32), sms,
+                      f32 ? 4 : a.act_bf16 ? 5 : 3, 2};
+    if (us(f32 ? 6 : a.act_bf16 ? 9.5 : 7, f32 ? 2.5 : a.act_bf16 ? 1.5 : 2.9, t.kt, t.rows, t.item_units, t.grid) <
+        us(4, f32 ? 3.3 : 1.3, p.kt, p.rows, p.item_units, p.grid))
       p = t;
   }
   return p;
@@ -1286,6 +1291,7 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& base, int hd, int max_ne
   a.flush = reinterpret_cast<float*>(ws + w.flush);
   auto run = [&](const PagedPlan& p, int i) {
     a.item_units = p.item_units;
+    a.least_units = p.least_units;
     a.tpt = p.rows > 128 ? 2 * (128 / a.gq) : p.rows / a.gq;
     a.splits = reinterpret_cast<PagedSplit*>(ws + w.splits[i]);
     a.slots.ml = reinterpret_cast<float2*>(ws + w.ml[i]);
@@ -1318,6 +1324,7 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& base, int hd, int max_ne
     a.pre.kt = p.kt;
     a.pre.grid = p.grid;
     a.pre.item_units = p.item_units;
+    a.pre.least_units = p.least_units;
   }
   return run(own, 0);
 }

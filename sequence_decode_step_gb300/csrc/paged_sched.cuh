@@ -22,8 +22,6 @@
 
 namespace qw {
 
-constexpr int kPagedLeastUnits = 4;  // least share of a CTA: fewer records of a short line to join
-
 // Units are counted in 32 bits (the host refuses calls whose line could be longer). The code of
 // these kernels is kept short on purpose: a decode step's weights sweep the instructions out of the
 // caches between two calls, and a cold line of 128 bytes costs 0.2 us from L2 and 0.7 us from HBM,
@@ -191,7 +189,7 @@ __device__ __forceinline__ void paged_find_start(const PagedAttnArgs& a, PagedSt
       if (w < warp) before += warp_sums[w];
       total += warp_sums[w];
     }
-    per = max((total + (int)gridDim.x - 1) / (int)gridDim.x, kPagedLeastUnits);
+    per = max((total + (int)gridDim.x - 1) / (int)gridDim.x, a.least_units);
     r = per * (int)blockIdx.x - before;
     if (per * (int)blockIdx.x >= total || r < 0 || r >= mine) break;
   }
@@ -314,7 +312,7 @@ __device__ __forceinline__ PagedShare paged_prefix_share(const PagedAttnArgs& a,
   const int lo = min(max(__ldg(a.c.q_start), 0), end);
   const int nrt = (end - lo + p.tpt - 1) / p.tpt, nkt = (a.c.prefix_len + p.kt - 1) / p.kt;
   const int rt = (token - lo) / p.tpt, units = p.item_units + nkt;
-  const int per = max((a.c.nkv * nrt * units + p.grid - 1) / p.grid, kPagedLeastUnits);
+  const int per = max((a.c.nkv * nrt * units + p.grid - 1) / p.grid, p.least_units);
   const int first = (kvh * nrt + rt) * units + p.item_units;
   return PagedShare{first / per, (first + nkt - 1) / per, (token - lo - rt * p.tpt) * a.gq + head_in_group};
 }
