@@ -93,7 +93,7 @@ struct PagedAttnArgs {
   float scale_log2;         // log2(e) / sqrt(hd)
   PagedSlots slots;         // of this launch
   int* counters;            // [grid] arrivals of split items, 0 between launches
-  float* flush;             // [grid][128][128] (f32 activations on tensor-core tiles)
+  float* flush;             // [grid][128][128] of this launch (f32 sums on tensor-core tiles)
   PagedSplit* splits;       // [grid], for the joining kernel (prefix and tensor-core launches)
   int prefix_pass;          // 1: this launch reads the prefix's keys
   PagedPrefix pre;

@@ -1195,9 +1195,9 @@ cudaError_t set_attributes_hd() {
   return e;
 }
 
-// Workspace of a call: counters and split descriptors, the slots of the two launches, the
-// prefix's whole records. A slot holds as many rows as an item can have: at most kMaxRows and at
-// most 8 query heads of every token.
+// Workspace of a call: counters (of the launch over own keys), then split descriptors, O records and
+// slots, a copy for each of the two launches, which may overlap; the prefix's whole records. A slot
+// holds as many rows as an item can have: at most kMaxRows and at most 8 query heads of every token.
 constexpr int kMaxSms = 192;
 constexpr int kMaxCtas = 3 * kMaxSms;  // of a launch
 constexpr int kMaxRows = 256;
@@ -1206,7 +1206,7 @@ int slot_rows(int n_tokens) {
   return std::max(16, (int)std::min<long long>(kMaxRows, (8LL * n_tokens + 15) / 16 * 16));
 }
 struct Workspace {
-  size_t counters = 0, splits[2], flush, ml[2], o[2], whole_ml, whole_o, total;
+  size_t counters = 0, splits[2], flush[2], ml[2], o[2], whole_ml, whole_o, total;
   size_t rows;  // of a launch's slots
   Workspace(int n_tokens, int nq, int hd, bool prefix) {
     // tensor-core tiles have one CTA per SM, tiles of 32 rows (from 9 rows on: two tokens) two, smaller three
@@ -1214,12 +1214,12 @@ struct Workspace {
                                  2 * kMaxSms * (n_tokens > 1 ? 32 : 8), 3 * kMaxSms * 8});
     splits[0] = align256(kMaxCtas * 4);
     splits[1] = splits[0] + align256(kMaxCtas * sizeof(PagedSplit));
-    flush = splits[1] + align256(kMaxCtas * sizeof(PagedSplit));
-    // (tensor-core tiles have more than 16 rows: three tokens at least)
-    size_t at = flush + (n_tokens > 2 ? (size_t)kMaxSms * 128 * 128 * 4 : 0);
+    size_t at = splits[1] + align256(kMaxCtas * sizeof(PagedSplit));
     for (int i = 0; i < (prefix ? 2 : 1); ++i) {
-      ml[i] = at;
-      o[i] = at + align256(rows * 8);
+      flush[i] = at;
+      // (tensor-core tiles have more than 16 rows: three tokens at least)
+      ml[i] = at + (n_tokens > 2 ? (size_t)kMaxSms * 128 * 128 * 4 : 0);
+      o[i] = ml[i] + align256(rows * 8);
       at = o[i] + align256(rows * hd * 4);
     }
     whole_ml = at;
@@ -1288,12 +1288,12 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& base, int hd, int max_ne
   const Workspace w(a.n_tokens, a.nq, hd, prefix);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.counters = reinterpret_cast<int*>(ws);
-  a.flush = reinterpret_cast<float*>(ws + w.flush);
   auto run = [&](const PagedPlan& p, int i) {
     a.item_units = p.item_units;
     a.least_units = p.least_units;
     a.tpt = p.rows > 128 ? 2 * (128 / a.gq) : p.rows / a.gq;
     a.splits = reinterpret_cast<PagedSplit*>(ws + w.splits[i]);
+    a.flush = reinterpret_cast<float*>(ws + w.flush[i]);
     a.slots.ml = reinterpret_cast<float2*>(ws + w.ml[i]);
     a.slots.o = reinterpret_cast<float*>(ws + w.o[i]);
     a.slots.rows = p.tc ? slot_rows(a.n_tokens) : p.rows;

@@ -30,7 +30,9 @@ namespace qw {
 // Programmatic launches: every kernel here may start while the one before it still runs, and waits
 // for its end (griddepcontrol.wait) before it touches memory. The launch over the sequences' own keys
 // behind a prefix waits only before it reads the prefix's records: the prefix's launch lets it start
-// after its own wait, so everything older is done by then.
+// after its own wait, so everything older is done by then. Until that wait it may run beside the
+// prefix's launch, from which it shares nothing that either writes: split descriptors, slots and O
+// records have a copy per launch, counters belong to it alone, and outputs are written behind the wait.
 __device__ __forceinline__ void paged_pdl_open(const PagedAttnArgs& a) {
   if (a.prefix_pass || !a.pre.o) pdl_wait();
   pdl_launch_dependents();

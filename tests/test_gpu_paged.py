@@ -205,6 +205,52 @@ def test_f32_results_at_long_prefixes(kv, prefix, tokens):
     c.check()
 
 
+@pytest.mark.parametrize("kv,hd", [("bf16", 128), ("f32", 64), ("f32", 128)])
+@pytest.mark.parametrize("new", [(5,), (6, 4)])
+def test_few_tokens_behind_a_long_prefix_beside_other_work(kv, hd, new):
+    """Both launches of a call take tensor-core tiles whose O moves to records, with so few rows that the
+    joining kernel between them starts early; another stream's products make CTAs start late. The second
+    launch may then run beside the first: the same bits every time, and the right ones."""
+    from sequence_decode_step_gb300 import PagedKV
+    nq, nkv, page, prefix, own = 64, 8, 64, 20000, 16500
+    g = torch.Generator(device="cuda").manual_seed(11)
+    npre, per = -(-prefix // page), -(-own // page)
+    k, v = (torch.randn(npre + len(new) * per, nkv, page, hd, generator=g, device="cuda").to(DT[kv])
+            for _ in range(2))
+    i32 = {"device": "cuda", "dtype": torch.int32}
+    n = sum(new)
+    q = torch.randn(n, nq, hd, generator=g, device="cuda") * 1.5
+    table = npre + torch.arange(len(new) * per, **i32).view(len(new), per)
+    lens = [own - 37 * b for b in range(len(new))]
+    c = PagedKV(k, v, table, torch.tensor(lens, **i32), torch.tensor(np.cumsum([0, *new]), **i32),
+                prefix_pages=torch.arange(npre, **i32), prefix_len=prefix)
+    first = c.attend(q, max_new=max(new))
+    t = 0
+    for b, m in enumerate(new):
+        kk, vv = (torch.cat([x[:npre].permute(1, 0, 2, 3).reshape(nkv, -1, hd)[:, :prefix],
+                             x[table[b].long()].permute(1, 0, 2, 3).reshape(nkv, -1, hd)[:, :lens[b]]], 1).double()
+                  for x in (k, v))
+        s = torch.einsum("thgd,hkd->thgk", q[t:t + m].double().view(m, nkv, -1, hd), kk) / math.sqrt(hd)
+        see = torch.arange(kk.shape[1], device="cuda")[None] < (
+            prefix + lens[b] - m + 1 + torch.arange(m, device="cuda")[:, None])
+        p = torch.softmax(s.masked_fill(~see[:, None, None], -math.inf), -1)
+        want = torch.einsum("thgk,hkd->thgd", p, vv).reshape(m, nq, hd)
+        # 48 products of at most 2^-23 each run into one accumulator (5.7e-6 of the values, at most)
+        assert float((first[t:t + m].double() - want).norm() / want.norm()) <= 6e-6
+        t += m
+    side = torch.cuda.Stream()
+    x = torch.randn(1500, 1500, device="cuda")
+    torch.cuda.synchronize()
+    for i in range(30):
+        with torch.cuda.stream(side):
+            for _ in range(1 + i % 4):
+                x @ x
+        got = [c.attend(q, max_new=max(new)) for _ in range(3)]
+        assert all(torch.equal(y, first) for y in got)
+    torch.cuda.synchronize()
+    c.check()
+
+
 @pytest.mark.parametrize("act", ["f32", "bf16"])
 @pytest.mark.parametrize("nq,nkv,hd,page,prefix", [
     (8, 2, 64, 16, 0), (16, 2, 128, 64, 130), (5, 1, 128, 32, 0), (7, 1, 64, 256, 65), (3, 3, 128, 128, 1100)])

@@ -98,3 +98,11 @@ def test_workspace_sizes(L):
     assert 0 < f(0, 4, 64, 0) <= f(64, 16, 128, 0)
     # a prefix adds a record of hd + 2 floats per token and query head
     assert f(64, 16, 128, 1) >= f(64, 16, 128, 0) + 64 * 16 * 130 * 4
+
+
+def test_launches_of_a_call_share_no_scratch(L):
+    # the launch over a prefix and the one over own keys may overlap: each has slots and records of its
+    # own, and only the words per CTA at the front (below 64 KB) are laid out once
+    f = L.qw_paged_attention_workspace_bytes
+    for n in (1, 2, 3, 14, 64):
+        assert f(n, 16, 128, 1) >= 2 * f(n, 16, 128, 0) - (64 << 10)
