@@ -425,6 +425,10 @@ enum { QW_ACT_F32 = 0, QW_ACT_BF16 = 1 };
  * gave up; its outputs are invalid. */
 enum { QW_PAGED_TIMEOUT = 1, QW_PAGED_BAD_PAGE = 2, QW_PAGED_BAD_LENGTH = 4 };
 
+/* qw_paged_kv.wait_limit_us: every wait of attention's kernels gives up at once (to test what
+ * follows: TIMEOUT is reported, the call ends, and its workspace is ready for the next one). */
+#define QW_PAGED_WAIT_NONE 0xffffffffu
+
 /* One layer's pages and the batch that uses them. Set struct_size =
  * sizeof(qw_paged_kv). All pointers are DEVICE addresses on the current device.
  *
@@ -450,7 +454,8 @@ typedef struct qw_paged_kv {
   int32_t max_pages;           /* columns of page_table; prefix_len + max_pages * page_size
                                   < 2^31 - 512 */
   int32_t prefix_len;          /* keys of the shared prefix, 0 for none */
-  uint32_t reserved0;
+  uint32_t wait_limit_us;      /* bound of a device-side wait of attention, in microseconds: 0 for
+                                  one second, QW_PAGED_WAIT_NONE to give up at once */
   void* k_pages;               /* [n_pages, n_kv_heads, page_size, head_dim], 16-byte aligned */
   void* v_pages;               /* the same shape */
   const int32_t* page_table;   /* [n_seqs, max_pages] */

@@ -35,6 +35,7 @@ QW_ACT_BF16 = 1
 QW_PAGED_TIMEOUT = 1
 QW_PAGED_BAD_PAGE = 2
 QW_PAGED_BAD_LENGTH = 4
+QW_PAGED_WAIT_NONE = 0xffffffff
 QW_CAPTURE_EMBEDDING = 0
 QW_CAPTURE_BLOCK0 = 1
 QW_CAPTURE_FINAL_NORM = 2
@@ -82,7 +83,7 @@ class qw_paged_kv(C.Structure):
     _fields_ = [("struct_size", C.c_uint32), ("kv_format", C.c_uint32), ("n_pages", C.c_int32),
                 ("page_size", C.c_int32), ("n_kv_heads", C.c_int32), ("head_dim", C.c_int32),
                 ("n_seqs", C.c_int32), ("max_pages", C.c_int32), ("prefix_len", C.c_int32),
-                ("reserved0", C.c_uint32), ("k_pages", C.c_void_p), ("v_pages", C.c_void_p),
+                ("wait_limit_us", C.c_uint32), ("k_pages", C.c_void_p), ("v_pages", C.c_void_p),
                 ("page_table", C.c_void_p), ("kv_len", C.c_void_p), ("q_start", C.c_void_p),
                 ("prefix_pages", C.c_void_p), ("status", C.c_void_p)]
 

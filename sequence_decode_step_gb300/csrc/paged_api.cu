@@ -192,7 +192,9 @@ extern "C" int qw_paged_attention(const qw_paged_kv* c, const void* q, uint32_t 
   a.gq = n_q_heads / c->n_kv_heads;
   a.act_bf16 = act_format == QW_ACT_BF16;
   a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)hd));
-  a.wait_ns = 1000000000ull;
+  a.wait_ns = c->wait_limit_us == 0                    ? 1000000000ull
+              : c->wait_limit_us == QW_PAGED_WAIT_NONE ? 0ull
+                                                       : 1000ull * c->wait_limit_us;
   e = qw::launch_paged_attention(a, hd, max_new, workspace, sms, (cudaStream_t)stream);
   if (e == cudaErrorInvalidValue)
     return fail(QW_ERR_ARG,

@@ -111,7 +111,9 @@ __device__ __forceinline__ void produce(const PagedAttnArgs& a, const CUtensorMa
       if (more) fetch_q(c);
     }
     if (more) page = page_of(c);
-    if (issued >= NS && !mbar_wait(&empty[stage], (uint32_t)((issued / NS - 1) & 1), a.wait_ns)) {
+    // (the lanes vote: one that gives up alone would miss the barriers of the others)
+    if (issued >= NS &&
+        !__all_sync(0xffffffffu, mbar_wait(&empty[stage], (uint32_t)((issued / NS - 1) & 1), a.wait_ns))) {
       ok = false;
       break;
     }
@@ -129,7 +131,7 @@ __device__ __forceinline__ void produce(const PagedAttnArgs& a, const CUtensorMa
     }
     ++issued;
   }
-  if (!__all_sync(0xffffffffu, ok) && lane == 0 && a.c.status) atomicOr(a.c.status, PG_TIMEOUT);
+  if (!ok && lane == 0 && a.c.status) atomicOr(a.c.status, PG_TIMEOUT);
   // leave only once the copies issued into this CTA's shared memory have landed
   for (int i = max(0, issued - NS); i < issued; ++i)
     mbar_wait(&full[i % NS], (uint32_t)((i / NS) & 1), kDrainNs);
@@ -364,7 +366,10 @@ __global__ void __launch_bounds__(kThreads, 3)
   const uint32_t gmul = 65536u / a.gq + 1;
   PagedCursor c = paged_cursor<KT>(a, st);
   int seen = 0;      // tiles taken from the ring
-  bool bad = false;  // a wait gave up: no more waits, the barriers are still kept
+  // A wait gave up: no more tiles, and their stages are not given back (a stage armed again before its copy
+  // has come would spoil its barrier), so that the producer gives up too; the block's barriers and the
+  // arrivals of split items are still kept.
+  bool bad = false;
   do {
     const int n = c.kend - c.kt;
     const int tok0 = c.rt * a.tpt, rows = min(a.tpt, c.s.nb - tok0) * a.gq;
@@ -425,8 +430,8 @@ __global__ void __launch_bounds__(kThreads, 3)
 
     for (int x = 0; x < n; ++x, ++seen) {
       const int stage = seen % NS;
-      if (!bad)
-        bad = !__all_sync(0xffffffffu, mbar_wait(&full[stage], (uint32_t)((seen / NS) & 1), a.wait_ns));
+      bad = bad || !__all_sync(0xffffffffu, mbar_wait(&full[stage], (uint32_t)((seen / NS) & 1), a.wait_ns));
+      if (bad) break;
       const uint32_t kb = ring + (uint32_t)stage * 2 * LY::kTile, vb = kb + LY::kTile;
       float s[4], s2[4];  // even and odd k-steps; with NT = 3 the first terms' and the others' products
 #pragma unroll
@@ -633,8 +638,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 
     for (int x = 0; x < n; ++x, ++seen) {
       const int stage = seen % NS;
-      if (!bad)
-        bad = !__all_sync(0xffffffffu, mbar_wait(&full[stage], (uint32_t)((seen / NS) & 1), a.wait_ns));
+      bad = bad || !__all_sync(0xffffffffu, mbar_wait(&full[stage], (uint32_t)((seen / NS) & 1), a.wait_ns));
+      if (bad) break;
       const uint8_t* kb = sm + (uint32_t)stage * 2 * LY::kTile;
       const uint8_t* vb = kb + LY::kTile;
       // products of weight 1, 2^-8 and 2^-16 apart: six chains of mma with the two key groups
@@ -849,8 +854,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 
     for (int x = 0; x < n; ++x, ++seen) {
       const int stage = seen % NS;
-      if (!bad)
-        bad = !__all_sync(0xffffffffu, mbar_wait(&full[stage], (uint32_t)((seen / NS) & 1), a.wait_ns));
+      bad = bad || !__all_sync(0xffffffffu, mbar_wait(&full[stage], (uint32_t)((seen / NS) & 1), a.wait_ns));
+      if (bad) break;
       if ((seen & 1) != pair) {  // the other pair's; a warp that left its phase out would mistake the next
         if (lane == 0) mbar_arrive_cta(&empty[stage]);
         continue;
@@ -1062,8 +1067,8 @@ __global__ void __launch_bounds__(kThreads, 3)
     }
     for (int x = 0; x < n; ++x, ++seen) {
       const int stage = seen % NS;
-      if (!bad)
-        bad = !__all_sync(0xffffffffu, mbar_wait(&full[stage], (uint32_t)((seen / NS) & 1), a.wait_ns));
+      bad = bad || !__all_sync(0xffffffffu, mbar_wait(&full[stage], (uint32_t)((seen / NS) & 1), a.wait_ns));
+      if (bad) break;
       const float* kb = reinterpret_cast<const float*>(sm + (uint32_t)stage * 2 * LY::kTile) +
                         warp * KW * HD + lane * E;
       const float* vb = kb + KT * HD;

@@ -51,7 +51,8 @@ namespace qw {
 namespace {
 
 
-// mbar_wait inlined: a call in the softmax loop would have to save the row of scores around it.
+// mbar_wait inlined: a call in the softmax loop would have to save the row of scores around it. A limit
+// of 0 is not looked at here: a warp whose waits give up at once begins as one that has given up.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, int phase, uint64_t limit_ns) {
   uint64_t t0 = 0;
   for (uint32_t n = 1;; ++n) {
@@ -257,7 +258,7 @@ __global__ void __launch_bounds__(TcLayout<HD, NT, F>::kThreads, 1)
       long long row;
       int keys;
     };
-    bool ok = true, more = true;
+    bool ok = a.wait_ns != 0, more = true;
     int page = 0;  // of the cursor's tile, not yet checked, so that nothing waits for it before it is used
     auto find = [&] {
       const int key = c.kt * KT + TcRows<HD>::kKeys * w;
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(TcLayout<HD, NT, F>::kThreads, 1)
       return key < x.limit ? paged_page(a, x.b, key) : -1;
     };
     int page = page_of(c), issued = 0;
-    bool ok = true, more = true;
+    bool ok = a.wait_ns != 0, more = true;
     while (ok && more) {
       const int key = c.kt * KT + piece * prow, kvh = c.kvh, now = page;
       const int pieces = min(np, (max(c.limit - c.kt * KT, 0) + prow - 1) / prow);
@@ -410,8 +411,8 @@ __global__ void __launch_bounds__(TcLayout<HD, NT, F>::kThreads, 1)
       return __all_sync(0xffffffffu, wait_for(bar, n, a.wait_ns)) != 0;
     };
     auto kv_wait = [&](int use) { return wait(&kv_full[LY::slot(use)], LY::phase(use)); };
-    bool ok = true;
-    do {
+    bool ok = a.wait_ns != 0;
+    if (ok) do {
       const int n = __shfl_sync(0xffffffffu, c.kend - c.kt, 0);
       const int streams =  // the second stream may have no rows in this item
           __shfl_sync(0xffffffffu, NT == 1 && c.s.nb - c.rt * a.tpt > half ? 2 : 1, 0);
@@ -521,7 +522,9 @@ __global__ void __launch_bounds__(TcLayout<HD, NT, F>::kThreads, 1)
     PagedCursor c = paged_cursor<KT>(a, st);
     int tiles = 0, mine = 0;  // of the CTA; of this stream
     int ends = 0;             // items whose end this stream has waited for
-    bool bad = false;
+    // A wait gave up: this warp leaves, without another arrival (a slot given back before its copy has
+    // come would be armed twice), so that the warps behind these barriers give up as well.
+    bool bad = a.wait_ns == 0;
     auto wait = [&](uint64_t* bar, int n) {
       if (!bad) bad = !__all_sync(0xffffffffu, wait_for(bar, n, a.wait_ns));
     };
@@ -621,6 +624,7 @@ __global__ void __launch_bounds__(TcLayout<HD, NT, F>::kThreads, 1)
         const int g = tiles + x, buf = NT == 1 ? s : g & 1;
         const uint32_t ts = tb + LY::t_s * buf + lrow;
         wait(&s_full[buf], NT == 1 ? mine : g >> 1);
+        if (bad) break;
         tc_fence_after();
         if (NT == 1 && (warp & 3) == 0 && lane == 0) {  // S_g and P V of tile g - 1 have finished
           mbar_arrive_cta(&kv_empty[(2 * g) % NS]);
@@ -631,6 +635,7 @@ __global__ void __launch_bounds__(TcLayout<HD, NT, F>::kThreads, 1)
           // values behind the last key are whatever the page held: cleared (0 * NaN is NaN), by both
           // streams alike, each before its own products
           wait(&kv_full[(2 * g + 1) % NS], (2 * g + 1) / NS);
+          if (bad) break;
           if (k0 + r >= c.limit) {
             uint4* v = reinterpret_cast<uint4*>(sm + LY::off_ring + ((2 * g + 1) % NS) * LY::kTile + r * 128);
 #pragma unroll
@@ -665,6 +670,7 @@ __global__ void __launch_bounds__(TcLayout<HD, NT, F>::kThreads, 1)
         if (x > 0 && !take && __any_sync(0xffffffffu, mn != m)) {  // O moves to the new reference
           if (NT == 3) {  // (NT = 1: P V of the last tile was done before s_full of this one)
             wait(&o_full[0], g - 1);
+            if (bad) break;
             tc_fence_after();
           }
 #pragma unroll 1
@@ -738,21 +744,20 @@ __global__ void __launch_bounds__(TcLayout<HD, NT, F>::kThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
+        if (NT == 3 && bad) break;
         if (lane == 0) mbar_arrive_cta(&p_full[NT == 1 ? s : 0]);
       }
       if (NT == 1 && rows == 0 && (warp & 3) == 0) {  // a stream without rows lets the tiles pass
         for (int u = 2 * tiles; u < 2 * (tiles + n); ++u) {
           wait(&kv_full[u % NS], u / NS);
+          if (bad) break;
           if (lane == 0) mbar_arrive_cta(&kv_empty[u % NS]);
         }
       }
       if (rows > 0) {
-        if constexpr (NT == 1) {
-          wait(&o_full[s], ends++);
-          if ((warp & 3) == 0 && lane == 0) mbar_arrive_cta(&kv_empty[(2 * (tiles + n) - 1) % NS]);
-        } else {
-          wait(&o_full[0], tiles + n - 1);
-        }
+        wait(&o_full[NT == 1 ? s : 0], NT == 1 ? ends++ : tiles + n - 1);
+        if (bad) break;
+        if (NT == 1 && (warp & 3) == 0 && lane == 0) mbar_arrive_cta(&kv_empty[(2 * (tiles + n) - 1) % NS]);
         tc_fence_after();
         if (whole && a.pre.o && !a.prefix_pass) pdl_wait();  // the prefix's records
         // O out through shared memory (the q tile's, which no MMA reads any more), 32 columns of the
@@ -834,6 +839,7 @@ __global__ void __launch_bounds__(TcLayout<HD, NT, F>::kThreads, 1)
         }
         tc_fence_before();
       }
+      if (bad) break;
       if (!whole && first && s == 0 && r == 0)  // the joining kernel's work
         a.splits[blockIdx.x] = PagedSplit{c.last_cta(), c.s.lo + c.rt * a.tpt,
                                           min(a.tpt, c.s.nb - c.rt * a.tpt) * a.gq, c.kvh * a.gq};

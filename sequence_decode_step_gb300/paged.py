@@ -62,12 +62,13 @@ class PagedKV:
     call's new tokens; q_start: int32 [n_seqs + 1], first token row of each sequence;
     prefix_pages: int32 pages of ``prefix_len`` keys that all sequences share, or None.
     workspace: another PagedKV's ``workspace``, to share its scratch.
+    wait_limit_us: bound of a device-side wait of ``attend`` (0: one second).
     All are contiguous tensors on one CUDA device. They are borrowed, not copied: write new lengths
     or page ids into them between calls (or into a captured graph's inputs before a replay).
     """
 
     def __init__(self, k_pages, v_pages, page_table, kv_len, q_start, prefix_pages=None,
-                 prefix_len: int = 0, workspace: "Workspace" = None):
+                 prefix_len: int = 0, workspace: "Workspace" = None, wait_limit_us: int = 0):
         torch = _torch()
         if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
             raise ValueError("k_pages and v_pages: two [n_pages, n_kv_heads, page_size, head_dim] "
@@ -100,7 +101,7 @@ class PagedKV:
             struct_size=C.sizeof(B.qw_paged_kv), kv_format=_format(k_pages, "pages"),
             n_pages=k_pages.shape[0], page_size=page, n_kv_heads=k_pages.shape[1],
             head_dim=k_pages.shape[3], n_seqs=n_seqs, max_pages=page_table.shape[1],
-            prefix_len=prefix_len, k_pages=k_pages.data_ptr(), v_pages=v_pages.data_ptr(),
+            prefix_len=prefix_len, wait_limit_us=wait_limit_us, k_pages=k_pages.data_ptr(), v_pages=v_pages.data_ptr(),
             page_table=page_table.data_ptr(), kv_len=kv_len.data_ptr(),
             q_start=q_start.data_ptr(), status=self.status.data_ptr(),
             prefix_pages=prefix_pages.data_ptr() if prefix_len > 0 else None)

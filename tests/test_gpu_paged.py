@@ -607,3 +607,22 @@ def test_tensors_that_do_not_fit_are_refused():
         PagedKV(b.kd, b.vd, b.table_d.long(), b.len_d, b.start_d)
     with pytest.raises(ValueError):
         PagedKV(b.kd, b.vd, b.table_d, b.len_d, b.start_d, prefix_pages=b.len_d, prefix_len=17)
+
+
+@pytest.mark.parametrize("act,kv", TYPES)
+@pytest.mark.parametrize("seqs,nq,prefix,cols", [
+    ([(1, 700), (1, 33), (1, 4000)], 4, 0, 1), ([(1, 700), (1, 33)], 16, 2000, 1),
+    ([(30, 700), (0, 3), (9, 60)], 16, 0, 2048), ([(150, 0), (1, 900), (6, 9)], 16, 3000, 2048)])
+def test_waits_that_give_up(act, kv, seqs, nq, prefix, cols):
+    # every wait gives up at once: the call ends and reports it, and its workspace serves the next call,
+    # on decode kernels and on tensor-core tiles, with items split over several CTAs
+    from sequence_decode_step_gb300 import _binding as B
+    b = Batch(seqs, nq, 2, 64, 16, act, kv, prefix=prefix, seed=113, extra_cols=cols)
+    new = int(b.new.max())
+    c = b.cache(wait_limit_us=B.QW_PAGED_WAIT_NONE)
+    c.attend(b.q.cuda(), max_new=new)
+    with pytest.raises(RuntimeError, match="TIMEOUT"):
+        c.check()
+    d = b.cache(workspace=c.workspace)
+    attend_close(b, d.attend(b.q.cuda(), max_new=new))
+    d.check()

@@ -106,3 +106,9 @@ def test_launches_of_a_call_share_no_scratch(L):
     f = L.qw_paged_attention_workspace_bytes
     for n in (1, 2, 3, 14, 64):
         assert f(n, 16, 128, 1) >= 2 * f(n, 16, 128, 0) - (64 << 10)
+
+
+def test_wait_limit_takes_the_reserved_word(L):
+    assert B.qw_paged_kv.wait_limit_us.offset == 36 and C.sizeof(B.qw_paged_kv) == 96
+    c = cache(wait_limit_us=B.QW_PAGED_WAIT_NONE)
+    assert attend(L, c, n=0, q=None, out=None, ws=None, nbytes=0) == B.QW_OK
