@@ -40,6 +40,13 @@ class Workspace:
     def __init__(self, device):
         self.device, self.bytes, self.ptr = device, 0, None
         self._kept = []
+        self.streams = set()  # raw handles of the streams that the present buffer is known to be used on
+
+    def use(self, raw: int) -> None:
+        """The current stream (raw handle ``raw``) works on the scratch: once dropped, its memory is not
+        given out again before that stream has done so."""
+        self._kept[-1].record_stream(_torch().cuda.current_stream(self.device))
+        self.streams.add(raw)
 
     def grow(self, need: int) -> None:
         torch = _torch()
@@ -52,6 +59,7 @@ class Workspace:
         self._kept.append(torch.zeros(size, dtype=torch.uint8, device=self.device))
         torch.cuda.current_stream(self.device).synchronize()  # zero for calls on any stream
         self.bytes, self.ptr = size, self._kept[-1].data_ptr()
+        self.streams.clear()
 
 
 class PagedKV:
@@ -64,7 +72,9 @@ class PagedKV:
     workspace: another PagedKV's ``workspace``, to share its scratch.
     wait_limit_us: bound of a device-side wait of ``attend`` (0: one second).
     All are contiguous tensors on one CUDA device. They are borrowed, not copied: write new lengths
-    or page ids into them between calls (or into a captured graph's inputs before a replay).
+    or page ids into them between calls (or into a captured graph's inputs before a replay). Calls queue
+    on the current stream; a PagedKV may be dropped while they run, but not while a captured graph that
+    holds its calls may still be replayed (the graph knows its scratch by address only).
     """
 
     def __init__(self, k_pages, v_pages, page_table, kv_len, q_start, prefix_pages=None,
@@ -90,6 +100,7 @@ class PagedKV:
             raise ValueError("prefix_pages do not hold prefix_len keys")
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         torch.cuda.current_stream(self.device).synchronize()  # zero for calls on any stream
+        self._streams = set()  # those that status is known to be used on
         self._keep = (k_pages, v_pages, page_table, kv_len, q_start, prefix_pages)
         self.workspace = workspace if workspace is not None else Workspace(self.device)
         if self.workspace.device != self.device:
@@ -134,7 +145,11 @@ class PagedKV:
     def _stream(self):
         if self._current() != self._index:
             raise ValueError("the cache's device is not the current one")
-        return _raw_stream(self._index)
+        raw = _raw_stream(self._index)
+        if raw not in self._streams:
+            self.status.record_stream(_torch().cuda.current_stream(self.device))
+            self._streams.add(raw)
+        return raw
 
     def append(self, qkv, n_q_heads: int, q_norm=None, k_norm=None, eps: float = 1e-6,
                rope_theta: float = 1e6, positions=None, sections=None, out=None):
@@ -185,8 +200,11 @@ class PagedKV:
         ws = self.workspace
         if ws.bytes < need:
             ws.grow(need)
+        raw = self._stream()
+        if raw not in ws.streams:
+            ws.use(raw)
         rc = self._lib.qw_paged_attention(self._cref, q.data_ptr(), fmt, ld, n, heads, max_new,
-                                          out.data_ptr(), ws.ptr, ws.bytes, self._stream())
+                                          out.data_ptr(), ws.ptr, ws.bytes, raw)
         if rc:
             B.check("qw_paged_attention", rc)
         return out

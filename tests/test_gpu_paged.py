@@ -555,6 +555,32 @@ def test_other_streams():
     attend_close(b, got)
 
 
+def test_scratch_outlives_its_cache_on_other_streams():
+    """Made on one stream, used on another, dropped while that one is still busy: nobody gets the memory."""
+    import gc
+    b = Batch([(1, 500), (1, 3)], 8, 2, 128, 16, "bf16", "bf16", prefix=40, seed=43)
+    c = b.cache()
+    c.reserve(2, 8)
+    q = b.q.cuda()
+    out = torch.zeros_like(q)
+    mine = [c.workspace.ptr, c.status.data_ptr()]
+    size = c.workspace.bytes
+    gc.collect()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(1 << 30)               # half a second
+        c.attend(q, out=out)
+    del c
+    other = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    words = [torch.empty(1, dtype=torch.int32, device="cuda") for _ in range(4096)]
+    busy = not s.query()
+    taken = {t.data_ptr() for t in other + words} & set(mine)
+    s.synchronize()
+    assert busy and not taken
+    attend_close(b, out)
+
+
 # ------------------------------------------------------------------------------- reported errors
 def test_bad_pages_and_lengths_are_reported():
     b = Batch([(1, 20), (1, 20)], 4, 2, 64, 16, "f32", "bf16", seed=47)

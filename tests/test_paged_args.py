@@ -1,6 +1,7 @@
 """Refusals of the paged-cache calls: all of them return from the host checks, before any launch."""
 import ctypes as C
 import os
+from types import SimpleNamespace
 
 import pytest
 
@@ -112,3 +113,34 @@ def test_wait_limit_takes_the_reserved_word(L):
     assert B.qw_paged_kv.wait_limit_us.offset == 36 and C.sizeof(B.qw_paged_kv) == 96
     c = cache(wait_limit_us=B.QW_PAGED_WAIT_NONE)
     assert attend(L, c, n=0, q=None, out=None, ws=None, nbytes=0) == B.QW_OK
+
+
+def test_scratch_is_recorded_on_every_stream_that_uses_it(monkeypatch):
+    from sequence_decode_step_gb300 import paged
+    recorded = []
+
+    class Buffer:
+        def __init__(self, size):
+            self.size = size
+
+        def data_ptr(self):
+            return 16 * self.size
+
+        def record_stream(self, stream):
+            recorded.append((self.size, stream.name))
+
+    stream = SimpleNamespace(name="a", synchronize=lambda: None)
+    torch = SimpleNamespace(uint8=None, zeros=lambda size, dtype, device: Buffer(size), cuda=SimpleNamespace(
+        is_current_stream_capturing=lambda: False, current_stream=lambda device: stream))
+    monkeypatch.setattr(paged, "_torch", lambda: torch)
+    w = paged.Workspace("cuda:0")
+    w.grow(100)
+    w.use(7)
+    stream.name = "b"
+    assert 7 in w.streams and 9 not in w.streams
+    w.use(9)
+    assert recorded == [(100, "a"), (100, "b")]
+    w.grow(300)                     # a new buffer: no stream is known to use it
+    assert not w.streams and w.bytes == 300
+    w.use(9)
+    assert recorded[2:] == [(300, "b")]
