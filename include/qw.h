@@ -421,8 +421,9 @@ enum { QW_ACT_F32 = 0, QW_ACT_BF16 = 1 };
  * use lies outside [0, n_pages); append drops that row, attention reads page 0 instead
  * (that sequence's output is then meaningless). BAD_LENGTH: a kv_len outside
  * [0, max_pages * page_size], or smaller than the sequence's new tokens (append drops
- * rows that have no place, attention clamps). TIMEOUT: a device-side wait of attention
- * gave up; its outputs are invalid. */
+ * rows that have no place, attention clamps), or a q_start that decreases or leaves
+ * [0, n_tokens] (rows outside the call are left out; the others keep their places).
+ * TIMEOUT: a device-side wait of attention gave up; its outputs are invalid. */
 enum { QW_PAGED_TIMEOUT = 1, QW_PAGED_BAD_PAGE = 2, QW_PAGED_BAD_LENGTH = 4 };
 
 /* qw_paged_kv.wait_limit_us: every wait of attention's kernels gives up at once (to test what
@@ -460,7 +461,7 @@ typedef struct qw_paged_kv {
   void* v_pages;               /* the same shape */
   const int32_t* page_table;   /* [n_seqs, max_pages] */
   const int32_t* kv_len;       /* [n_seqs]: keys of each sequence, the call's tokens included */
-  const int32_t* q_start;      /* [n_seqs + 1], not decreasing */
+  const int32_t* q_start;      /* [n_seqs + 1], not decreasing, within [0, n_tokens] */
   const int32_t* prefix_pages; /* [ceil(prefix_len / page_size)], or NULL */
   int32_t* status;             /* [1], QW_PAGED_* bits, or NULL */
 } qw_paged_kv;

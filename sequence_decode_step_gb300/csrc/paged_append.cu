@@ -153,6 +153,8 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
   for (int b = threadIdx.x; b < a.c.n_seqs; b += kThreads) {
     const int lo = __ldg(a.c.q_start + b), hi = __ldg(a.c.q_start + b + 1);
     const int len = __ldg(a.c.kv_len + b);
+    if (blockIdx.x == 0 && a.c.status && paged_bad_start(a.c, b, a.n_tokens))
+      atomicOr(a.c.status, PG_BAD_LENGTH);
     const int first = max(lo, t0), last = min(hi, t0 + nt);
     if (first < last) {
       for (int t = first; t < last; ++t) {

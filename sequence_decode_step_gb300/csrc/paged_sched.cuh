@@ -54,11 +54,13 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedAttnArgs& a, int b) {
     s.base = s.len;
   } else {
     s.lo = min(max(__ldg(a.c.q_start + b), 0), a.n_tokens);
-    s.nb = min(max(__ldg(a.c.q_start + b + 1), s.lo), a.n_tokens) - s.lo;
+    // the sequence may go on behind the call's rows: its last token still has its last key
+    const int end = max(__ldg(a.c.q_start + b + 1), s.lo);
+    s.nb = min(end, a.n_tokens) - s.lo;
     const long long cap = (long long)a.c.max_pages << a.c.page_shift;
     const int len = __ldg(a.c.kv_len + b);
     s.len = (int)min((long long)max(len, 0), cap);
-    s.base = s.len - s.nb;
+    s.base = s.len - (end - s.lo);
   }
   s.nrt = (s.nb + a.tpt - 1) / a.tpt;
   return s;
@@ -145,7 +147,8 @@ __device__ __forceinline__ void paged_find_start(const PagedAttnArgs& a, PagedSt
       const PagedSeq s = paged_seq(a, b);
       const int hu = paged_head_units<KT>(a, s), units = hu * a.c.nkv;
       if (pass == 0) {
-        if (blockIdx.x == 0 && !a.prefix_pass && a.c.status && (s.base < 0 || s.len != __ldg(a.c.kv_len + b)))
+        if (blockIdx.x == 0 && !a.prefix_pass && a.c.status &&
+            (s.base < 0 || s.len != __ldg(a.c.kv_len + b) || paged_bad_start(a.c, b, a.n_tokens)))
           atomicOr(a.c.status, PG_BAD_LENGTH);
         mine += units;
         continue;

@@ -611,6 +611,39 @@ def test_bad_pages_and_lengths_are_reported():
         c.check()
 
 
+@pytest.mark.parametrize("act,kv", TYPES)
+@pytest.mark.parametrize("nq,cols", [(4, 1), (16, 2048)])
+def test_sequences_past_the_rows_of_a_call(act, kv, nq, cols):
+    # a q_start that goes on behind the call's rows (a graph of fewer tokens): the rows that are there keep
+    # their positions, see the keys that they see otherwise, and the rest is reported by both calls
+    b = Batch([(3, 10), (40, 20), (2, 7)], nq, 2, 64, 16, act, kv, seed=127, extra_cols=cols)
+    want, tol = b.attend()
+    n = 30
+    c = b.cache()
+    got = c.attend(b.q.cuda()[:n], max_new=40).double().cpu()
+    assert ((got - want[:n]).abs() <= tol[:n]).all()
+    with pytest.raises(RuntimeError, match="BAD_LENGTH"):
+        c.check()
+    d, e = b.cache(), b.cache()
+    qkv = torch.randn(b.rows, (nq + 4) * 64, device="cuda").to(DT[act])
+    short, whole = d.append(qkv[:n], nq), e.append(qkv, nq)
+    assert torch.equal(short, whole[:n])
+    with pytest.raises(RuntimeError, match="BAD_LENGTH"):
+        d.check()
+    e.check()
+
+
+def test_starts_that_decrease_are_reported():
+    b = Batch([(2, 10), (3, 20)], 4, 2, 64, 16, "f32", "bf16", seed=131)
+    for start in ([0, 3, 2], [-1, 2, 5]):
+        for call in ("append", "attend"):
+            c = b.cache()
+            b.start_d.copy_(torch.tensor(start, dtype=torch.int32))
+            c.append(b.qkv.cuda(), 4) if call == "append" else c.attend(b.q.cuda(), max_new=3)
+            with pytest.raises(RuntimeError, match="BAD_LENGTH"):
+                c.check()
+
+
 def test_tensors_that_do_not_fit_are_refused():
     from sequence_decode_step_gb300 import PagedKV
     b = Batch([(1, 20)], 4, 2, 64, 16, "f32", "bf16", seed=53)
