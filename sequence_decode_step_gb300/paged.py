@@ -189,9 +189,13 @@ class PagedKV:
         sequences' keys (and the shared prefix). max_new: the most new tokens of one sequence.
         Calls that share a workspace (those of one PagedKV, captured ones too) must not overlap on the
         GPU, and it has to exist before a capture: call once before, or ``reserve``."""
-        n = q.shape[0]
-        width = q.shape[1] * q.shape[2] if q.dim() == 3 else q.shape[1]
-        heads = width // self.head_dim
+        shape, hd = q.shape, self.head_dim
+        # (a head's size is not taken from the product: 8 heads of 64 are not 4 of 128)
+        if not (len(shape) == 3 and shape[2] == hd or len(shape) == 2 and shape[1] % hd == 0):
+            raise ValueError(f"q: [n_tokens, n_q_heads, {hd}] (or [n_tokens, n_q_heads * {hd}]) wanted, got "
+                             f"{tuple(shape)}")
+        n = shape[0]
+        heads = shape[1] if len(shape) == 3 else shape[1] // hd
         fmt = _format(q, "q")
         ld = self._rows(q, "q", heads * self.head_dim, n)
         out = self._out(out, q, heads, n)

@@ -685,3 +685,16 @@ def test_waits_that_give_up(act, kv, seqs, nq, prefix, cols):
     d = b.cache(workspace=c.workspace)
     attend_close(b, d.attend(b.q.cuda(), max_new=new))
     d.check()
+
+
+def test_queries_of_another_head_size_are_refused():
+    b = Batch([(1, 20), (1, 5)], 4, 2, 128, 16, "f32", "bf16", seed=137)
+    c = b.cache()
+    q = b.q.cuda()
+    for bad in (q.view(2, 8, 64), q.view(2, 2, 256), q.view(2, 1, 512), q.view(-1), q.view(2, 4, 2, 64),
+                torch.zeros(2, 4 * 128 + 64, device="cuda")):
+        with pytest.raises(ValueError, match="n_q_heads"):
+            c.attend(bad)
+    attend_close(b, c.attend(q))
+    attend_close(b, c.attend(q.view(2, 512)))
+    c.check()
