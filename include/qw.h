@@ -474,8 +474,8 @@ size_t qw_sizeof_paged_kv(void);
  *   qkv:       act_format [n_tokens, ld] DEVICE, ld >= (n_q_heads + 2 n_kv_heads) * head_dim
  *              elements and a multiple of 16 bytes; 16-byte aligned
  *   q_norm, k_norm: bf16 [head_dim] DEVICE, 4-byte aligned, both or neither (NULL)
- *   rotation (rotate-half): pair (j, j + head_dim/2) turns by position * rope_theta^(-2j/head_dim);
- *              the angle keeps f32 accuracy for positions up to 2^24 in magnitude
+ *   rotation (rotate-half): pair (j, j + head_dim/2) turns by position * rope_theta^(-2j/head_dim),
+ *              rope_theta >= 1; the angle keeps f32 accuracy for positions up to 2^24 in magnitude
  *   positions: without sections, int32 [n_tokens] DEVICE, or NULL for prefix_len + cache row;
  *              with sections, int32 [n_tokens, 3] DEVICE (time, height, width)
  *   sections:  HOST int32 [3] or NULL: how many of the head_dim/2 pairs turn by each axis, the

@@ -105,8 +105,10 @@ extern "C" int qw_paged_append(const qw_paged_kv* c, const void* qkv, uint32_t a
                 "multiple of 16 bytes");
   if (((uintptr_t)qkv | (uintptr_t)q_out) & 15)
     return fail(QW_ERR_ARG, "qw_paged_append: qkv and q_out must be 16-byte aligned");
-  if (!(rope_theta > 0.f) || !isfinite(rope_theta) || !(eps >= 0.f))
-    return fail(QW_ERR_ARG, "qw_paged_append: rope_theta must be positive and finite, eps not negative");
+  // (below 1 the frequencies grow along the head, past what two f32 terms carry: 9e-6 rad at 0.01 and
+  // position 2^24, no digit at 1e-12)
+  if (!(rope_theta >= 1.f) || !isfinite(rope_theta) || !(eps >= 0.f))
+    return fail(QW_ERR_ARG, "qw_paged_append: rope_theta must be finite and at least 1, eps not negative");
   qw::AppendArgs a{};
   a.sec0 = a.sec1 = hd / 2;
   a.n_axes = 1;

@@ -429,6 +429,16 @@ def test_append_far_and_negative_positions():
     check_append(b, got, {"positions": pos, "theta": 1e4})
 
 
+@pytest.mark.parametrize("theta", [1.0, 5e8, 3e38])
+def test_append_at_the_ends_of_theta(theta):
+    # one frequency for all pairs, and frequencies down to subnormal ones
+    b = Batch([(6, 0)], 2, 1, 64, 64, "f32", "f32", seed=139)
+    c = b.cache()
+    pos = torch.tensor([0, 1, 65537, 999999, (1 << 24) - 1, -(1 << 24)], dtype=torch.int32)
+    theta = float(np.float32(theta))
+    check_append(b, c.append(b.qkv.cuda(), 2, positions=pos.cuda(), rope_theta=theta), {"positions": pos, "theta": theta})
+
+
 def test_prefix_shifts_the_default_positions():
     b = Batch([(3, 4), (1, 0)], 4, 2, 64, 16, "f32", "bf16", prefix=77, seed=29)
     c = b.cache()

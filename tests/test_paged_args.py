@@ -144,3 +144,8 @@ def test_scratch_is_recorded_on_every_stream_that_uses_it(monkeypatch):
     assert not w.streams and w.bytes == 300
     w.use(9)
     assert recorded[2:] == [(300, "b")]
+
+
+@pytest.mark.parametrize("theta", [0.999, 0.01, 1e-12, 1e-38])
+def test_frequencies_that_grow_along_the_head_are_refused(L, theta):
+    assert append(L, cache(), theta=theta) == B.QW_ERR_ARG and "rope_theta" in B.last_error()
