@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "paged_plan.h"
+
 namespace qw {
 
 // A launch that may start while the kernel before it in the stream still runs; the kernel waits for
@@ -107,22 +109,12 @@ struct PagedAttnArgs {
   PagedPrefix pre;
   uint64_t wait_ns;
 };
-// Keys per tile, query rows per item, CTAs and an item's own cost of a launch: a rule on types and
-// row counts.
-struct PagedPlan {
-  bool tc;                  // paged_attention_tc.cu, else paged_attention.cu
-  int kt, rows, grid, item_units, least_units;
-};
 size_t paged_attn_workspace_bytes(int n_tokens, int nq, int hd, bool prefix);
 cudaError_t launch_paged_attention(const PagedAttnArgs& base, int hd, int max_new, void* workspace,
                                    int sms, cudaStream_t s);
 cudaError_t set_paged_attributes();
 
 // ---- tensor-core tiles (paged_attention_tc.cu) ----
-constexpr __host__ __device__ int paged_tc_keys(bool kv_bf16) { return kv_bf16 ? 128 : 64; }  // per tile
-constexpr int paged_tc_rows(bool act_bf16, bool kv_bf16) {  // query rows per item
-  return act_bf16 && kv_bf16 ? 256 : 128;
-}
 cudaError_t launch_paged_tc(const PagedAttnArgs& a, int hd, int grid, cudaStream_t s);
 // Joins the records of the items that the launch before it (`grid` CTAs) has split.
 cudaError_t launch_paged_join(const PagedAttnArgs& a, int hd, int grid, int item_rows, cudaStream_t s);

@@ -1203,7 +1203,7 @@ cudaError_t set_attributes_hd() {
 // Workspace of a call: counters (of the launch over own keys), then split descriptors, O records and
 // slots, a copy for each of the two launches, which may overlap; the prefix's whole records. A slot
 // holds as many rows as an item can have: at most kMaxRows and at most 8 query heads of every token.
-constexpr int kMaxSms = 192;
+constexpr int kMaxSms = kPagedMaxSms;
 constexpr int kMaxCtas = 3 * kMaxSms;  // of a launch
 constexpr int kMaxRows = 256;
 constexpr size_t align256(size_t v) { return (v + 255) / 256 * 256; }
@@ -1245,47 +1245,6 @@ cudaError_t set_paged_attributes() {
   return e == cudaSuccess ? set_paged_tc_attributes() : e;
 }
 
-// Tiles of 32 KB that an item's q, join and output cost a CTA: 6 us against 1.3 us a tile (3 to 5 give
-// the same within 2 % on the ragged cases).
-constexpr int kDecodeItemUnits = 5;
-
-// Keys per tile, query rows per item, CTAs and an item's own cost of a launch over sequences with
-// `rows` query rows (tokens x heads of a KV head) that meet up to `keys` keys.
-//
-// bf16 pages: few rows run the mma.sync kernel; more than 16 the tensor-core tiles, unless there is so
-// little of it that their start (3 to 5.5 us more, with q, first product and output) is most of the time.
-// Measured per tile and CTA: 1.3 us for 64 keys here, and for 128 keys there 1.5 us (bf16) or 2.9 us (f32 in
-// three terms). Calls with 4K prefix keys: 32 rows 20.6 us against 22.5 there, 64 rows 27.4 against 22.9 (f32
-// 30.8 and 27.6), 128 rows 44 against 28.7; one chunk of 64 tokens behind 2K keys 26.7 against 21, 512 keys 16.8
-// against 20.5. An item of tensor-core tiles costs about 7 us beside them; a share of 2 instead of 4 tiles at
-// least lets a 4K prefix of 128 rows use all SMs (36.8 us instead of 40.8 with f32 q).
-// f32 pages: the least tile that holds the rows: 2 or 4 with FMAs, 8 or 32 with mma.sync. More than 16
-// rows by the same estimate: 3.3 us for 32 rows x 32 keys on mma.sync, 2.5 us for 128 rows x 64 keys on the
-// tensor-core tiles, whose start takes 2 us more. Measured, with a key of each sequence's own: a prefix of
-// 1K keys and 32 rows 20 us against 27, 256 rows 49 against 37; of 16K keys 66 against 56 and 381 against 103.
-PagedPlan plan_paged_pass(const PagedAttnArgs& a, long long rows, long long keys, int sms) {
-  sms = std::min(sms, kMaxSms);
-  const bool f32 = !a.c.kv_bf16;
-  PagedPlan p{false, f32 ? 32 : 64, 8, 3 * sms, kDecodeItemUnits, 4};
-  if (f32) {
-    p.rows = rows <= 2 ? 2 : rows <= 4 ? 4 : rows <= 8 ? 8 : 32;
-    if (p.rows > 4) p.grid = 2 * sms;
-    if (p.rows > 8) p.least_units = 2;  // (a tile takes 3.3 us: 32 rows x 1K keys 22.5 -> 19.7 us)
-  }
-  if (rows > 16) {
-    auto us = [&](double start, double tile, int kt, int item_rows, int units, int grid) {
-      const double items = (double)a.c.nkv * ((rows + item_rows - 1) / item_rows);
-      return start + tile * std::ceil(items * (keys / kt + 1 + units) / grid);
-    };
-    const PagedPlan t{true, paged_tc_keys(!f32), paged_tc_rows(a.act_bf16, !f32), sms,
-                      f32 ? 4 : a.act_bf16 ? 5 : 3, 2};
-    if (us(f32 ? 6 : a.act_bf16 ? 9.5 : 7, f32 ? 2.5 : a.act_bf16 ? 1.5 : 2.9, t.kt, t.rows, t.item_units, t.grid) <
-        us(4, f32 ? 3.3 : 1.3, p.kt, p.rows, p.item_units, p.grid))
-      p = t;
-  }
-  return p;
-}
-
 cudaError_t launch_paged_attention(const PagedAttnArgs& base, int hd, int max_new, void* workspace,
                                    int sms, cudaStream_t s) {
   PagedAttnArgs a = base;
@@ -1312,13 +1271,16 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& base, int hd, int max_ne
   };
   const long long cap = (long long)a.c.max_pages << a.c.page_shift;
   // (the lengths are on the device: the longest that the table can hold stands for them)
-  const PagedPlan own = plan_paged_pass(a, (long long)std::min(max_new, a.n_tokens) * a.gq, cap, sms);
+  auto plan = [&](int seqs, int new_tokens, long long keys) {
+    return plan_paged_pass(a.c.kv_bf16, a.act_bf16, a.c.nkv, a.gq, a.n_tokens, seqs, new_tokens, keys, sms);
+  };
+  const PagedPlan own = plan(a.c.n_seqs, max_new, cap);
   if (too_long(own, cap, a.c.n_seqs)) return cudaErrorInvalidValue;
   if (prefix) {
     a.pre.ml = reinterpret_cast<float2*>(ws + w.whole_ml);
     a.pre.o = reinterpret_cast<float*>(ws + w.whole_o);
     a.prefix_pass = 1;
-    const PagedPlan p = plan_paged_pass(a, (long long)a.n_tokens * a.gq, a.c.prefix_len, sms);
+    const PagedPlan p = plan(1, a.n_tokens, a.c.prefix_len);
     if (too_long(p, a.c.prefix_len, 1)) return cudaErrorInvalidValue;
     cudaError_t e = run(p, 1);
     if (e == cudaSuccess && own.tc) e = launch_paged_join(a, hd, p.grid, p.rows, s);
