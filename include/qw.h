@@ -421,8 +421,9 @@ enum { QW_ACT_F32 = 0, QW_ACT_BF16 = 1 };
  * use lies outside [0, n_pages); append drops that row, attention reads page 0 instead
  * (that sequence's output is then meaningless). BAD_LENGTH: a kv_len outside
  * [0, max_pages * page_size], or smaller than the sequence's new tokens (append drops
- * rows that have no place, attention clamps), or a q_start that decreases or leaves
- * [0, n_tokens] (rows outside the call are left out; the others keep their places).
+ * rows that have no place, attention clamps), or a q_start that leaves [0, n_tokens]
+ * (rows outside the call are left out; the others keep their places) or decreases
+ * (attention then leaves its outputs as they were).
  * TIMEOUT: a device-side wait of attention gave up; its outputs are invalid. */
 enum { QW_PAGED_TIMEOUT = 1, QW_PAGED_BAD_PAGE = 2, QW_PAGED_BAD_LENGTH = 4 };
 

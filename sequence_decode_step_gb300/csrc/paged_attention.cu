@@ -1252,10 +1252,11 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& base, int hd, int max_ne
   const Workspace w(a.n_tokens, a.nq, hd, prefix);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.counters = reinterpret_cast<int*>(ws);
+  auto tile_tokens = [&](const PagedPlan& p) { return p.rows > 128 ? 2 * (128 / a.gq) : p.rows / a.gq; };
   auto run = [&](const PagedPlan& p, int i) {
     a.item_units = p.item_units;
     a.least_units = p.least_units;
-    a.tpt = p.rows > 128 ? 2 * (128 / a.gq) : p.rows / a.gq;
+    a.tpt = tile_tokens(p);
     a.splits = reinterpret_cast<PagedSplit*>(ws + w.splits[i]);
     a.flush = reinterpret_cast<float*>(ws + w.flush[i]);
     a.slots.ml = reinterpret_cast<float2*>(ws + w.ml[i]);
@@ -1266,7 +1267,7 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& base, int hd, int max_ne
   };
   // the line of a launch is counted in 32 bits
   auto too_long = [&](const PagedPlan& p, long long tiles, long long seqs) {
-    const long long items = a.n_tokens / (p.rows / a.gq) + seqs;
+    const long long items = a.n_tokens / tile_tokens(p) + seqs;
     return tiles / p.kt + 8 > INT32_MAX / 2 / a.c.nkv / items;
   };
   const long long cap = (long long)a.c.max_pages << a.c.page_shift;

@@ -22,7 +22,9 @@
 
 namespace qw {
 
-// Units are counted in 32 bits (the host refuses calls whose line could be longer). The code of
+// Units are counted in 32 bits: the host refuses calls whose line could be longer, as long as no row counts
+// twice. A q_start that decreases is reported and its line not walked, so neither that nor a row that the
+// prefix's launch did not take can lead out of the workspace. The code of
 // these kernels is kept short on purpose: a decode step's weights sweep the instructions out of the
 // caches between two calls, and a cold line of 128 bytes costs 0.2 us from L2 and 0.7 us from HBM,
 // more than most of the work it holds.
@@ -139,7 +141,7 @@ __device__ __forceinline__ void paged_find_start(const PagedAttnArgs& a, PagedSt
   const int b0 = min((int)threadIdx.x * spt, n), b1 = min(b0 + spt, n);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // the thread's sequences, twice: their units, then (in the one that holds the CTA's start) the place
-  int mine = 0, before = 0, r = -1, per = 0, total = 0;
+  int mine = 0, before = 0, r = -1, per = 0, total = 0, back = 0;
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll 1
@@ -151,6 +153,7 @@ __device__ __forceinline__ void paged_find_start(const PagedAttnArgs& a, PagedSt
             (s.base < 0 || s.len != __ldg(a.c.kv_len + b) || paged_bad_start(a.c, b, a.n_tokens)))
           atomicOr(a.c.status, PG_BAD_LENGTH);
         mine += units;
+        back |= !a.prefix_pass && __ldg(a.c.q_start + b + 1) < __ldg(a.c.q_start + b);
         continue;
       }
       if (r >= units) {
@@ -187,7 +190,7 @@ __device__ __forceinline__ void paged_find_start(const PagedAttnArgs& a, PagedSt
     }
     if (lane == 31) warp_sums[warp] = scan;
     if (threadIdx.x == 0) st->any = 0;
-    __syncthreads();
+    if (__syncthreads_or(back)) break;
     before = scan - mine;
 #pragma unroll 1
     for (int w = 0; w < W; ++w) {

@@ -654,6 +654,43 @@ def test_starts_that_decrease_are_reported():
                 c.check()
 
 
+@pytest.mark.parametrize("act,kv", TYPES)
+@pytest.mark.parametrize("nq,cols", [(4, 1), (16, 2048)])
+def test_starts_that_decrease_behind_a_prefix(act, kv, nq, cols):
+    # rows that the prefix's launch did not take have no records to join: the call does nothing, is reported
+    # and its workspace serves the next one
+    b = Batch([(5, 10), (3, 20), (8, 0)], nq, 2, 64, 16, act, kv, prefix=3000, seed=149, extra_cols=cols)
+    c = b.cache()
+    q = b.q.cuda()
+    for start in ([5, 0, 3, 3], [9, 16, 4, 2], [-3, 4, 1, 16], [0, 16, 0, 16], [1 << 30, -5, 7, 1 << 30]):
+        b.start_d.copy_(torch.tensor(start, dtype=torch.int32))
+        out = torch.full_like(q, 7.0)
+        c.attend(q, max_new=8, out=out)
+        with pytest.raises(RuntimeError, match="BAD_LENGTH"):
+            c.check()
+        assert (out == 7.0).all()
+        c.status.zero_()
+    b.start_d.copy_(torch.from_numpy(b.start.astype(np.int32)))
+    attend_close(b, c.attend(q, max_new=8))
+    c.check()
+
+
+def test_rows_counted_too_often_are_not_walked():
+    # every second sequence goes back over all rows: 128 x 2048 x 8 items of 5 units and 609 to 640 tiles (a row
+    # sees 38 913 to 40 960 keys), 1.32e9 units, more than the 2^30 - 1 that a line holds
+    from sequence_decode_step_gb300 import PagedKV
+    n, seqs = 2048, 256
+    i32 = {"dtype": torch.int32, "device": "cuda"}
+    k = torch.zeros(1, 8, 16, 64, dtype=torch.bfloat16, device="cuda")
+    c = PagedKV(k, k.clone(), torch.zeros(seqs, 2560, **i32), torch.full((seqs,), 40960, **i32),
+                torch.tensor([0, n] * 128 + [0], **i32))
+    out = torch.full((n, 64, 64), 7.0, device="cuda")
+    c.attend(torch.zeros(n, 64, 64, device="cuda"), out=out)
+    with pytest.raises(RuntimeError, match="BAD_LENGTH"):
+        c.check()
+    assert (out == 7.0).all()
+
+
 def test_tensors_that_do_not_fit_are_refused():
     from sequence_decode_step_gb300 import PagedKV
     b = Batch([(1, 20)], 4, 2, 64, 16, "f32", "bf16", seed=53)
