@@ -565,6 +565,31 @@ def test_other_streams():
     attend_close(b, got)
 
 
+@pytest.mark.parametrize("act,kv", TYPES)
+def test_two_streams_at_once(act, kv):
+    # a batch of steps behind a prefix on one stream, chunks on another, a workspace each: the same bits as alone
+    a = Batch([(1, 300 + 7 * i) for i in range(20)], 8, 2, 64, 16, act, kv, prefix=500, seed=151)
+    b = Batch([(60, 200), (1, 900), (33, 0)], 16, 2, 64, 16, act, kv, seed=157, extra_cols=2048)
+    ca, cb = a.cache(), b.cache()
+    qa, qb = a.q.cuda(), b.q.cuda()
+    alone = [ca.attend(qa), cb.attend(qb, max_new=60)]
+    attend_close(a, alone[0])
+    attend_close(b, alone[1])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(20):
+        with torch.cuda.stream(streams[0]):
+            got[0].append(ca.attend(qa))
+        with torch.cuda.stream(streams[1]):
+            got[1].append(cb.attend(qb, max_new=60))
+    torch.cuda.synchronize()
+    for x, y in zip(got, alone):
+        assert all(torch.equal(t, y) for t in x)
+    ca.check()
+    cb.check()
+
+
 def test_scratch_outlives_its_cache_on_other_streams():
     """Made on one stream, used on another, dropped while that one is still busy: nobody gets the memory."""
     import gc
