@@ -42,14 +42,6 @@ struct PagedView {
   int kv_bf16;
 };
 
-#ifdef __CUDACC__
-// Rows of sequence b that decrease or leave the call's.
-__device__ __forceinline__ bool paged_bad_start(const PagedView& c, int b, int n_tokens) {
-  const int lo = __ldg(c.q_start + b), hi = __ldg(c.q_start + b + 1);
-  return lo < 0 || hi < lo || hi > n_tokens;
-}
-#endif
-
 // ---- append (paged_append.cu) ----
 struct AppendArgs {
   PagedView c;

@@ -149,12 +149,12 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
 
   if (threadIdx.x < kMaxTb) row_s[threadIdx.x] = INT_MIN;
   __syncthreads();
+  bool bad = false;
   // each token's sequence: every thread looks at some sequences' ranges
   for (int b = threadIdx.x; b < a.c.n_seqs; b += kThreads) {
     const int lo = __ldg(a.c.q_start + b), hi = __ldg(a.c.q_start + b + 1);
     const int len = __ldg(a.c.kv_len + b);
-    if (blockIdx.x == 0 && a.c.status && paged_bad_start(a.c, b, a.n_tokens))
-      atomicOr(a.c.status, PG_BAD_LENGTH);
+    bad |= lo < 0 || hi < lo || hi > a.n_tokens;
     const int first = max(lo, t0), last = min(hi, t0 + nt);
     if (first < last) {
       for (int t = first; t < last; ++t) {
@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
       }
     }
   }
+  if (bad && a.c.status) atomicOr(a.c.status, PG_BAD_LENGTH);
   __syncthreads();
   if (threadIdx.x < nt) {
     const int row = row_s[threadIdx.x];

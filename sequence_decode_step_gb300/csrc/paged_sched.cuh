@@ -67,6 +67,11 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedAttnArgs& a, int b) {
   s.nrt = (s.nb + a.tpt - 1) / a.tpt;
   return s;
 }
+// Rows of sequence b that decrease or leave the call's.
+__device__ __forceinline__ bool paged_bad_start(const PagedAttnArgs& a, int b) {
+  const int lo = __ldg(a.c.q_start + b), hi = __ldg(a.c.q_start + b + 1);
+  return lo < 0 || hi < lo || hi > a.n_tokens;
+}
 // Keys that the last token of row tile rt sees.
 __device__ __forceinline__ int paged_limit(const PagedAttnArgs& a, const PagedSeq& s, int rt) {
   const int l = s.base + min(s.nb, (rt + 1) * a.tpt);
@@ -150,7 +155,7 @@ __device__ __forceinline__ void paged_find_start(const PagedAttnArgs& a, PagedSt
       const int hu = paged_head_units<KT>(a, s), units = hu * a.c.nkv;
       if (pass == 0) {
         if (blockIdx.x == 0 && !a.prefix_pass && a.c.status &&
-            (s.base < 0 || s.len != __ldg(a.c.kv_len + b) || paged_bad_start(a.c, b, a.n_tokens)))
+            (s.base < 0 || s.len != __ldg(a.c.kv_len + b) || paged_bad_start(a, b)))
           atomicOr(a.c.status, PG_BAD_LENGTH);
         mine += units;
         back |= !a.prefix_pass && __ldg(a.c.q_start + b + 1) < __ldg(a.c.q_start + b);
