@@ -481,6 +481,7 @@ size_t qw_sizeof_paged_kv(void);
  *              with sections, int32 [n_tokens, 3] DEVICE (time, height, width)
  *   sections:  HOST int32 [3] or NULL: how many of the head_dim/2 pairs turn by each axis, the
  *              first sections[0] by axis 0, the next sections[1] by axis 1, the rest by axis 2
+ *   n_q_heads: any number up to 4096 (qw_paged_attention reads multiples of n_kv_heads up to 8 times it)
  *   q_out:     act_format [n_tokens, n_q_heads * head_dim] DEVICE, 16-byte aligned; must not
  *              overlap qkv
  * n_tokens = 0 does nothing. Two tokens must not name the same slot. */
@@ -495,13 +496,18 @@ int qw_paged_append(const qw_paged_kv* c, const void* qkv, uint32_t act_format, 
  * n_kv_heads), at most 8 query heads per KV head. A token that sees no key gets zeros. The
  * prefix's keys are read once for the whole batch and joined with each sequence's own by
  * their softmax statistics. f32 activations give results of f32 accuracy from either cache
- * format; bf16 activations with a bf16 cache run one bf16 product with f32 sums. Results do
- * not depend on the order in which the CTAs finish. Keys and values that a call's tokens may
- * see are finite.
+ * format; bf16 activations with a bf16 cache run one bf16 product with f32 sums (the softmax's
+ * weights are rounded to bf16). Results do not depend on the order in which the CTAs finish: a call
+ * repeated gives the same bits. Keys and values that a call's tokens may see are finite.
  *   q:         act_format [n_tokens, ldq] DEVICE, ldq >= n_q_heads * head_dim elements and a
  *              multiple of 16 bytes; 16-byte aligned (q_out of qw_paged_append, ldq = n_q_heads * head_dim)
- *   max_new:   the most new tokens of one sequence, which chooses the kernel; a wrong value
- *              costs speed only
+ *   max_new:   the most new tokens of one sequence, which chooses the kernels together with
+ *              n_tokens, n_seqs, the heads, the table's width (max_pages * page_size stands for
+ *              the lengths, which are on the device) and prefix_len. Another kernel rounds
+ *              elsewhere; a wrong value costs speed only
+ *   limit:     n_kv_heads x row tiles (of the longest chunks that n_tokens and n_seqs allow) x key
+ *              tiles (of the table's width, and of the prefix) must stay below 2^30, else
+ *              QW_ERR_ARG: 256 sequences of 8 KV heads may have tables of 8M keys
  *   out:       act_format [n_tokens, n_q_heads * head_dim] DEVICE, 16-byte aligned; must not
  *              overlap q
  *   workspace: DEVICE scratch of qw_paged_attention_workspace_bytes(n_tokens, n_q_heads,

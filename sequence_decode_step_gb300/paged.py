@@ -157,7 +157,8 @@ class PagedKV:
 
         qkv: [n_tokens, (n_q_heads + 2 n_kv_heads) * head_dim] (rows may be strided); q_norm, k_norm:
         bfloat16 (or int16 bits) [head_dim]; positions: int32 [n_tokens], or [n_tokens, 3] with
-        sections = (pairs of axis 0, 1, 2), or None for each token's place in the cache.
+        sections = (pairs of axis 0, 1, 2), or None for each token's place in the cache; rope_theta >= 1.
+        ``out`` must not overlap qkv.
         """
         n = qkv.shape[0]
         fmt = _format(qkv, "qkv")
@@ -186,7 +187,8 @@ class PagedKV:
 
     def attend(self, q, max_new: int = 1, out=None):
         """Attention of the tokens' rotated queries [n_tokens, n_q_heads, head_dim] over their
-        sequences' keys (and the shared prefix). max_new: the most new tokens of one sequence.
+        sequences' keys (and the shared prefix). max_new: the most new tokens of one sequence, a hint that
+        chooses the kernels. ``out`` must not overlap q.
         Calls that share a workspace (those of one PagedKV, captured ones too) must not overlap on the
         GPU, and it has to exist before a capture: call once before, or ``reserve``."""
         shape, hd = q.shape, self.head_dim
