@@ -1,6 +1,6 @@
 // qw_paged_attention for few query rows per sequence: the decode step of a ragged batch, with the keys
 // read once from their pages where the rows fit one row tile. More rows run as several row tiles that
-// each stream the sequence's keys (9 to 16 over bf16 pages always: twice; more where the plan finds it
+// each stream the sequence's keys (9 to 16 over bf16 pages always, two or three times; more where the plan finds it
 // the shorter way).
 //
 //   o = sum_j p_j v_j / sum_j p_j,   p_j = 2^(s_j - m),   s_j = log2(e) / sqrt(hd) q . k_j

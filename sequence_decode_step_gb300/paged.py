@@ -80,6 +80,8 @@ class PagedKV:
     def __init__(self, k_pages, v_pages, page_table, kv_len, q_start, prefix_pages=None,
                  prefix_len: int = 0, workspace: "Workspace" = None, wait_limit_us: int = 0):
         torch = _torch()
+        if not 0 <= wait_limit_us < 1 << 32:
+            raise ValueError("wait_limit_us: 0 (one second) or microseconds below 2^32")
         if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
             raise ValueError("k_pages and v_pages: two [n_pages, n_kv_heads, page_size, head_dim] "
                              "tensors of one type")

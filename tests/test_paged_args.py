@@ -111,6 +111,10 @@ def test_launches_of_a_call_share_no_scratch(L):
 
 def test_wait_limit_takes_the_reserved_word(L):
     assert B.qw_paged_kv.wait_limit_us.offset == 36 and C.sizeof(B.qw_paged_kv) == 96
+    from sequence_decode_step_gb300 import PagedKV
+    for bad in (-1, 1 << 32):         # (the word would take -1 for no wait at all)
+        with pytest.raises(ValueError, match="wait_limit_us"):
+            PagedKV(None, None, None, None, None, wait_limit_us=bad)
     c = cache(wait_limit_us=B.QW_PAGED_WAIT_NONE)
     assert attend(L, c, n=0, q=None, out=None, ws=None, nbytes=0) == B.QW_OK
 
