@@ -515,6 +515,61 @@ def test_captured_graph_replays_with_new_lengths():
     c.check()
 
 
+@pytest.mark.parametrize("act,kv", TYPES)
+def test_captured_chunks_replay_with_new_lengths_and_starts(act, kv):
+    # chunks behind a prefix on tensor-core tiles (four launches), fewer tokens than captured in some replays
+    b = Batch([(40, 200), (1, 17), (23, 90)], 16, 2, 64, 16, act, kv, prefix=333, pad=3, seed=163, extra_cols=2048)
+    c = b.cache()
+    q, qkv = b.q.cuda(), b.qkv.cuda()
+    out, rot = torch.zeros_like(q), torch.zeros_like(q)
+    c.reserve(b.rows, 16)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.append(qkv, 16, out=rot)
+        c.attend(q, max_new=40, out=out)
+    for new, lens in (([40, 1, 23], [240, 18, 113]), ([2, 30, 0], [9, 30, 5]), ([0, 0, 1], [0, 16, 113]),
+                      ([33, 20, 11], [33, 20, 11])):
+        b.new, b.len, b.tokens = np.array(new), np.array(lens), sum(new)
+        b.start = np.concatenate([[0], np.cumsum(new)])
+        b.len_d.copy_(torch.from_numpy(b.len.astype(np.int32)))
+        b.start_d.copy_(torch.from_numpy(b.start.astype(np.int32)))
+        out.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        b.k, b.v = b.kd.cpu(), b.vd.cpu()
+        attend_close(b, out)
+        assert (out[b.tokens:] == 7.0).all()
+    c.check()
+
+
+@pytest.mark.parametrize("act,kv", TYPES)
+@pytest.mark.parametrize("nq,new,cols", [(4, 1, 1), (16, 1, 1), (16, 30, 2048)])
+def test_pools_past_2_31_elements(act, kv, nq, new, cols):
+    """The batch's pages at the end of a pool of 2.2e9 elements, on every kernel; what lies at the same
+    place modulo 2^32 bytes or 2^31 elements is other data."""
+    from sequence_decode_step_gb300 import PagedKV
+    b = Batch([(new, 700), (1, 33), (new, 0)], nq, 2, 128, 256, act, kv, prefix=600, seed=167, extra_cols=cols)
+    n = 33600
+    pools = [torch.empty(n, 2, 256, 128, dtype=DT[kv], device="cuda") for _ in range(2)]
+    assert pools[0].numel() > (1 << 31) + (1 << 24)
+    for big, small in zip(pools, (b.k, b.v)):
+        big[-b.n_pages:] = small.cuda()
+        big[:b.n_pages + 1024] = 3.0
+    i32 = {"device": "cuda", "dtype": torch.int32}
+    table = torch.from_numpy(np.where(b.table < b.n_pages, b.table + n - b.n_pages, 1 << 30).astype(np.int32)).cuda()
+    c = PagedKV(*pools, table, torch.from_numpy(b.len.astype(np.int32)).cuda(),
+                torch.from_numpy(b.start.astype(np.int32)).cuda(),
+                prefix_pages=torch.from_numpy(b.pre + n - b.n_pages).to(**i32), prefix_len=600)
+    attend_close(b, c.attend(b.q.cuda(), max_new=new))
+    got = c.append(b.qkv.cuda(), nq)
+    b.kd, b.vd = (p[-b.n_pages:].clone() for p in pools)
+    check_append(b, got, {})
+    assert all((p[:b.n_pages + 1024] == 3.0).all() for p in pools)
+    c.check()
+    del c, pools
+    torch.cuda.empty_cache()
+
+
 def test_capture_needs_its_workspace_and_keeps_it():
     b = Batch([(1, 200), (1, 17)], 4, 2, 64, 16, "f32", "bf16", seed=73)
     c = b.cache()
