@@ -825,3 +825,22 @@ def test_queries_of_another_head_size_are_refused():
     attend_close(b, c.attend(q))
     attend_close(b, c.attend(q.view(2, 512)))
     c.check()
+
+
+@pytest.mark.parametrize("act,kv", TYPES)
+@pytest.mark.parametrize("seqs,prefix,cols", [([(1, 4000), (1, 900), (1, 33)], 2000, 1),
+                                              ([(60, 3000), (1, 900), (30, 9)], 3000, 2048)])
+def test_waits_that_give_up_now_and_then(act, kv, seqs, prefix, cols):
+    # a limit of a microsecond, which some waits keep and others do not: every call ends, one that reports
+    # nothing is right, and the workspace serves the next call
+    b = Batch(seqs, 16, 2, 64, 16, act, kv, prefix=prefix, seed=173, extra_cols=cols)
+    ref, q, new = b.attend(), b.q.cuda(), int(b.new.max())
+    c = b.cache(wait_limit_us=1)
+    d = b.cache(workspace=c.workspace)
+    for _ in range(10):
+        got = c.attend(q, max_new=new)
+        if int(c.status.item()) == 0:
+            attend_close(b, got, ref)
+        c.status.zero_()
+        attend_close(b, d.attend(q, max_new=new), ref)
+    d.check()
