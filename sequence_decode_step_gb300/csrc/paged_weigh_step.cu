@@ -212,12 +212,16 @@ __global__ void __launch_bounds__(kThreads, step_ctas(HD, KB, QT)) step_scores_k
     }
     const int step = alone ? kStrip : kTile;
     const int first = (c.k0 + (alone ? 0 : warp)) * kStrip, end = min(c.k1 * kStrip, limit);
-    bool ok;
-    int row = 0, page = 0;  // the strip's; the next one's page
-    if (first < end) {
-      row = strip_row<false>(a, c.b, c.kvh, first, &ok);
-      stage_strip<F::kRow>(mine, a.c.k_pages, row, lane);
-    }
+    // the strip's place in the pool (-1 behind a bad page: page 0, which is read for it, keeps its owner's scores), and
+    // the next one's page
+    int row = 0, page = 0;
+    auto fetch = [&](int entry, int key, uint8_t* to) {
+      bool ok;
+      row = row_in(a, entry, c.kvh, key, &ok);
+      stage_strip<F::kRow>(to, a.c.k_pages, row, lane);
+      if (!ok) row = -1;
+    };
+    if (first < end) fetch(strip_page<false>(a, c.b, first), first, mine);
     stage_commit();
     if (first + step < end) page = strip_page<false>(a, c.b, first + step);
     QFrag<HD, KB, QT> q;
@@ -234,8 +238,7 @@ __global__ void __launch_bounds__(kThreads, step_ctas(HD, KB, QT)) step_scores_k
     for (int key = first; key < end; key += step, at ^= 1) {
       const int here = row;
       if (key + step < end) {
-        row = row_in(a, page, c.kvh, key + step, &ok);
-        stage_strip<F::kRow>(mine + (at ^ 1) * kBytes, a.c.k_pages, row, lane);
+        fetch(page, key + step, mine + (at ^ 1) * kBytes);
         if (key + 2 * step < end) page = strip_page<false>(a, c.b, key + 2 * step);
       }
       stage_commit();
@@ -245,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, step_ctas(HD, KB, QT)) step_scores_k
       float y[1][4];
       scores<HD, KB, QT, 1>(f, q.get(), y);
       const float(&x)[4] = y[0];
-      if (2 * t < a.keep) {
+      if (here >= 0 && 2 * t < a.keep) {
         float* to = a.kept + (long long)(here + g) * a.keep + 2 * t;
         *reinterpret_cast<float2*>(to) = make_float2(x[0] * a.scale_log2, x[1] * a.scale_log2);
         *reinterpret_cast<float2*>(to + 8 * a.keep) = make_float2(x[2] * a.scale_log2, x[3] * a.scale_log2);
