@@ -576,7 +576,7 @@ int qw_paged_attention(const qw_paged_kv* c, const void* q, uint32_t act_format,
  *   workspace: DEVICE scratch of qw_paged_weigh_workspace_bytes(c, n_tokens, n_q_heads, max_new, window) bytes,
  *              16-byte aligned, no initialisation needed; calls that overlap on the GPU need one each. With up to 8
  *              counted query rows per sequence and KV head it has room for their scores: 4 bytes for each row and
- *              key of the pool
+ *              key of the pool, so that a call of few tokens can need more than one of many
  * status: BAD_PAGE (the keys of that page count as page 0's, their scores are not written), BAD_LENGTH, TIMEOUT (a
  * tensor-core product over bf16 pages was not done within the cache's wait_limit_us: scores of the call's sequences are
  * then undefined). */

@@ -68,7 +68,8 @@ class Workspace:
         torch = _torch()
         if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("the workspace is too small and cannot be made inside a graph "
-                               "capture: call reserve(n_tokens, n_q_heads) before it")
+                               "capture: call reserve(n_tokens, n_q_heads), for weigh and evict with "
+                               "eviction=True, before it")
         # smaller ones are kept, as a captured graph may hold their address; each is at least twice
         # the one before, so that they stay below the largest together
         size = max(need, 2 * self.bytes)
@@ -296,13 +297,16 @@ class PagedKV:
 
     def reserve(self, n_tokens: int, n_q_heads: int, eviction: bool = False, max_new: int = 1, window: int = 0) -> None:
         """Workspace for attention calls of up to n_tokens rows (as the first such call would), and with
-        ``eviction`` that of ``evict`` and of ``weigh`` with these arguments."""
+        ``eviction`` that of ``evict`` and of every ``weigh`` of up to n_tokens rows, max_new and window (0: any).
+        Few counted rows need more than many: up to 8 of them per KV head keep their scores, 4 bytes for each of
+        them and each key and KV head of the pool."""
         lib, c = self._lib, self.c
         needs = [(self.workspace, lib.qw_paged_attention_workspace_bytes(n_tokens, n_q_heads, self.head_dim,
                                                                          c.prefix_len))]
         if eviction:
-            needs.append((self.workspace.eviction, max(
-                self._evict_bytes, lib.qw_paged_weigh_workspace_bytes(self._cref, n_tokens, n_q_heads, max_new, window))))
+            needs.append((self.workspace.eviction, max([self._evict_bytes] + [
+                lib.qw_paged_weigh_workspace_bytes(self._cref, n_tokens, n_q_heads, m, window)
+                for m in {*range(1, min(max_new, 8) + 1), max_new}])))
         for ws, need in needs:
             if ws.bytes < need:
                 ws.grow(need)
