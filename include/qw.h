@@ -578,8 +578,8 @@ int qw_paged_attention(const qw_paged_kv* c, const void* q, uint32_t act_format,
  *              counted query rows per sequence and KV head it has room for their scores: 4 bytes for each row and
  *              key of the pool, so that a call of few tokens can need more than one of many
  * status: BAD_PAGE (the keys of that page count as page 0's, their scores are not written), BAD_LENGTH, TIMEOUT (a
- * tensor-core product over bf16 pages was not done within the cache's wait_limit_us: scores of the call's sequences are
- * then undefined). */
+ * tensor-core product, of more than 8 counted rows or of the prefix, was not done within the cache's wait_limit_us:
+ * scores of the call's sequences are then undefined). */
 size_t qw_paged_weigh_workspace_bytes(const qw_paged_kv* c, int32_t n_tokens, int32_t n_q_heads, int32_t max_new,
                                       int32_t window);
 int qw_paged_weigh(const qw_paged_kv* c, const void* q, uint32_t act_format, int64_t ldq, int32_t n_tokens,
