@@ -41,6 +41,11 @@ def _raw(index: int) -> int:
     return _raw_stream(index)
 
 
+def _i32(value: int) -> int:
+    """A count, at most what a 32-bit argument holds (ctypes would drop its upper bits: 2^32 + 10 is no 10)."""
+    return max(min(value, (1 << 31) - 1), -1 << 31)
+
+
 class Workspace:
     """Scratch of PagedKV.attend, one for all caches whose calls follow one another (the layers of
     a model): pass the first cache's ``workspace`` to the others."""
@@ -262,6 +267,7 @@ class PagedKV:
         """
         n, heads, fmt, ld = self._queries(q)
         to = self._scores(scores, "scores")
+        max_new, window = _i32(max_new), _i32(window)
         ws = self.workspace.eviction
         raw = self._scratch(ws, self._lib.qw_paged_weigh_workspace_bytes(self._cref, n, heads, max_new, window))
         rc = self._lib.qw_paged_weigh(self._cref, q.data_ptr(), fmt, ld, n, heads, max_new, window, decay, to,
@@ -289,8 +295,8 @@ class PagedKV:
         dst = src if scores_out is None else self._scores(scores_out, "scores_out")
         ws = self.workspace.eviction
         raw = self._scratch(ws, self._evict_bytes)
-        rc = self._lib.qw_paged_evict(self._cref, src, dst, budget, recent, lengths.data_ptr(), ws.ptr, ws.bytes,
-                                      raw)
+        rc = self._lib.qw_paged_evict(self._cref, src, dst, _i32(budget), _i32(recent), lengths.data_ptr(), ws.ptr,
+                                      ws.bytes, raw)
         if rc:
             B.check("qw_paged_evict", rc)
         return lengths
@@ -301,6 +307,7 @@ class PagedKV:
         Few counted rows need more than many: up to 8 of them per KV head keep their scores, 4 bytes for each of
         them and each key and KV head of the pool."""
         lib, c = self._lib, self.c
+        max_new, window = _i32(max_new), _i32(window)
         needs = [(self.workspace, lib.qw_paged_attention_workspace_bytes(n_tokens, n_q_heads, self.head_dim,
                                                                          c.prefix_len))]
         if eviction:

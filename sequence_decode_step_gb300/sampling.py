@@ -7,7 +7,7 @@ from __future__ import annotations
 import ctypes as C
 
 from . import _binding as B
-from .paged import _format, _raw, _torch
+from .paged import _format, _i32, _raw, _torch
 
 
 def sample_batch(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, probs=None):
@@ -44,7 +44,7 @@ def sample_batch(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=
             if name == "top_p":
                 p.top_p = 1.0
         else:
-            setattr(p, name, value)
+            setattr(p, name, _i32(value) if name == "top_k" else value)
     u_ptr = column(u, "u")
     if out is None:
         out = torch.empty(n, dtype=torch.int32, device=logits.device)
