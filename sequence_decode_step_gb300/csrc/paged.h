@@ -114,7 +114,7 @@ cudaError_t set_paged_tc_attributes();
 
 // ---- scores by attention weight (paged_weigh.cu) ----
 struct WeighStats {     // softmax statistics (maximum, sum; base 2) of query rows
-  float2* slots;        // of split items: two slots of 8 r rows per CTA
+  float2* slots;        // of split items: two slots of an item's rows per CTA
   float2* whole;        // [n_tokens][nq], of the others
 };
 struct WeighArgs {
@@ -128,9 +128,6 @@ struct WeighArgs {
   float* scores;        // [n_pages][nkv][page_size]
   WeighStats own, pre;  // over the sequences' own keys and over the prefix
   int grid, pre_grid;   // CTAs of these launches
-  int r, pre_r;         // row tiles of 8 per item of them
-  int tiles;            // row tiles that the second launch holds: more take further passes over the keys
-  int tile_cost;        // of a pass over a tile's keys there, in row tiles
   float* kept;          // [pool rows][keep] scores (base 2) of sequences with up to `keep` query rows
   int keep;             // even, or 0
   uint64_t wait_ns;     // bound of a wait for tensor-core products

@@ -47,9 +47,6 @@
 namespace qw {
 namespace {
 
-constexpr int kRows = 128;                  // query rows of an item
-constexpr int kRowTiles = kRows / 8;
-constexpr int kTileCost = 56;  // of a pass over a tile's keys, in row tiles: 16 rows take 0.8 of the time of 128
 static_assert(kTile == 128, "keys of a tile are lanes or columns of S");
 
 // QT and KT: bf16 planes that hold q and the keys (three for f32)
@@ -321,15 +318,15 @@ __global__ void __launch_bounds__(kThreads, TcLayout<HD, QT, KT>::kCtas) weigh_l
   TcState st;
   tc_open(st, bars, &slot);
   pdl_launch_dependents();
-  find_share<PRE, false>(a, kRowTiles, &sh, warp_sums);
+  find_share<PRE, false>(a, &sh, warp_sums);
   if (sh.b < (PRE ? 1 : a.c.n_seqs)) {
     const WeighStats& out = PRE ? a.pre : a.own;
     float2* slots = out.slots + (size_t)blockIdx.x * 2 * kRows;
     int u = sh.u0, unit = sh.unit, b = sh.b;
     WSeq s = weigh_seq<PRE>(a, b);
     while (u < sh.u1) {
-      for (int n; u - unit >= (n = lse_units(a, s, kRowTiles, sh.head)); s = weigh_seq<PRE>(a, ++b)) unit += n;
-      const LseTiles part_of = lse_tiles(s, kRowTiles, sh.head, unit, sh.u1, &u);
+      for (int n; u - unit >= (n = lse_units(a, s, sh.head)); s = weigh_seq<PRE>(a, ++b)) unit += n;
+      const LseTiles part_of = lse_tiles(s, sh.head, unit, sh.u1, &u);
       const int kvh = part_of.kvh, r0 = part_of.r0, kt0 = part_of.kt0, kt1 = part_of.kt1, rows = min(kRows, s.rows - r0);
       if (kt0 >= kt1) continue;
       const int limit = row_sees<PRE>(a, s, r0 + rows - 1);
@@ -445,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, TcLayout<HD, QT, KT>::kCtas) weigh_s
   float* big_l = reinterpret_cast<float*>(sm + LY::off_l);  // [128]
   int* see = reinterpret_cast<int*>(big_l + kRows);         // [128]
   float* other = reinterpret_cast<float*>(see + kRows);     // [2][128]: the second half's sums of a tile's keys
-  find_share<false, true>(a, a.r, &sh, warp_sums);
+  find_share<false, true>(a, &sh, warp_sums);
   pdl_wait();
   TcState st;
   tc_open(st, bars, &slot);
@@ -455,8 +452,8 @@ __global__ void __launch_bounds__(kThreads, TcLayout<HD, QT, KT>::kCtas) weigh_s
     WSeq s = weigh_seq<false>(a, b);
     while (u < sh.u1) {
       for (int n; u - unit >= (n = sum_units(a, s, sh.head)); s = weigh_seq<false>(a, ++b))
-        unit += n, lse += lse_units(a, s, a.r, sh.lse_line.head);
-      const SumTiles part = sum_tiles(a, s, sh.head, unit, sh.u1, &u);
+        unit += n, lse += lse_units(a, s, sh.lse_line.head);
+      const SumTiles part = sum_tiles(s, sh.head, unit, sh.u1, &u);
       const int kvh = part.kvh, kt0 = part.kt0, kt1 = part.kt1;
       if (kt0 >= kt1) continue;
       for (int r0 = 0; r0 == 0 || r0 < s.rows; r0 += kRows) {
@@ -530,13 +527,10 @@ struct Tc {
     return e;
   }
   static cudaError_t prefix(WeighArgs& a, int sms, cudaStream_t s) {
-    a.pre_r = kRowTiles;
     a.pre_grid = LY::kCtas * sms;
     return launch_pdl(weigh_lse_kernel<HD, QT, KT, true>, dim3(a.pre_grid), kThreads, LY::bytes, s, a);
   }
   static cudaError_t run(WeighArgs a, int sms, cudaStream_t s) {
-    a.r = a.tiles = kRowTiles;
-    a.tile_cost = kTileCost;
     a.grid = LY::kCtas * sms;
     const cudaError_t e = launch_pdl(weigh_lse_kernel<HD, QT, KT, false>, dim3(a.grid), kThreads, LY::bytes, s, a);
     return e == cudaSuccess ? launch_pdl(weigh_sum_kernel<HD, QT, KT>, dim3(a.grid), kThreads, LY::bytes, s, a) : e;

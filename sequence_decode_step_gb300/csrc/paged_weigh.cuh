@@ -13,7 +13,8 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kStrip = 16;               // keys of a warp at a time
 constexpr int kTile = kStrip * kWarps;   // keys of a CTA at a time
-constexpr int kLeast = 1;                // least units of a share
+constexpr int kRows = 128;               // query rows of an item: more take further passes over the keys
+constexpr int kTileCost = 56;  // of a pass over a tile's keys, in tiles of 8 rows: 16 rows take 0.8 of the time of 128
 
 __device__ __forceinline__ float exp2_approx(float x) {  // 2^-inf = 0
   float y;
@@ -82,31 +83,31 @@ __device__ __forceinline__ WSeq weigh_seq(const WeighArgs& a, int b) {
   return s;
 }
 
-// The first launch's line: items of r row tiles of 8 for each KV head, each its key tiles and, before them, `head` tiles
+// The first launch's line: items of kRows query rows for each KV head, each its key tiles and, before them, `head` tiles
 // that stand for what comes before the keys: q, page entries, one after another. Shares of few tiles go without, as
 // every CTA has that to do once there: they would mostly lie idle (9 chunks of 61 tokens 98 us, with head tiles 104).
 constexpr int kHeadTiles = 3;
 __device__ __forceinline__ int head_tiles(int tiles, int grid) { return tiles >= 8 * grid ? kHeadTiles : 0; }
-__device__ __forceinline__ int row_blocks(const WSeq& s, int r) { return (s.rows + 8 * r - 1) / (8 * r); }
-__device__ __forceinline__ int lse_units(const WeighArgs& a, const WSeq& s, int r, int head) {
-  return s.nkt ? a.c.nkv * row_blocks(s, r) * (s.nkt + head) : 0;
+__device__ __forceinline__ int row_blocks(const WSeq& s) { return (int)((unsigned)(s.rows + kRows - 1) / kRows); }
+__device__ __forceinline__ int lse_units(const WeighArgs& a, const WSeq& s, int head) {
+  return s.nkt ? a.c.nkv * row_blocks(s) * (s.nkt + head) : 0;
 }
 // Key tiles kt0 .. kt1 - 1 of an item that units u .. u1 - 1 of a line hold; moves u behind them.
 struct LseTiles {
   int kvh, r0, kt0, kt1;
 };
-__device__ __forceinline__ LseTiles lse_tiles(const WSeq& s, int r, int head, int unit, int u1, int* u) {
-  const int nrb = row_blocks(s, r), n = s.nkt + head, item = (*u - unit) / n;
+__device__ __forceinline__ LseTiles lse_tiles(const WSeq& s, int head, int unit, int u1, int* u) {
+  const int nrb = row_blocks(s), n = s.nkt + head, item = (*u - unit) / n;
   const int in = *u - unit - item * n, to = min(n, in + (u1 - *u));
   *u += to - in;
-  return LseTiles{item / nrb, item % nrb * 8 * r, max(in - head, 0), max(to - head, 0)};
+  return LseTiles{item / nrb, item % nrb * kRows, max(in - head, 0), max(to - head, 0)};
 }
 // How a line is shared: units of a share, and its head tiles.
 struct Line {
   int per, head;
 };
 __device__ __forceinline__ int share_of(int total, int grid) {
-  return max((int)(((unsigned)total + grid - 1) / (unsigned)grid), kLeast);
+  return max((int)(((unsigned)total + grid - 1) / (unsigned)grid), 1);
 }
 
 // ------------------------------------------------------------------ fragments
@@ -116,7 +117,6 @@ template <int HD, bool KB, int QT>
 struct Frag {
   static constexpr int L = KB ? HD / 32 : HD / 16;  // loads of 16 bytes per row
   static constexpr int S = HD / 16;         // k-steps
-  static constexpr int kQ = QT * S / 2;     // uint4 (two k-steps) of a row tile's q per lane
   static constexpr int kRow = HD * (KB ? 2 : 4);  // bytes
   uint4 lo[L], hi[L];                       // keys g and g + 8
 
@@ -146,64 +146,44 @@ struct Frag {
     split<3>(__uint_as_float(hi[s].z), __uint_as_float(hi[s].w), k[3]);
   }
 };
-// One k-step of f32 keys for N row tiles: products of like size in one accumulator, so that chains stay short and
-// small terms are added up before large ones.
-template <int QT, int N>
-__device__ __forceinline__ void step_f32(const uint32_t (&k)[4][3], const uint2 (&q)[N][QT], float (&c)[N][3][4]) {
+// One k-step of f32 keys: products of like size in one accumulator, so that chains stay short and small terms are
+// added up before large ones.
+template <int QT>
+__device__ __forceinline__ void step_f32(const uint32_t (&k)[4][3], const uint2 (&q)[QT], float (&c)[3][4]) {
 #pragma unroll
   for (int x = 0; x < QT; ++x)
 #pragma unroll
-    for (int y = 2 - x; y >= 0; --y)
-#pragma unroll
-      for (int n = 0; n < N; ++n) mma(c[n][x + y], k[0][y], k[1][y], k[2][y], k[3][y], q[n][x].x, q[n][x].y);
+    for (int y = 2 - x; y >= 0; --y) mma(c[x + y], k[0][y], k[1][y], k[2][y], k[3][y], q[x].x, q[x].y);
 }
-template <int N>
-__device__ __forceinline__ void add_up(const float (&c)[N][3][4], float (&s)[N][4]) {
-#pragma unroll
-  for (int n = 0; n < N; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s[n][i] = c[n][0][i] + (c[n][1][i] + c[n][2][i]);
-}
-// Scores of 16 keys x N tiles of 8 query rows (several, as one accumulator's products wait for one another);
-// q(n, term, i): this lane's fragments of tile n, k-steps 2 i and 2 i + 1.
-template <int HD, bool KB, int QT, int N, class Q>
-__device__ __forceinline__ void scores(const Frag<HD, KB, QT>& f, Q q, float (&s)[N][4]) {
+// Scores of 16 keys x 8 query rows; q[term][i]: this lane's fragments, k-steps 2 i and 2 i + 1.
+template <int HD, bool KB, int QT>
+__device__ __forceinline__ void scores(const Frag<HD, KB, QT>& f, const uint4 (&q)[QT][HD / 32], float (&s)[4]) {
   constexpr int H = HD / 32;
   if constexpr (KB) {
-#pragma unroll
-    for (int n = 0; n < N; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+    s[0] = s[1] = s[2] = s[3] = 0.f;
 #pragma unroll
     for (int x = QT - 1; x >= 0; --x)
 #pragma unroll
       for (int i = 0; i < H; ++i) {
-        const uint4 &a = f.lo[i], &b = f.hi[i];
-        uint4 w[N];
-#pragma unroll
-        for (int n = 0; n < N; ++n) w[n] = q(n, x, i);
-#pragma unroll
-        for (int n = 0; n < N; ++n) mma(s[n], a.x, b.x, a.y, b.y, w[n].x, w[n].y);
-#pragma unroll
-        for (int n = 0; n < N; ++n) mma(s[n], a.z, b.z, a.w, b.w, w[n].z, w[n].w);
+        const uint4 &a = f.lo[i], &b = f.hi[i], &w = q[x][i];
+        mma(s, a.x, b.x, a.y, b.y, w.x, w.y);
+        mma(s, a.z, b.z, a.w, b.w, w.z, w.w);
       }
   } else {
-    float c[N][3][4] = {};
+    float c[3][4] = {};
 #pragma unroll
     for (int i = 0; i < H; ++i) {
-      uint2 w0[N][QT], w1[N][QT];
+      uint2 w0[QT], w1[QT];
 #pragma unroll
-      for (int n = 0; n < N; ++n)
-#pragma unroll
-        for (int x = 0; x < QT; ++x) {
-          const uint4 w = q(n, x, i);
-          w0[n][x] = make_uint2(w.x, w.y), w1[n][x] = make_uint2(w.z, w.w);
-        }
+      for (int x = 0; x < QT; ++x) w0[x] = make_uint2(q[x][i].x, q[x][i].y), w1[x] = make_uint2(q[x][i].z, q[x][i].w);
       uint32_t k[4][3];
       f.split_key(2 * i, k);
-      step_f32<QT, N>(k, w0, c);
+      step_f32<QT>(k, w0, c);
       f.split_key(2 * i + 1, k);
-      step_f32<QT, N>(k, w1, c);
+      step_f32<QT>(k, w1, c);
     }
-    add_up<N>(c, s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = c[0][i] + (c[1][i] + c[2][i]);
   }
 }
 // A strip of 16 rows into shared memory, by its warp; rows alternate in which half of 128 bytes they begin, so that
@@ -269,13 +249,13 @@ __device__ __forceinline__ void report_length(const WeighArgs& a, int b) {
 }
 
 // (maximum, sum) of a query row over all CTAs of the first launch that had part of its item. unit: the first unit
-// of its sequence, r: row tiles per item.
+// of its sequence.
 __device__ __forceinline__ float2 row_stats(const WeighArgs& a, const WeighStats& st, const WSeq& s, int unit,
-                                            Line line, int r, int kvh, int row, int lane, int lanes) {
-  const int rb = row / (8 * r);
+                                            Line line, int kvh, int row, int lane, int lanes) {
+  const int rb = (int)((unsigned)row / kRows);
   float2 x = make_float2(-INFINITY, 0.f);
   if (s.nkt == 0) return x;
-  const int u = unit + (kvh * row_blocks(s, r) + rb) * (s.nkt + line.head) + line.head;  // (of the first tile)
+  const int u = unit + (kvh * row_blocks(s) + rb) * (s.nkt + line.head) + line.head;  // (of the first tile)
   const int c0 = u / line.per, c1 = (u + s.nkt - 1) / line.per;
   if (c0 == c1) {
     const int token = row / a.gq;
@@ -287,7 +267,7 @@ __device__ __forceinline__ float2 row_stats(const WeighArgs& a, const WeighStats
       for (int i = 0; i < 8; ++i) {
         const int at = c + i * lanes;
         y[i] = make_float2(-INFINITY, 0.f);
-        if (at <= c1) y[i] = __ldcg(st.slots + ((size_t)at * 2 + (at == c0)) * 8 * r + (row - rb * 8 * r));
+        if (at <= c1) y[i] = __ldcg(st.slots + ((size_t)at * 2 + (at == c0)) * kRows + (row - rb * kRows));
       }
 #pragma unroll
       for (int i = 4; i > 0; i >>= 1)
@@ -299,23 +279,22 @@ __device__ __forceinline__ float2 row_stats(const WeighArgs& a, const WeighStats
   return x;
 }
 // ------------------------------------------------------------------ shares of key tiles
-// The second launch's line: a key tile takes as long as it has row tiles, and for each pass over its keys as long as
-// `tile_cost` more. Each KV head begins as the first launch's items do (without that, and with a lower cost of the keys,
+// The second launch's line: a key tile takes as long as it has tiles of 8 rows, and for each pass over its keys as long
+// as kTileCost more. Each KV head begins as the first launch's items do (without that, and with a lower cost of the keys,
 // the slowest CTA of 16 ragged windows took 73 us where others took 47), always: a share of a tile and a half that reaches into the next
 // head does the start twice (64 rows over 8192 keys of 8 heads: 25 us, without 31).
-__device__ __forceinline__ int key_cost(const WeighArgs& a, const WSeq& s) {
-  const int tiles = (s.rows + 7) / 8;
-  return a.tile_cost * max((tiles + a.tiles - 1) / a.tiles, 1) + tiles;
+__device__ __forceinline__ int key_cost(const WSeq& s) {
+  return kTileCost * max(row_blocks(s), 1) + (int)((unsigned)(s.rows + 7) / 8);
 }
 __device__ __forceinline__ int sum_units(const WeighArgs& a, const WSeq& s, int head) {
-  return s.nkt ? a.c.nkv * (s.nkt + head) * key_cost(a, s) : 0;
+  return s.nkt ? a.c.nkv * (s.nkt + head) * key_cost(s) : 0;
 }
 // The tiles (of keys) that begin in units u .. u1 - 1 of a sequence's line, which begins at `unit`; moves u to their end.
 struct SumTiles {
   int kvh, kt0, kt1;
 };
-__device__ __forceinline__ SumTiles sum_tiles(const WeighArgs& a, const WSeq& s, int head, int unit, int u1, int* u) {
-  const int cost = key_cost(a, s), n = s.nkt + head, all = n * cost, kvh = (*u - unit) / all;
+__device__ __forceinline__ SumTiles sum_tiles(const WSeq& s, int head, int unit, int u1, int* u) {
+  const int cost = key_cost(s), n = s.nkt + head, all = n * cost, kvh = (*u - unit) / all;
   const int in = *u - unit - kvh * all, t0 = (in + cost - 1) / cost, t1 = min(n, (in + (u1 - *u) + cost - 1) / cost);
   *u = unit + kvh * all + (t0 < n ? max(t0, t1) * cost : all);
   return SumTiles{kvh, max(t0 - head, 0), max(t1 - head, 0)};
@@ -330,7 +309,7 @@ struct Share {            // in shared memory: where a CTA's share begins
 
 // Block-wide. SUM: the second launch. Reports lengths out of range (the second launch does).
 template <bool PRE, bool SUM>
-__device__ void find_share(const WeighArgs& a, int r, Share* sh, int (*warp_sums)[kWarps]) {
+__device__ void find_share(const WeighArgs& a, Share* sh, int (*warp_sums)[kWarps]) {
   const int n = PRE ? 1 : a.c.n_seqs, spt = (n + kThreads - 1) / kThreads;
   const int b0 = min((int)threadIdx.x * spt, n), b1 = min(b0 + spt, n);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -340,9 +319,9 @@ __device__ void find_share(const WeighArgs& a, int r, Share* sh, int (*warp_sums
   bool back = false;
   for (int b = b0; b < b1; ++b) {
     const WSeq s = weigh_seq<PRE>(a, b);
-    const int whole = lse_units(a, s, r, 0);
+    const int whole = lse_units(a, s, 0);
     mine[0] += whole;
-    mine[1] += lse_units(a, s, r, 1) - whole;
+    mine[1] += lse_units(a, s, 1) - whole;
     if (SUM) {
       const int keys = sum_units(a, s, 0);
       mine[2] += keys;
@@ -384,7 +363,7 @@ __device__ void find_share(const WeighArgs& a, int r, Share* sh, int (*warp_sums
   if (u0 < all && u0 >= unit && u0 < unit + mine[H] + head * mine[H + 1]) {
     for (int b = b0; b < b1; ++b) {
       const WSeq s = weigh_seq<PRE>(a, b);
-      const int l = lse_units(a, s, r, head_lse), u = SUM ? sum_units(a, s, head) : l;
+      const int l = lse_units(a, s, head_lse), u = SUM ? sum_units(a, s, head) : l;
       if (u0 < unit + u) {
         sh->u0 = u0, sh->u1 = min(u0 + per, all);
         sh->head = head;
@@ -401,8 +380,8 @@ __device__ void find_share(const WeighArgs& a, int r, Share* sh, int (*warp_sums
 
 // How the prefix's launch has shared its line.
 __device__ __forceinline__ Line prefix_line(const WeighArgs& a, const WSeq& pre) {
-  const int head = head_tiles(lse_units(a, pre, a.pre_r, 0), a.pre_grid);
-  return Line{share_of(lse_units(a, pre, a.pre_r, head), a.pre_grid), head};
+  const int head = head_tiles(lse_units(a, pre, 0), a.pre_grid);
+  return Line{share_of(lse_units(a, pre, head), a.pre_grid), head};
 }
 struct SumItem {  // in shared memory: tiles kt0 .. kt1 - 1 of a sequence and KV head
   WSeq s;
@@ -411,17 +390,17 @@ struct SumItem {  // in shared memory: tiles kt0 .. kt1 - 1 of a sequence and KV
   Line line;         // its shares
 };
 // L and the keys seen of `n` query rows from row r0 on, into shared memory: the CTA's threads share a row's records.
-__device__ __noinline__ void stage_stats(const WeighArgs& a, const SumItem& it, int r0, int n, float* big_l, int* see) {
-  const int lanes = n <= 8 ? 32 : n <= 64 ? 4 : 2;  // a power of two, within a warp
+__device__ __forceinline__ void stage_stats(const WeighArgs& a, const SumItem& it, int r0, int n, float* big_l, int* see) {
+  const int lanes = n <= 64 ? 4 : 2;  // a power of two, within a warp
   const WSeq pre = weigh_seq<true>(a, 0);
   const Line pre_line = prefix_line(a, pre);
   for (int i0 = 0; i0 < n; i0 += kThreads / lanes) {
     const int i = i0 + (int)threadIdx.x / lanes, lane = (int)threadIdx.x % lanes, row = r0 + i;
     float2 x = make_float2(-INFINITY, 0.f);
     if (i < n && row < it.s.rows) {
-      x = row_stats(a, a.own, it.s, it.lse, it.line, a.r, it.kvh, row, lane, lanes);
+      x = row_stats(a, a.own, it.s, it.lse, it.line, it.kvh, row, lane, lanes);
       if (pre.nkt)
-        x = join(x, row_stats(a, a.pre, pre, 0, pre_line, a.pre_r, it.kvh, row + (it.s.lo - pre.lo) * a.gq, lane, lanes));
+        x = join(x, row_stats(a, a.pre, pre, 0, pre_line, it.kvh, row + (it.s.lo - pre.lo) * a.gq, lane, lanes));
     }
     for (int o = 1; o < lanes; o <<= 1)
       x = join(x, make_float2(__shfl_xor_sync(0xffffffffu, x.x, o), __shfl_xor_sync(0xffffffffu, x.y, o)));

@@ -163,9 +163,6 @@ struct QFrag {
       }
     }
   }
-  __device__ __forceinline__ auto get() const {
-    return [this](int, int x, int i) { return w[x][i]; };
-  }
 };
 
 // CTAs per SM of the first launch: as many as the strips' shared memory and the fragments' registers leave room for.
@@ -245,9 +242,8 @@ __global__ void __launch_bounds__(kThreads, step_ctas(HD, KB, QT)) step_scores_k
       stage_wait<1>();
       F f;
       f.take(mine + at * kBytes, lane);
-      float y[1][4];
-      scores<HD, KB, QT, 1>(f, q.get(), y);
-      const float(&x)[4] = y[0];
+      float x[4];
+      scores<HD, KB, QT>(f, q.w, x);
       if (here >= 0 && 2 * t < a.keep) {
         float* to = a.kept + (long long)(here + g) * a.keep + 2 * t;
         *reinterpret_cast<float2*>(to) = make_float2(x[0] * a.scale_log2, x[1] * a.scale_log2);
@@ -305,8 +301,7 @@ __device__ __forceinline__ float step_stats(const WeighArgs& a, const WSeq& s, i
     }
     if (a.c.prefix_len > 0) {
       const WSeq pre = weigh_seq<true>(a, 0);
-      x = join(x, row_stats(a, a.pre, pre, 0, prefix_line(a, pre), a.pre_r, kvh,
-                            row + (s.lo - pre.lo) * a.gq, sub, 4));
+      x = join(x, row_stats(a, a.pre, pre, 0, prefix_line(a, pre), kvh, row + (s.lo - pre.lo) * a.gq, sub, 4));
     }
   }
   x = join(x, make_float2(__shfl_xor_sync(0xffffffffu, x.x, 1), __shfl_xor_sync(0xffffffffu, x.y, 1)));
@@ -331,9 +326,8 @@ __device__ __noinline__ void step_again(const WeighArgs& a, int b, int unit, int
       const int row = strip_row<false>(a, b, kvh, k * kStrip, &ok);
       Frag<HD, KB, QT> f;
       f.load(a.c.k_pages, row, lane);
-      float y[1][4], w[2] = {0.f, 0.f};
-      scores<HD, KB, QT, 1>(f, q.get(), y);
-      const float(&x)[4] = y[0];
+      float x[4], w[2] = {0.f, 0.f};
+      scores<HD, KB, QT>(f, q.w, x);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         if (key < see[e]) w[0] += exp2_approx(fmaf(x[e], a.scale_log2, -big[e]));
