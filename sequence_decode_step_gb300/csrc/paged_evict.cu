@@ -331,7 +331,8 @@ __global__ void __launch_bounds__(256) evict_lengths_kernel(const int* from, int
   if (i < n) to[i] = __ldcg(from + i);
 }
 
-// Most scores of a sequence in shared memory: 160 KB, or 64 KB (three CTAs per SM) where there are CTAs enough.
+// Most scores of a sequence in shared memory: 160 KB, or 64 KB where there are CTAs enough for two on an SM (each has 20 KB
+// of EvictShared besides, of 228).
 constexpr int kMostKeys = 40960, kManyKeys = 16384;
 
 }  // namespace
