@@ -568,8 +568,9 @@ int qw_paged_attention(const qw_paged_kv* c, const void* q, uint32_t act_format,
  * Two sequences must not share pages outside the prefix. Results are f32 whatever the types, and the same bits
  * on every run.
  *   q, act_format, ldq, n_tokens, n_q_heads, max_new: as for qw_paged_attention
- *   limit:     n_kv_heads x (tiles of 128 keys of the table's width, or of the prefix, + 3) x (58 n_seqs + n_tokens *
- *              n_q_heads / n_kv_heads + 2) must stay below 2^30, else QW_ERR_ARG
+ *   limit:     n_kv_heads x (tiles of 128 keys of the table's width + 3) x (58 n_seqs + counted tokens * n_q_heads /
+ *              n_kv_heads + 2) must stay below 2^30, else QW_ERR_ARG; at most n_seqs * window tokens are counted.
+ *              So must n_kv_heads x (tiles of the prefix + 3) x (n_tokens * n_q_heads / n_kv_heads / 128 + 2)
  *   window:    0 for all tokens
  *   decay:     in [0, 1], of what was there; 1 accumulates
  *   scores:    f32 [n_pages, n_kv_heads, page_size] DEVICE, one per key and KV head of the pools

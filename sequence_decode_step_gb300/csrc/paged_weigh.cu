@@ -578,10 +578,14 @@ cudaError_t set_weigh_attributes() {
 
 cudaError_t launch_paged_weigh(const WeighArgs& base, int hd, int max_new, void* workspace, int sms, cudaStream_t s) {
   WeighArgs a = base;
-  // units of the longest possible lines are counted in 32 bits
-  const long long tiles = std::max((((long long)a.c.max_pages << a.c.page_shift) + kTile - 1) / kTile,
-                                   ((long long)a.c.prefix_len + kTile - 1) / kTile);
-  if ((double)a.c.nkv * (tiles + kHeadTiles) * (58.0 * a.c.n_seqs + (double)a.n_tokens * a.gq + 2) >= 1073741824.0)
+  // units of the longest possible lines are counted in 32 bits: of the counted tokens' rows over the sequences' own keys
+  // (key_cost() is at most 58 and a unit for every row), and of blocks of all tokens' rows over the prefix
+  auto units = [&](long long keys, double of_a_tile) {
+    return a.c.nkv * (double)((keys + kTile - 1) / kTile + kHeadTiles) * of_a_tile;
+  };
+  const double tokens = a.n_tokens, counted = a.window > 0 ? std::min(tokens, (double)a.c.n_seqs * a.window) : tokens;
+  if (units((long long)a.c.max_pages << a.c.page_shift, 58.0 * a.c.n_seqs + counted * a.gq + 2) >= 1073741824.0 ||
+      units(a.c.prefix_len, tokens * a.gq / kRows + 2) >= 1073741824.0)
     return cudaErrorInvalidValue;
   uint8_t* w = static_cast<uint8_t*>(workspace);
   auto stats = [&] {
