@@ -411,9 +411,11 @@ int qw_sample_last(qw_handle* h, float temperature, int32_t top_k, float top_p, 
  *   top_k <= 0 or >= vocab: no cut; top_p >= 1: no nucleus; min_p = 0: none.
  * A logit of -inf is never drawn. A row gets token -1 and probability 0 when it holds a NaN, +inf or
  * nothing above -inf, or when its settings lie outside their ranges (temperature NaN or infinite, top_p not
- * above 0, min_p outside [0, 1], u outside [0, 1)). A running sum is right to 2^-27 of itself whatever the
- * vocabulary is, so that the token is the one of exact sums unless a border lies within 2^-26 of what is
- * compared with it, and the same on every run.
+ * above 0, min_p outside [0, 1], u outside [0, 1)); one value for all rows outside its range is QW_ERR_ARG, for
+ * greedy rows too. A running sum is right to 2^-27 of itself whatever the vocabulary is, so that the token is the
+ * one of exact sums unless a border lies within 2^-26 of what is compared with it, and the same on every run.
+ * Weights below e^-48 count as 0, a difference l_0 - l_i beyond f32's range as infinite, and a temperature between 0
+ * and 3.2e-29 as 3.2e-29.
  *   params:    each setting as one value for all rows, or (its pointer not NULL) DEVICE [n_rows], which a
  *              captured graph may replay with new ones
  *   logits:    act_format [n_rows, ld] DEVICE, ld >= vocab elements, aligned to its type; vocab <= 2^20
@@ -565,7 +567,8 @@ int qw_paged_attention(const qw_paged_kv* c, const void* q, uint32_t act_format,
  * share the weight but have no score). Counted are the last `window` tokens of each sequence, or all of them.
  * Append first; scores need no initialisation (a key's score starts when it is new), and those of sequences
  * without tokens in the call, of rows behind kv_len and of pages that no sequence uses are left as they are.
- * Two sequences must not share pages outside the prefix. Results are f32 whatever the types, and the same bits
+ * Keys that the call's tokens see are finite, as for attention. Two sequences must not share pages outside the
+ * prefix. Results are f32 whatever the types, and the same bits
  * on every run.
  *   q, act_format, ldq, n_tokens, n_q_heads, max_new: as for qw_paged_attention
  *   limit:     n_kv_heads x (tiles of 128 keys of the table's width + 3) x (58 n_seqs + counted tokens * n_q_heads /

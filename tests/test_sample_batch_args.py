@@ -46,6 +46,12 @@ def test_bad_settings(L, bad):
     assert call(L, params(**bad)) == B.QW_ERR_ARG and B.last_error()
 
 
+@pytest.mark.parametrize("bad", [dict(top_p=0.0), dict(min_p=1.1), dict(min_p=float("nan"))])
+@pytest.mark.parametrize("greedy", [dict(temperature=0.0), dict(top_k=1)])
+def test_bad_settings_of_a_greedy_call(L, bad, greedy):
+    assert call(L, params(**bad, **greedy)) == B.QW_ERR_ARG and B.last_error()
+
+
 def test_struct_size_and_no_rows(L):
     assert call(L, params(struct_size=52)) == B.QW_ERR_ABI
     assert call(L, None) == B.QW_ERR_ARG
