@@ -10,8 +10,8 @@
 // A cluster of CTAs serves one sequence and KV head. Each of its CTAs finds the least score that stays by
 // histograms over the scores' bits (2048 bins between the least and the largest: two rounds, or three), then
 // the places and their fillers by running counts in row order: cheaper than sharing them, and the moves are
-// dealt to the CTAs. Bytes bound the moves: 128 sequences of up to 4K f32 keys cut to 3333, 1.14 GB in 200 us (5.7
-// TB/s). 24 prompts of up to 16K keys take 56 us, half of them for the longest one's histograms and counts; one step's
+// dealt to the CTAs. Bytes bound the moves: 128 sequences of 4K f32 keys cut to 3333, 1.14 GB in 200 us (5.7
+// TB/s). 24 prompts of up to 16K keys take 57 us, half of them for the longest one's histograms and counts; one step's
 // eviction of 64 sequences 17 us, a chain of barriers and dependent reads.
 
 #include <cuda_runtime.h>

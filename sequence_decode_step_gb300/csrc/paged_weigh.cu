@@ -14,8 +14,8 @@
 // launch), in pairs where the instructions take two. For a tile of each of an SM's two CTAs the exponentials (32 a clock
 // and SM) take 0.5 us, the products 0.3, the keys' bytes 1.4 at HBM's rate (64 KB): the bytes bound both launches where
 // a KV head has up to 128 rows, the scores' instructions beyond. Measured 1.2 to 1.7 us a tile in the first launch, 1.3 to
-// 1.5 in the second, and 5 in each before the first tile. 16 windows of 32 tokens over up to 8K keys: 70 us, for 160
-// MB in 33 us and again in 38. The scores are formed twice because kept ones would be more bytes than the keys.
+// 1.5 in the second, and 5 in each before the first tile. 16 windows of 32 tokens over up to 8K keys: 68 us, for 160
+// MB in 33 us and again in 36. The scores are formed twice because kept ones would be more bytes than the keys.
 // Tried without gain: the second launch backwards, for what L2 still holds, and the copies of the next tile behind the
 // products instead of before them.
 //
@@ -26,8 +26,8 @@
 // through registers, one tile ahead. The products of a tile run while the scores of the one before it are worked on, from
 // two S buffers of 128 TMEM columns. All eight warps copy and work on scores; a barrier per tile hands the tile to
 // the thread that issues the products. mma.sync in place of this took 137 us for 16 windows of 32 tokens over bf16
-// pages (70 here), 99 for 9 chunks of 61 tokens over f32 pages (50 here); it was up to a third faster only with 9 to 32
-// rows over f32 pages of 128 dimensions (16 rows x 16 sequences of up to 8K keys 134 us, 196 here; 128 rows 360, 208 here).
+// pages (68 here), 99 for 9 chunks of 61 tokens over f32 pages (48 here); it was up to a third faster only with 9 to 32
+// rows over f32 pages of 128 dimensions (16 rows x 16 sequences of up to 8K keys 134 us, 198 here; 128 rows 360, 208 here).
 //
 // Work is shared as in attention: every sequence's tiles of 128 keys, for each KV head (and, in the first launch,
 // each block of query rows), laid end to end form one line that is cut into equal shares. Items at a share's ends

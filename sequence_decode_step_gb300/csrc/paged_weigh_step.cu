@@ -9,9 +9,10 @@
 // a warp's own part of shared memory, 16 ahead of the 16 at work, and from there into mma.sync fragments (m16n8k16: keys on
 // the 16-row side, query rows on the 8-column side, so that a thread sums its keys' weights by itself); a 128-row
 // tcgen05 tile would be empty.
-// 256 sequences of up to 4K bf16 keys, 8 heads of 128 dimensions: 2.2 GB in 393 us (5.6 TB/s) and the scores in 48.
-// (Sums over whole CTAs with barriers between items took 146 us for that second launch.) 64 ragged sequences: 32 us,
-// a chain of dependent reads per launch: lengths, page entries, keys, records. One sequence of 4K keys: 13 us.
+// 256 sequences of up to 8K bf16 keys, 8 heads of 128 dimensions: 2.2 GB in 391 us (5.6 TB/s) and the scores in 48.
+// (Sums over whole CTAs with barriers between items took 146 us for that second launch.) 64 ragged sequences: 32 us
+// (39 from cold caches), a chain of dependent reads per launch: lengths, page entries, keys, records. One sequence of 4K
+// keys: 13 us.
 
 #include <cuda_runtime.h>
 #include <math.h>
